@@ -354,6 +354,121 @@ GEMM_API int gemm_f16f32_ws(int64_t M, int64_t N, int64_t K,
                             void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
+ * Products with an operand held in fewer bits: weights in 4 bits for serving,
+ * saved activations in 8 bits for the backward pass. The codes are small
+ * integers, exact in bf16 and fp16, and their scales are applied to fp32 sums,
+ * so both products are those of the stored values, (q - z) * s or q * s, with
+ * fp32 accumulation: only the order of the sums differs from the definition.
+ * Layout, ownership, streams, degenerate shapes, thread safety and CUDA graphs
+ * are as for the products above (row-major, packed, asynchronous); one matrix
+ * has at most 2^40 elements, and what a call writes must not overlap what it
+ * reads or, for the two-output conversions, its other outputs.
+ *
+ * 4-bit weights (w4). W (K x N) in groups of `group` (32, 64 or 128)
+ * consecutive k of one column; the last group may be shorter. G = ceil(K /
+ * group).
+ *     codes   uint8, N rows of ceil(K / 128) * 64 bytes, 16-byte aligned: row n
+ *             holds column n of W, 64 bytes for each 128 k. In such a block the
+ *             32-bit little-endian word w of the 16-byte quarter c holds
+ *             k = 32 w + 8 c + i, i = 0..7, code i in bits 4 (i / 2) + 16 (i mod
+ *             2) and up. Codes of k >= K may be anything.
+ *     scales  bf16 (or fp16) bits, G x N, the type of the other operand
+ *     zeros   uint8, G x N, values 0..15; null stands for 8 everywhere
+ *     W[k][n] = (q[k][n] - zeros[k / group][n]) * scales[k / group][n]
+ *
+ * gemm_w4_codes_bytes — bytes of `codes`, or GEMM_ERR_INVALID_ARG.
+ *
+ * gemm_bf16_w4_quantize / gemm_f16_w4_quantize — codes, scales and (zeros not
+ * null) zero points of a 2-byte W. With hi = max(0, max w) and lo = min(0, min
+ * w) over a group: s = (hi - lo) * (1/15) rounded to W's type, z = rint(-lo *
+ * (1/s)) clamped to 0..15; without zero points s = max|w| * (1/7) rounded, z =
+ * 8. q = clamp(rint(w * (1/s)) + z, 0, 15), every step in fp32, halves to even.
+ * A scale that rounds below 2^-126 is 0, with q = z (0 with zero points, 8
+ * without). A group with a weight that is not finite gets a NaN scale.
+ *
+ * gemm_bf16_w4_dequantize / gemm_f16_w4_dequantize — W back, (q - z) * s in
+ * fp32 rounded once to its type.
+ *
+ * gemm_w4_pack — codes of weights quantised elsewhere: `q` is K x N, one code a
+ * byte (its low four bits); writes the layout above.
+ */
+GEMM_API int64_t gemm_w4_codes_bytes(int64_t K, int64_t N);
+GEMM_API int gemm_bf16_w4_quantize(int64_t K, int64_t N, int group, const uint16_t *W,
+                                   uint8_t *codes, uint16_t *scales, uint8_t *zeros, void *stream);
+GEMM_API int gemm_f16_w4_quantize(int64_t K, int64_t N, int group, const uint16_t *W,
+                                  uint8_t *codes, uint16_t *scales, uint8_t *zeros, void *stream);
+GEMM_API int gemm_w4_pack(int64_t K, int64_t N, const uint8_t *q, uint8_t *codes, void *stream);
+GEMM_API int gemm_bf16_w4_dequantize(int64_t K, int64_t N, int group, const uint8_t *codes,
+                                     const uint16_t *scales, const uint8_t *zeros, uint16_t *W,
+                                     void *stream);
+GEMM_API int gemm_f16_w4_dequantize(int64_t K, int64_t N, int group, const uint8_t *codes,
+                                    const uint16_t *scales, const uint8_t *zeros, uint16_t *W,
+                                    void *stream);
+
+/*
+ * gemm_bf16w4f32 / gemm_f16w4f32 — C = A.W (M x N, fp32) with A (M x K) bf16 or
+ * fp16 and W in 4 bits:
+ *     C[i][j] = sum_g scales[g][j] * sum_{k in g} A[i][k] * (q[k][j] - zeros[g][j])
+ * Any M (1: a single token), N and K, A and scales 2-byte, codes 16-byte, C
+ * 4-byte aligned. `workspace` may be null; gemm_w4_workspace_bytes says how
+ * many bytes (16-byte aligned, overlapping nothing) the call can use, whatever
+ * the pointers. The contents of the workspace on return are unspecified; two
+ * calls in flight must not share one.
+ */
+GEMM_API int64_t gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+GEMM_API int gemm_bf16w4f32(int64_t M, int64_t N, int64_t K, const uint16_t *A,
+                            const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
+                            int group, float *C, void *workspace, int64_t workspace_bytes,
+                            void *stream);
+GEMM_API int gemm_f16w4f32(int64_t M, int64_t N, int64_t K, const uint16_t *A,
+                           const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
+                           int group, float *C, void *workspace, int64_t workspace_bytes,
+                           void *stream);
+
+/*
+ * 8-bit saved activations (q8). X (M x K: tokens x channels) in columns of 128
+ * rows; the last block of rows may be shorter. B = ceil(M / 128).
+ *     codes   int8, M rows of ceil16(K) bytes, 16-byte aligned; the bytes past K
+ *             are written as 0 and may be anything in what is read
+ *     scales  fp32, B x K
+ *     X[m][k] = codes[m][k] * scales[m / 128][k]
+ * A scale for each channel keeps the few channels of large magnitude that
+ * activations have from coarsening the others.
+ *
+ * gemm_q8_codes_bytes — bytes of `codes`, or GEMM_ERR_INVALID_ARG.
+ *
+ * gemm_bf16_q8_quantize / gemm_f16_q8_quantize — s = max|x| * (1/127) over a
+ * column's block, codes = rint(x * (1/s)), in fp32, halves to even. A block
+ * whose largest magnitude is below 2^-100 is saved as zeros with scale 0, one
+ * with a value that is not finite as zeros with a NaN scale (it reads back, and
+ * enters a gradient, as NaN).
+ *
+ * gemm_bf16_q8_dequantize / gemm_f16_q8_dequantize — X back, rounded once.
+ *
+ * gemm_q8tbf16f32 / gemm_q8tf16f32 — the weight gradient of Y = X.W from the
+ * saved X: dW = X^T.dY (K x N, fp32), dY (M x N) bf16 or fp16,
+ *     dW[k][j] = sum_b scales[b][k] * sum_{m in b} codes[m][k] * dY[m][j]
+ * Any M, N, K; codes 16-byte, scales and dW 4-byte, dY 2-byte aligned.
+ * gemm_q8t_workspace_bytes and `workspace` as for gemm_bf16w4f32.
+ */
+GEMM_API int64_t gemm_q8_codes_bytes(int64_t M, int64_t K);
+GEMM_API int gemm_bf16_q8_quantize(int64_t M, int64_t K, const uint16_t *X, int8_t *codes,
+                                   float *scales, void *stream);
+GEMM_API int gemm_f16_q8_quantize(int64_t M, int64_t K, const uint16_t *X, int8_t *codes,
+                                  float *scales, void *stream);
+GEMM_API int gemm_bf16_q8_dequantize(int64_t M, int64_t K, const int8_t *codes,
+                                     const float *scales, uint16_t *X, void *stream);
+GEMM_API int gemm_f16_q8_dequantize(int64_t M, int64_t K, const int8_t *codes,
+                                    const float *scales, uint16_t *X, void *stream);
+GEMM_API int64_t gemm_q8t_workspace_bytes(int64_t M, int64_t N, int64_t K);
+GEMM_API int gemm_q8tbf16f32(int64_t M, int64_t N, int64_t K, const int8_t *codes,
+                             const float *scales, const uint16_t *dY, float *dW, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+GEMM_API int gemm_q8tf16f32(int64_t M, int64_t N, int64_t K, const int8_t *codes,
+                            const float *scales, const uint16_t *dY, float *dW, void *workspace,
+                            int64_t workspace_bytes, void *stream);
+
+/*
  * gemm_get_device_error — synchronises `stream`, then returns and clears the
  * current device's error word: GEMM_OK, or GEMM_ERR_TIMEOUT if a bounded wait
  * in any kernel of this library on this device gave up since the last call.

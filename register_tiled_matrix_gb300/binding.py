@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import List, Optional, Tuple
+from typing import Callable, List, Optional, Tuple
 
 import torch
 
@@ -74,6 +74,23 @@ def load_library() -> ctypes.CDLL:
         lib.gemm_bf16f32_selftest_timeout.restype = ctypes.c_int
         lib.gemm_f32_selftest_timeout.argtypes = [i64, i64, i64, p, p, p, i64, p]
         lib.gemm_f32_selftest_timeout.restype = ctypes.c_int
+        c_int = ctypes.c_int
+        for name, args in (("gemm_w4_codes_bytes", [i64, i64]), ("gemm_q8_codes_bytes", [i64, i64]),
+                           ("gemm_w4_workspace_bytes", [i64, i64, i64]),
+                           ("gemm_q8t_workspace_bytes", [i64, i64, i64])):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, i64
+        lib.gemm_w4_pack.argtypes = [i64, i64, p, p, p]
+        lib.gemm_w4_pack.restype = c_int
+        for t in ("bf16", "f16"):
+            for name, args in ((f"gemm_{t}_w4_quantize", [i64, i64, c_int, p, p, p, p, p]),
+                               (f"gemm_{t}_w4_dequantize", [i64, i64, c_int, p, p, p, p, p]),
+                               (f"gemm_{t}_q8_quantize", [i64, i64, p, p, p, p]),
+                               (f"gemm_{t}_q8_dequantize", [i64, i64, p, p, p, p]),
+                               (f"gemm_{t}w4f32", [i64] * 3 + [p] * 4 + [c_int, p, p, i64, p]),
+                               (f"gemm_q8t{t}f32", [i64] * 3 + [p] * 5 + [i64, p])):
+                f = getattr(lib, name)
+                f.argtypes, f.restype = args, c_int
         lib.gemm_fp32_pipe_peak.argtypes = [i64, ctypes.c_int, p, ctypes.POINTER(ctypes.c_double),
                                             p]
         lib.gemm_fp32_pipe_peak.restype = ctypes.c_int
@@ -309,6 +326,258 @@ def gemm_f16f32_ws(A: torch.Tensor, B: torch.Tensor, out: Optional[torch.Tensor]
                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """gemm_f16f32 with the workspace rule of gemm_bf16f32_ws."""
     return _gemm_2byte_ws("gemm_f16f32_ws", A, B, torch.float16, out, workspace, stream)
+
+
+# ---------------------------------------------------------------- low-bit operands
+
+W4_BLOCK = 128  # k per 64-byte block of packed 4-bit codes
+W4_GROUPS = (32, 64, 128)
+Q8_ROWS = 128   # rows sharing a scale
+_TYPE_NAMES = {torch.bfloat16: "bf16", torch.float16: "f16"}
+
+
+def _type_name(dtype: torch.dtype) -> str:
+    try:
+        return _TYPE_NAMES[dtype]
+    except KeyError:
+        raise ValueError(f"the type must be torch.bfloat16 or torch.float16, got {dtype}") from None
+
+
+def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device=None) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {' x '.join(map(str, shape))} tensor, "
+                         f"got {' x '.join(map(str, t.shape))}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _matrix(name: str, t: torch.Tensor) -> Tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D (row-major) matrix")
+    return t.shape
+
+
+def _empty(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory of the stream the call runs on, so that it is reused in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _w4_check(codes, scales, zeros, K: int, group: int, device) -> int:
+    """Checks the three parts of a 4-bit weight with K rows; returns its columns."""
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    N = _matrix("codes", codes)[0]
+    _need("codes", codes, torch.uint8, (N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), device)
+    meta = ((K + group - 1) // group, N)
+    _type_name(scales.dtype)
+    _need("scales", scales, scales.dtype, meta, device)
+    if zeros is not None:
+        _need("zeros", zeros, torch.uint8, meta, device)
+    return N
+
+
+def gemm_w4_quantize(W: torch.Tensor, group: int = 128, zeros: bool = True,
+                     stream: Optional[torch.cuda.Stream] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """(codes, scales, zero points) of a bf16 or fp16 K x N weight in 4 bits, `group`
+    (32, 64 or 128) consecutive k of a column to a scale; zeros=False: symmetric
+    codes around 8 and None for the zero points. Layout: include/gemm.h."""
+    K, N = _matrix("W", W)
+    name = _type_name(W.dtype)
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    with _on_device(W):
+        codes = _empty((N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), torch.uint8, W.device, stream)
+        meta = ((K + group - 1) // group, N)
+        scales = _empty(meta, W.dtype, W.device, stream)
+        zp = _empty(meta, torch.uint8, W.device, stream) if zeros else None
+        _check(getattr(_library(), f"gemm_{name}_w4_quantize")(
+            K, N, group, W.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+            zp.data_ptr() if zeros else 0, _stream_handle(stream, W.get_device())))
+    return codes, scales, zp
+
+
+def gemm_w4_pack(q: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Packed codes of a K x N uint8 tensor of 4-bit codes, one a byte (weights
+    quantised elsewhere)."""
+    K, N = _matrix("q", q)
+    _need("q", q, torch.uint8, (K, N))
+    with _on_device(q):
+        codes = _empty((N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), torch.uint8, q.device, stream)
+        _check(_library().gemm_w4_pack(K, N, q.data_ptr(), codes.data_ptr(),
+                                       _stream_handle(stream, q.get_device())))
+    return codes
+
+
+def gemm_w4_dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor],
+                       K: int, group: int = 128, out: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The K x N weight (q - z) * s in the scales' type."""
+    N = _w4_check(codes, scales, zeros, K, group, scales.device)
+    with _on_device(codes):
+        if out is None:
+            out = _empty((K, N), scales.dtype, codes.device, stream)
+        else:
+            _need("out", out, scales.dtype, (K, N), codes.device)
+        _check(getattr(_library(), f"gemm_{_type_name(scales.dtype)}_w4_dequantize")(
+            K, N, group, codes.data_ptr(), scales.data_ptr(),
+            0 if zeros is None else zeros.data_ptr(), out.data_ptr(),
+            _stream_handle(stream, codes.get_device())))
+    return out
+
+
+def _workspace(workspace: Optional[torch.Tensor], rows16: bool, nbytes: Callable[..., int], size,
+               device, stream) -> Tuple[int, int, Optional[torch.Tensor]]:
+    """(pointer, bytes, tensor) of the caller's workspace, or of one made for this call
+    when the 2-byte operand's rows are off 16-byte boundaries."""
+    if workspace is None:
+        need = 0 if rows16 else int(nbytes(*size))
+        if need <= 0:
+            return 0, 0, None
+        workspace = _empty((need,), torch.uint8, device, stream)
+    elif (not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _w4_product(entry: str, dtype: torch.dtype, A, codes, scales, zeros, group, out, workspace,
+                stream) -> torch.Tensor:
+    M, K = _matrix("A", A)
+    device = A.device
+    _need("A", A, dtype, (M, K))
+    _need("scales", scales, dtype, scales.shape, device)
+    N = _w4_check(codes, scales, zeros, K, group, device)
+    with _on_device(A):
+        lib = _library()
+        if out is None:
+            out = _empty((M, N), torch.float32, device, stream)
+        else:
+            _need("out", out, torch.float32, (M, N), device)
+        ptr, nbytes, workspace = _workspace(workspace, _rows_on_16_bytes(A),
+                                            lib.gemm_w4_workspace_bytes, (M, N, K), device, stream)
+        _check(getattr(lib, entry)(M, N, K, A.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                   0 if zeros is None else zeros.data_ptr(), group, out.data_ptr(),
+                                   ptr, nbytes, _stream_handle(stream, A.get_device())))
+    return out
+
+
+def gemm_bf16w4f32(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                   zeros: Optional[torch.Tensor] = None, group: int = 128,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """C = A @ W (fp32) with bf16 A (M x K) and W (K x N) in 4 bits, as gemm_w4_quantize
+    gives it. `workspace` (a CUDA tensor of gemm_w4_workspace_bytes(M, N, K) bytes)
+    is allocated for this call when None and the call can use one."""
+    return _w4_product("gemm_bf16w4f32", torch.bfloat16, A, codes, scales, zeros, group, out,
+                       workspace, stream)
+
+
+def gemm_f16w4f32(A: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                  zeros: Optional[torch.Tensor] = None, group: int = 128,
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """gemm_bf16w4f32 for fp16 A and scales."""
+    return _w4_product("gemm_f16w4f32", torch.float16, A, codes, scales, zeros, group, out,
+                       workspace, stream)
+
+
+def gemm_w4_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Largest workspace gemm_bf16w4f32 / gemm_f16w4f32 can use for this shape (0: none)."""
+    n = int(load_library().gemm_w4_workspace_bytes(int(M), int(N), int(K)))
+    _check(n if n < 0 else 0)
+    return n
+
+
+def gemm_q8_quantize(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(codes, scales): a bf16 or fp16 M x K activation saved in 8 bits, one scale
+    for each column of 128 rows. codes: int8, M x ceil16(K); scales: fp32."""
+    M, K = _matrix("X", X)
+    name = _type_name(X.dtype)
+    with _on_device(X):
+        codes = _empty((M, (K + 15) // 16 * 16), torch.int8, X.device, stream)
+        scales = _empty(((M + Q8_ROWS - 1) // Q8_ROWS, K), torch.float32, X.device, stream)
+        _check(getattr(_library(), f"gemm_{name}_q8_quantize")(
+            M, K, X.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+            _stream_handle(stream, X.get_device())))
+    return codes, scales
+
+
+def _q8_check(codes, scales, M: int, K: int, device) -> None:
+    _need("codes", codes, torch.int8, (M, (K + 15) // 16 * 16), device)
+    _need("scales", scales, torch.float32, ((M + Q8_ROWS - 1) // Q8_ROWS, K), device)
+
+
+def gemm_q8_dequantize(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int,
+                       dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The saved M x K activation, codes * scales, in `dtype` (bf16 or fp16)."""
+    name = _type_name(dtype)
+    _q8_check(codes, scales, M, K, scales.device)
+    with _on_device(codes):
+        if out is None:
+            out = _empty((M, K), dtype, codes.device, stream)
+        else:
+            _need("out", out, dtype, (M, K), codes.device)
+        _check(getattr(_library(), f"gemm_{name}_q8_dequantize")(
+            M, K, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+            _stream_handle(stream, codes.get_device())))
+    return out
+
+
+def _q8t_product(entry: str, dtype: torch.dtype, codes, scales, dY, out, workspace,
+                 stream) -> torch.Tensor:
+    M, N = _matrix("dY", dY)
+    K = _matrix("scales", scales)[1]
+    device = dY.device
+    _need("dY", dY, dtype, (M, N))
+    _q8_check(codes, scales, M, K, device)
+    with _on_device(dY):
+        lib = _library()
+        if out is None:
+            out = _empty((K, N), torch.float32, device, stream)
+        else:
+            _need("out", out, torch.float32, (K, N), device)
+        ptr, nbytes, workspace = _workspace(workspace, _rows_on_16_bytes(dY),
+                                            lib.gemm_q8t_workspace_bytes, (M, N, K), device, stream)
+        _check(getattr(lib, entry)(M, N, K, codes.data_ptr(), scales.data_ptr(), dY.data_ptr(),
+                                   out.data_ptr(), ptr, nbytes,
+                                   _stream_handle(stream, dY.get_device())))
+    return out
+
+
+def gemm_q8tbf16f32(codes: torch.Tensor, scales: torch.Tensor, dY: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """dW = X^T @ dY (K x N, fp32): the weight gradient of Y = X @ W from X as
+    gemm_q8_quantize saved it and a bf16 dY (M x N). `workspace` (a CUDA tensor of
+    gemm_q8t_workspace_bytes(M, N, K) bytes) is allocated for this call when None
+    and the call can use one."""
+    return _q8t_product("gemm_q8tbf16f32", torch.bfloat16, codes, scales, dY, out, workspace,
+                        stream)
+
+
+def gemm_q8tf16f32(codes: torch.Tensor, scales: torch.Tensor, dY: torch.Tensor,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """gemm_q8tbf16f32 for fp16 dY."""
+    return _q8t_product("gemm_q8tf16f32", torch.float16, codes, scales, dY, out, workspace, stream)
+
+
+def gemm_q8t_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Largest workspace gemm_q8tbf16f32 / gemm_q8tf16f32 can use for this shape (0: none)."""
+    n = int(load_library().gemm_q8t_workspace_bytes(int(M), int(N), int(K)))
+    _check(n if n < 0 else 0)
+    return n
 
 
 def gemm_bf16f32_selftest_timeout(A: torch.Tensor, B: torch.Tensor, out: torch.Tensor,

@@ -13,6 +13,7 @@
 
 #include "gemm.h"
 #include "kernels.h"
+#include "lowbit.h"
 #include "ptx.cuh"
 
 namespace {
@@ -355,6 +356,17 @@ int run_bf16(int64_t M, int64_t N, int64_t K, const uint16_t *A, const uint16_t 
 } // namespace
 
 namespace rtm {
+int device_context(DeviceContext *out)
+{
+    DeviceInfo d;
+    const int st = current_device(&d);
+    out->sms = d.sms;
+    out->err = d.err;
+    out->encode_tiled = st == GEMM_OK ? encode_tiled_fn() : nullptr;
+    out->wait_limit_ns = kDefaultWaitLimitNs;
+    return st;
+}
+
 int check_f32_args(int64_t M, int64_t N, int64_t K, const float *A, const float *B, const float *C,
                    bool *nothing_to_do)
 {
