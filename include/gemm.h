@@ -373,7 +373,8 @@ GEMM_API int gemm_f16f32_ws(int64_t M, int64_t N, int64_t K,
  *             k = 32 w + 8 c + i, i = 0..7, code i in bits 4 (i / 2) + 16 (i mod
  *             2) and up. Codes of k >= K may be anything.
  *     scales  bf16 (or fp16) bits, G x N, the type of the other operand
- *     zeros   uint8, G x N, values 0..15; null stands for 8 everywhere
+ *     zeros   uint8, G x N, values 0..15 (the low four bits are read); null
+ *             stands for 8 everywhere
  *     W[k][n] = (q[k][n] - zeros[k / group][n]) * scales[k / group][n]
  *
  * gemm_w4_codes_bytes — bytes of `codes`, or GEMM_ERR_INVALID_ARG.

@@ -59,7 +59,14 @@ struct Q8tLaunch {
     const uint16_t *dY;
     float *C;
 };
-// lowbit_simt.cu
+// lowbit_tc.cu: the tensor cores. lda, ldy: row stride of A, dY in elements, rows
+// on 16-byte boundaries. mute: the failure-detection self-test (no loads are
+// issued, every wait runs out, C is left unspecified).
+cudaError_t launch_w4_tc(const W4Launch &L, int64_t lda, const DeviceContext &d, bool mute,
+                         cudaStream_t stream);
+cudaError_t launch_q8t_tc(const Q8tLaunch &L, int64_t ldy, const DeviceContext &d, bool mute,
+                          cudaStream_t stream);
+// lowbit_simt.cu: any alignment.
 cudaError_t launch_w4_simt(const W4Launch &L, cudaStream_t stream);
 cudaError_t launch_q8t_simt(const Q8tLaunch &L, cudaStream_t stream);
 

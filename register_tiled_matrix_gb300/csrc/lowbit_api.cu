@@ -52,6 +52,14 @@ int finish(cudaError_t e)
     return GEMM_OK;
 }
 
+bool rows16(const void *p, int64_t cols) { return cols % 8 == 0 && !misaligned(p, 16); }
+
+// Bytes of a copy of a rows x cols 2-byte matrix with its rows padded to 16 bytes.
+int64_t padded_bytes(int64_t rows, int64_t cols)
+{
+    return (rows * ((cols + 7) / 8 * 8) * 2 + 255) / 256 * 256;
+}
+
 int64_t groups(int64_t K, int group) { return (K + group - 1) / group; }
 
 // The checks and the launch of both quantise entries' outputs.
@@ -169,7 +177,8 @@ int w4_product(int64_t M, int64_t N, int64_t K, int f16, const uint16_t *A, cons
                          {codes, N * rtm::w4_row_bytes(K)},
                          {scales, meta * 2},
                          {zeros, meta}};
-    if (K > 0 && overlaps({C, M * N * 4}, in, 4))
+    const Range out = {C, M * N * 4};
+    if (K > 0 && overlaps(out, in, 4))
         return GEMM_ERR_INVALID_ARG;
     if (misaligned(C, 4) ||
         (K > 0 && (misaligned(A, 2) || misaligned(codes, 16) || misaligned(scales, 2))))
@@ -192,6 +201,20 @@ int w4_product(int64_t M, int64_t N, int64_t K, int f16, const uint16_t *A, cons
     L.scales = scales;
     L.zeros = zeros;
     L.C = C;
+    if (d.encode_tiled && rows16(A, K))
+        return finish(rtm::launch_w4_tc(L, K, d, false, s));
+    const int64_t need = padded_bytes(M, K);
+    if (d.encode_tiled && workspace && !misaligned(workspace, 16) && workspace_bytes >= need) {
+        if (overlaps({workspace, need}, in, 4) || overlaps({workspace, need}, &out, 1))
+            return GEMM_ERR_INVALID_ARG;
+        const int64_t lda = (K + 7) / 8 * 8;
+        uint16_t *copy = static_cast<uint16_t *>(workspace);
+        const cudaError_t e = rtm::launch_pack_rows_2b(A, M, K, copy, lda, d.sms, s);
+        if (e != cudaSuccess)
+            return finish(e);
+        L.A = copy;
+        return finish(rtm::launch_w4_tc(L, lda, d, false, s));
+    }
     return finish(rtm::launch_w4_simt(L, s));
 }
 
@@ -209,7 +232,8 @@ int q8t_product(int64_t M, int64_t N, int64_t K, int f16, const int8_t *codes, c
     const Range in[3] = {{codes, M * rtm::q8_pitch(K)},
                          {scales, groups(M, rtm::kQ8Rows) * K * 4},
                          {dY, M * N * 2}};
-    if (M > 0 && overlaps({C, K * N * 4}, in, 3))
+    const Range out = {C, K * N * 4};
+    if (M > 0 && overlaps(out, in, 3))
         return GEMM_ERR_INVALID_ARG;
     if (misaligned(C, 4) ||
         (M > 0 && (misaligned(codes, 16) || misaligned(scales, 4) || misaligned(dY, 2))))
@@ -230,6 +254,20 @@ int q8t_product(int64_t M, int64_t N, int64_t K, int f16, const int8_t *codes, c
     L.scales = scales;
     L.dY = dY;
     L.C = C;
+    if (d.encode_tiled && rows16(dY, N))
+        return finish(rtm::launch_q8t_tc(L, N, d, false, s));
+    const int64_t need = padded_bytes(M, N);
+    if (d.encode_tiled && workspace && !misaligned(workspace, 16) && workspace_bytes >= need) {
+        if (overlaps({workspace, need}, in, 3) || overlaps({workspace, need}, &out, 1))
+            return GEMM_ERR_INVALID_ARG;
+        const int64_t ldy = (N + 7) / 8 * 8;
+        uint16_t *copy = static_cast<uint16_t *>(workspace);
+        const cudaError_t e = rtm::launch_pack_rows_2b(dY, M, N, copy, ldy, d.sms, s);
+        if (e != cudaSuccess)
+            return finish(e);
+        L.dY = copy;
+        return finish(rtm::launch_q8t_tc(L, ldy, d, false, s));
+    }
     return finish(rtm::launch_q8t_simt(L, s));
 }
 
@@ -306,14 +344,14 @@ int64_t gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (!size_ok(M, K) || !size_ok(K, N) || !size_ok(M, N))
         return GEMM_ERR_INVALID_ARG;
-    return 0;
+    return N > 0 ? padded_bytes(M, K) : 0;
 }
 
 int64_t gemm_q8t_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (!size_ok(M, K) || !size_ok(K, N) || !size_ok(M, N))
         return GEMM_ERR_INVALID_ARG;
-    return 0;
+    return K > 0 ? padded_bytes(M, N) : 0;
 }
 
 int64_t gemm_q8_codes_bytes(int64_t M, int64_t K)

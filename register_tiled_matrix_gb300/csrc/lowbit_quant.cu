@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads)
                 if (k < K) {
                     s = to_f32<F16>(__ldg(scales + k / GROUP * N + n));
                     if (zeros)
-                        z = (float)__ldg(zeros + k / GROUP * N + n);
+                        z = (float)(__ldg(zeros + k / GROUP * N + n) & 15);
                 }
             }
 #pragma unroll

@@ -28,7 +28,7 @@ struct W4Operands {
         const uint32_t word = *reinterpret_cast<const uint32_t *>(
             p.codes + n * w4_row_bytes(p.K) + (unsigned)k / kW4Block * kW4BlockBytes + c * 16 + w * 4);
         const int64_t g = (int64_t)((unsigned)k / (unsigned)p.group) * p.N + n;
-        const float z = p.zeros ? (float)p.zeros[g] : 8.f;
+        const float z = p.zeros ? (float)(p.zeros[g] & 15) : 8.f;
         return ((float)((word >> w4_shift((int)i)) & 15u) - z) * to_f32<F16>(p.scales[g]);
     }
 };

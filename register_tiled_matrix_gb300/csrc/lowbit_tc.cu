@@ -1,0 +1,927 @@
+// Products with a low-bit operand on the sm_103a tensor cores (tcgen05):
+//
+//     w4:  C^T[n][m]  = sum_g s[g][n] * sum_{k in g} (q[k][n] - z[g][n]) * A[m][k]
+//     q8t: dW[k][j]   = sum_b s[b][k] * sum_{m in b} q[m][k] * dY[m][j]
+//
+// Both are sums over a "depth" (k or m) of a low-bit operand, which owns the
+// 128 lanes of the accumulator (n or k), times a 2-byte operand, which owns its
+// columns (m or j). The scale is constant over a run of the depth (a group) and
+// belongs to one lane, so nothing is rounded that the definition does not
+// round: the codes minus their zero point are integers of at most 8 bits, exact
+// in bf16 and fp16, the tensor core sums their products with the 2-byte values
+// of one group in fp32, and the scale multiplies that sum when it is added to
+// the running fp32 total. Applied to the codes instead, the scale would cost a
+// rounding to 8 or 11 bits of every weight.
+//
+// One CTA computes 128 lanes x NT columns (NT = 32 .. 256) and its roles are
+//  * a raw producer thread: TMA of the packed codes into a ring (8 KB slots);
+//  * DW dequantising warpgroups: codes -> integers in bf16/fp16, written to the
+//    128-byte-swizzled stage the MMA reads (a w4 thread owns a lane and reads
+//    its 64-byte block, a q8 thread 16 channels of a row; neither store nor
+//    load meets a bank conflict);
+//  * a producer thread: TMA of the 2-byte operand into the same stages, 64 deep;
+//  * an MMA thread: one accumulation set in tensor memory per group, SETS sets
+//    in turn, so the next group is multiplied while the last one is read;
+//  * PW promoting warpgroups: read a set (a lane a thread), multiply it by the
+//    lane's scale, add it to fp32 totals in registers, and at the end of the
+//    tile store them.
+// Scales and zero points are 4-byte asynchronous copies that each thread makes
+// for itself many groups ahead. Registers move between the warpgroups: 56 for
+// the issuing threads, 88 for the dequantising, 184 for the promoting ones,
+// which keep up to 128 totals.
+//
+// With few tiles the depth is split over S CTAs of a cluster; their totals meet
+// in shared memory and are added in rank order through distributed shared
+// memory, so results repeat exactly. Without a split the CTAs are persistent,
+// and the stores of one tile overlap the multiplications of the next.
+//
+// Every wait is bounded: a thread that gives up records GEMM_ERR_TIMEOUT in the
+// device error word, and all threads still reach the barriers at the end.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <type_traits>
+
+#include "kernels.h"
+#include "lowbit.h"
+#include "lowbit_types.cuh"
+#include "ptx.cuh"
+
+namespace rtm {
+namespace lbt {
+
+constexpr int LANES = 128;
+constexpr int BK = 64;        // depth of a stage: 64 2-byte values = a 128-byte swizzle row
+constexpr int BLOCK = 128;    // depth of a raw w4 slot, and the granularity of a split
+constexpr int UMMA_K = 16;
+constexpr int kThreads = 512;
+constexpr uint32_t A_BYTES = LANES * BK * 2;   // 16 KB
+constexpr uint32_t ATOM_BYTES = 64 * BK * 2;   // 8 KB: 64 columns x 64 depth, MN-major
+constexpr uint32_t RAW_BYTES = 8192;           // w4: 128 lanes x 64 B; q8: 64 rows x 128 B
+constexpr int SCALE_SLOTS = 16;
+constexpr int SCALE_AHEAD = 14;                // groups a promoting thread copies ahead: a slot
+                                               // is written two groups after its last use
+constexpr int ZERO_SLOTS = 4;                  // blocks a dequantising thread copies ahead
+
+enum Mode { kW4, kQ8t };
+
+template <int NT>
+struct Cfg {
+    static constexpr int DW = NT == 256 ? 1 : 2;  // dequantising warpgroups
+    static constexpr int PW = 3 - DW;             // promoting warpgroups
+    // Registers a thread after the split: the four warpgroups share what the block
+    // was launched with, 4 x 128.
+    static constexpr int R_ISSUE = 56, R_DEQUANT = 88, R_PROMOTE = 184;
+    static_assert(R_ISSUE + DW * R_DEQUANT + PW * R_PROMOTE <= 512, "register split");
+    static constexpr int CPT = NT / PW;           // columns of a promoting thread
+    static constexpr int SETS = NT == 256 ? 2 : 4;
+    static constexpr uint32_t TMEM_COLS = SETS * NT;
+    static constexpr uint32_t B_BYTES = NT * BK * 2;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = NT == 256 ? 3 : 4;
+    static constexpr int RAW = NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 10 : 12;
+    static constexpr uint32_t OFF_RAW = STAGES * STAGE_BYTES;
+    static constexpr uint32_t OFF_SCALE = OFF_RAW + RAW * RAW_BYTES;
+    static constexpr uint32_t OFF_ZERO = OFF_SCALE + PW * SCALE_SLOTS * LANES * 4;
+    static constexpr uint32_t OFF_BARS = OFF_ZERO + DW * ZERO_SLOTS * 4 * LANES * 4;
+    static constexpr size_t SMEM_BYTES = OFF_BARS + 512 + 1024 /*align*/;
+    static constexpr int PITCH = NT + 4;  // floats per lane of a partial tile
+    static_assert(LANES * PITCH * 4 <= OFF_RAW, "a partial tile fits the stages");
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+struct Params {
+    int lanes, cols, depth;  // w4: N, M, K; q8t: K, N, M
+    int group;               // depth of a group: 32, 64 or 128
+    const void *scales;      // w4: 2-byte, q8t: fp32; [group][lane]
+    const uint8_t *zeros;    // w4: [group][lane], or null
+    float *C;
+    int *err;
+    unsigned long long limit_ns;
+    int splits;  // CTAs of a cluster, each summing a range of the depth
+    int tiles;
+    int mute;    // failure-detection self-test: issue no loads
+    int c_vec;   // q8t: rows of dW on 16-byte boundaries
+};
+
+// kind::f16, D fp32, M = 128, N = NT; w4: both operands K-major, q8t: both MN-major.
+template <Mode MODE, bool F16, int NT>
+__host__ __device__ constexpr uint32_t idesc()
+{
+    constexpr uint32_t mn = MODE == kQ8t ? 1u : 0u, t = F16 ? 0u : 1u;
+    return (1u << 4) | (t << 7) | (t << 10) | (mn << 15) | (mn << 16) |
+           ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(LANES >> 4) << 24);
+}
+
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void give_up(int *err, volatile int *abort)
+{
+    atomicCAS(err, 0, kDevErrTimeout);
+    *abort = 1;
+}
+
+template <int R>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// Each thread of the warp reads its TMEM lane, 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, float (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]),
+          "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// acc += s * v, two at a time.
+__device__ __forceinline__ void fma2(float &a0, float &a1, float s, float v0, float v1)
+{
+    asm("{\n\t.reg .b64 a, v, s;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 v, {%2, %3};\n\t"
+        "mov.b64 s, {%4, %4};\n\t"
+        "fma.rn.f32x2 a, v, s, a;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}\n"
+        : "+f"(a0), "+f"(a1)
+        : "f"(v0), "f"(v1), "f"(s));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    if constexpr (F16)
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// 2^7 in bf16 and 2^10 in fp16 have ulp 1: a small integer in the low mantissa
+// bits adds itself, exactly.
+template <bool F16>
+__device__ __forceinline__ constexpr uint32_t magic2()
+{
+    return F16 ? 0x64006400u : 0x43004300u;
+}
+
+// Eight 4-bit codes minus their zero point, in order; zz = magic + z, twice.
+template <bool F16>
+__device__ __forceinline__ uint4 w4_values(uint32_t word, uint32_t zz)
+{
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v[j] = sub2<F16>(((word >> (4 * j)) & 0x000f000fu) | magic2<F16>(), zz);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Four signed bytes, in order. fp16: 1024 + (q + 128) - 1152. bf16 has seven
+// mantissa bits, so the sign bit goes to the subtrahend: with u = q mod 128 and
+// the sign bit on the exponent's lowest bit, (128 + u) - (sign ? 256 : 128).
+template <bool F16>
+__device__ __forceinline__ uint2 q8_values(uint32_t word)
+{
+    if constexpr (F16) {
+        const uint32_t u = word ^ 0x80808080u;
+        return make_uint2(sub2<true>(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u),
+                          sub2<true>(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u));
+    } else {
+        const uint32_t u = word & 0x7f7f7f7fu, s = word & 0x80808080u;
+        return make_uint2(sub2<false>(__byte_perm(u, 0x43434343u, 0x4140),
+                                      __byte_perm(s, 0x43434343u, 0x4140)),
+                          sub2<false>(__byte_perm(u, 0x43434343u, 0x4342),
+                                      __byte_perm(s, 0x43434343u, 0x4342)));
+    }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// Tiles in bands of 16 lane tiles, so that the tiles in flight share both operands in L2.
+__device__ __forceinline__ void tile_origin(int t, int lanes, int cols, int nt, int &l0, int &c0)
+{
+    constexpr int BAND = 16;
+    const int tl = (lanes + LANES - 1) / LANES, tc = (cols + nt - 1) / nt;
+    const int band = t / (BAND * tc), first = band * BAND;
+    const int rows = min(tl - first, BAND), in = t - band * BAND * tc;
+    l0 = (first + in % rows) * LANES;
+    c0 = in / rows * nt;
+}
+
+template <Mode MODE, bool F16, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    lowbit_tc_kernel(const __grid_constant__ CUtensorMap tm_codes,
+                     const __grid_constant__ CUtensorMap tm_b, const Params p)
+{
+    using Cf = Cfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+    uint64_t *raw_full = reinterpret_cast<uint64_t *>(smem + Cf::OFF_BARS);
+    uint64_t *raw_empty = raw_full + Cf::RAW;
+    uint64_t *a_full = raw_empty + Cf::RAW;
+    uint64_t *b_full = a_full + Cf::STAGES;
+    uint64_t *empty = b_full + Cf::STAGES;
+    uint64_t *tfull = empty + Cf::STAGES;
+    uint64_t *tempty = tfull + Cf::SETS;
+    uint64_t *drain = tempty + Cf::SETS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    static_assert((2 * Cf::RAW + 3 * Cf::STAGES + 2 * Cf::SETS + 1) * 8 + 8 <= 512, "barriers");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wg = warp >> 2;
+    const int S = p.splits;
+    const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
+    const int unit = blockIdx.x / S, units = gridDim.x / S;
+
+    // This CTA's depth: whole blocks, the last one possibly ragged.
+    const int blocks = (p.depth + BLOCK - 1) / BLOCK;
+    const int per = (blocks + S - 1) / S;
+    const int block0 = min(blocks, (int)rank * per), block1 = min(blocks, block0 + per);
+    const int d0 = block0 * BLOCK;
+    const int depth = max(0, (block1 == blocks ? p.depth : block1 * BLOCK) - d0);
+    const int nstages = (depth + BK - 1) / BK;
+    const int ngroups = (depth + p.group - 1) / p.group;
+    const int group0 = d0 / p.group;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Cf::RAW; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 4);  // the warps that read the slot
+        }
+        for (int i = 0; i < Cf::STAGES; ++i) {
+            mbar_init(&a_full[i], 4);  // the warps that wrote the stage
+            mbar_init(&b_full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < Cf::SETS; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4 * Cf::PW);
+        }
+        mbar_init(drain, 1);
+        *abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tm_codes);
+        tma_prefetch_desc(&tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Cf::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (wg == 0) {
+        regs_dec<Cf::R_ISSUE>();
+        if (warp == 0 && lane == 0 && !p.mute) {
+            // ------------------------------------------------ codes
+            uint32_t slot = 0, phase = 0, issued = 0, parity = 0;
+            const int steps = MODE == kW4 ? (depth + BLOCK - 1) / BLOCK : nstages;
+            for (int t = unit; t < p.tiles && !*abort; t += units) {
+                int l0, c0;
+                tile_origin(t, p.lanes, p.cols, NT, l0, c0);
+                for (int i = 0; i < steps; ++i) {
+                    if (!mbar_wait_bounded(&raw_empty[slot], phase ^ 1, p.limit_ns, abort)) {
+                        give_up(p.err, abort);
+                        break;
+                    }
+                    const uint32_t dst = smem_u32(smem + Cf::OFF_RAW + slot * RAW_BYTES);
+                    mbar_arrive_expect_tx(&raw_full[slot], RAW_BYTES);
+                    if constexpr (MODE == kW4)
+                        tma_load_2d(dst, &tm_codes, &raw_full[slot], (block0 + i) * kW4BlockBytes, l0);
+                    else
+                        tma_load_2d(dst, &tm_codes, &raw_full[slot], l0, d0 + i * BK);
+                    issued |= 1u << slot;
+                    parity = (parity & ~(1u << slot)) | (phase << slot);
+                    if (++slot == Cf::RAW) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // No copy into this CTA's shared memory may outlive it.
+            volatile int no_abort = 0;
+#pragma unroll 1
+            for (int i = 0; i < Cf::RAW; ++i)
+                if (issued & (1u << i))
+                    mbar_wait_bounded(&raw_full[i], (parity >> i) & 1u, p.limit_ns, &no_abort);
+        } else if (warp == 2 && lane == 0 && !p.mute) {
+            // ------------------------------------------------ 2-byte operand
+            uint32_t stage = 0, phase = 0, issued = 0, parity = 0;
+            for (int t = unit; t < p.tiles && !*abort; t += units) {
+                int l0, c0;
+                tile_origin(t, p.lanes, p.cols, NT, l0, c0);
+                for (int i = 0; i < nstages; ++i) {
+                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                        give_up(p.err, abort);
+                        break;
+                    }
+                    const uint32_t dst = smem_u32(smem + stage * Cf::STAGE_BYTES + A_BYTES);
+                    mbar_arrive_expect_tx(&b_full[stage], Cf::B_BYTES);
+                    if constexpr (MODE == kW4) {
+                        tma_load_2d(dst, &tm_b, &b_full[stage], d0 + i * BK, c0);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < NT / 64; ++j)
+                            tma_load_2d(dst + j * ATOM_BYTES, &tm_b, &b_full[stage], c0 + 64 * j,
+                                        d0 + i * BK);
+                    }
+                    issued |= 1u << stage;
+                    parity = (parity & ~(1u << stage)) | (phase << stage);
+                    if (++stage == Cf::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            volatile int no_abort = 0;
+#pragma unroll 1
+            for (int i = 0; i < Cf::STAGES; ++i)
+                if (issued & (1u << i))
+                    mbar_wait_bounded(&b_full[i], (parity >> i) & 1u, p.limit_ns, &no_abort);
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------ MMA issuer
+            uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
+            bool issued_any = false, ok = true;
+            const int per_group = p.group / UMMA_K;
+            for (int t = unit; t < p.tiles && ok; t += units) {
+                int in_group = 0;
+                for (int i = 0; i < nstages && ok; ++i) {
+                    if (!mbar_wait_bounded(&b_full[stage], phase, p.limit_ns, abort) ||
+                        !mbar_wait_bounded(&a_full[stage], phase, p.limit_ns, abort)) {
+                        give_up(p.err, abort);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * Cf::STAGE_BYTES);
+                    const uint32_t sb = sa + A_BYTES;
+                    const int steps = min(BK / UMMA_K, (depth - i * BK + UMMA_K - 1) / UMMA_K);
+                    for (int kk = 0; kk < steps; ++kk) {
+                        if (in_group == 0) {
+                            if (!mbar_wait_bounded(&tempty[set], set_phase ^ 1, p.limit_ns, abort)) {
+                                give_up(p.err, abort);
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+                        uint64_t adesc, bdesc;
+                        if constexpr (MODE == kW4) {
+                            adesc = sdesc_sw128(sa + kk * UMMA_K * 2, 16, 1024);
+                            bdesc = sdesc_sw128(sb + kk * UMMA_K * 2, 16, 1024);
+                        } else {
+                            adesc = sdesc_sw128(sa + kk * UMMA_K * 128, ATOM_BYTES, 1024);
+                            bdesc = sdesc_sw128(sb + kk * UMMA_K * 128, ATOM_BYTES, 1024);
+                        }
+                        umma_f16(tmem_base + set * NT, adesc, bdesc, idesc<MODE, F16, NT>(),
+                                 in_group != 0 ? 1u : 0u);
+                        issued_any = true;
+                        if (++in_group == per_group || (i == nstages - 1 && kk == steps - 1)) {
+                            umma_commit(&tfull[set]);
+                            in_group = 0;
+                            if (++set == Cf::SETS) {
+                                set = 0;
+                                set_phase ^= 1;
+                            }
+                        }
+                    }
+                    umma_commit(&empty[stage]);
+                    if (++stage == Cf::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (issued_any) {
+                umma_commit(drain);
+                volatile int no_abort = 0;
+                mbar_wait_bounded(drain, 0, p.limit_ns, &no_abort);  // before TMEM is freed
+            }
+        }
+        __syncwarp();
+    } else if (wg <= Cf::DW) {
+        // ------------------------------------------------ dequantise
+        // Warpgroup d takes every DW-th raw slot, in order.
+        regs_dec<Cf::R_DEQUANT>();
+        const int d = wg - 1, tid = threadIdx.x & 127;
+        bool ok = true;
+        if constexpr (MODE == kW4) {
+            const uint32_t zring = smem_u32(smem + Cf::OFF_ZERO) +
+                                   (uint32_t)(d * ZERO_SLOTS * 4 * LANES + tid) * 4u;
+            const int gpb = BLOCK / p.group;  // groups of a block: 1, 2 or 4
+            const int nblocks = block1 - block0;
+            const int gs = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+            const int glast = (p.depth - 1) >> gs;
+            int seq = 0, sbase = 0;  // this CTA's raw slots and stages so far, over all tiles
+            for (int t = unit; t < p.tiles && ok; t += units) {
+                int l0, c0;
+                tile_origin(t, p.lanes, p.cols, NT, l0, c0);
+                const int n = min(l0 + tid, p.lanes - 1);  // lanes past the end: any zero point
+                // The word that holds the zero point of (group, lane).
+                auto fetch = [&](int i, int slot) {
+                    if (p.zeros && i < nblocks)
+                        for (int g = 0; g < gpb; ++g) {
+                            const int gg = group0 + i * gpb + g;
+                            if (gg <= glast) {
+                                const uintptr_t a = reinterpret_cast<uintptr_t>(
+                                    p.zeros + (int64_t)gg * p.lanes + n);
+                                cp_async_4_full(zring + (uint32_t)((slot * 4 + g) * LANES) * 4u,
+                                                reinterpret_cast<const void *>(a & ~uintptr_t(3)));
+                            }
+                        }
+                    cp_async_commit();
+                };
+                const int first = (d - seq % Cf::DW + Cf::DW) % Cf::DW;
+                for (int a = 0; a < ZERO_SLOTS - 1; ++a)
+                    fetch(first + a * Cf::DW, a);
+                int zslot = 0;
+                for (int i = first; i < nblocks; i += Cf::DW) {
+                    const int r = seq + i;  // raw slot number
+                    const uint32_t slot = (uint32_t)(r % Cf::RAW), rphase = (uint32_t)(r / Cf::RAW) & 1u;
+                    fetch(i + (ZERO_SLOTS - 1) * Cf::DW, (zslot + ZERO_SLOTS - 1) % ZERO_SLOTS);
+                    if (!mbar_wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
+                        give_up(p.err, abort);
+                        ok = false;
+                        break;
+                    }
+                    // 64-byte rows, 64-byte swizzle: quarter c of row r at c ^ (r / 2 mod 4).
+                    const uint32_t src =
+                        smem_u32(smem + Cf::OFF_RAW + slot * RAW_BYTES) + (uint32_t)tid * 64u;
+                    uint4 q[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        q[c] = lds128(src + (uint32_t)((c ^ ((tid >> 1) & 3)) << 4));
+                    uint32_t zz[4];
+                    cp_async_wait<ZERO_SLOTS - 1>();
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t z = 8u;
+                        if (p.zeros) {
+                            const int g = (w * 32) >> gs;
+                            const int64_t gg = min(group0 + i * gpb + g, glast);
+                            const uintptr_t a =
+                                reinterpret_cast<uintptr_t>(p.zeros + gg * p.lanes + n);
+                            z = (lds32(zring + (uint32_t)((zslot * 4 + g) * LANES) * 4u) >>
+                                 (8 * (a & 3))) & 15u;
+                        }
+                        zz[w] = magic2<F16>() | z | (z << 16);
+                    }
+                    zslot = (zslot + 1) % ZERO_SLOTS;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (2 * i + h >= nstages)
+                            break;
+                        const int sn = sbase + 2 * i + h;
+                        const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
+                        const uint32_t phase = (uint32_t)(sn / Cf::STAGES) & 1u;
+                        if (!mbar_wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                            give_up(p.err, abort);
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t dst =
+                            smem_u32(smem + stage * Cf::STAGE_BYTES) + (uint32_t)tid * 128u;
+#pragma unroll
+                        for (int w = 0; w < 2; ++w)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint4 &qq = q[c];
+                                const uint32_t word = h == 0 ? (w == 0 ? qq.x : qq.y)
+                                                             : (w == 0 ? qq.z : qq.w);
+                                sts128(dst + (uint32_t)(((4 * w + c) ^ (tid & 7)) << 4),
+                                       w4_values<F16>(word, zz[2 * h + w]));
+                            }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&a_full[stage]);
+                            // The slot is free once its words have been used, not when
+                            // their loads were issued: an arrival between the loads and
+                            // their first use let the next copy overtake them.
+                            if (h == 0)
+                                mbar_arrive(&raw_empty[slot]);
+                        }
+                    }
+                    if (!ok)
+                        break;
+                }
+                seq += nblocks;
+                sbase += nstages;
+                cp_async_wait<0>();
+            }
+        } else {
+            // Thread: 16 channels (chunk) of rows row + 16 j of a 64-row slot.
+            const int chunk = tid & 7, row = tid >> 3;
+            const uint32_t atom = (uint32_t)(chunk >> 2) * ATOM_BYTES;
+            const uint32_t odd = (uint32_t)(chunk >> 2);  // the halves of a row store in
+                                                          // opposite order: 32 banks at once
+            int seq = 0;
+            for (int t = unit; t < p.tiles && ok; t += units, seq += nstages)
+                for (int i = (d - seq % Cf::DW + Cf::DW) % Cf::DW; i < nstages; i += Cf::DW) {
+                    const int sn = seq + i;
+                    const uint32_t slot = (uint32_t)(sn % Cf::RAW), rphase = (uint32_t)(sn / Cf::RAW) & 1u;
+                    if (!mbar_wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
+                        give_up(p.err, abort);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t src =
+                        smem_u32(smem + Cf::OFF_RAW + slot * RAW_BYTES) + (uint32_t)tid * 16u;
+                    uint4 q[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        q[j] = lds128(src + j * 16 * 128);
+                    const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
+                    const uint32_t phase = (uint32_t)(sn / Cf::STAGES) & 1u;
+                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                        give_up(p.err, abort);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst =
+                        smem_u32(smem + stage * Cf::STAGE_BYTES) + atom + (uint32_t)row * 128u;
+                    const uint32_t at0 = ((2u * (chunk & 3) + odd) ^ (row & 7u)) << 4;
+                    const uint32_t at1 = ((2u * (chunk & 3) + (odd ^ 1u)) ^ (row & 7u)) << 4;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {  // rows 16 apart share the swizzle phase
+                        const uint2 a = q8_values<F16>(q[j].x), b = q8_values<F16>(q[j].y);
+                        const uint2 c = q8_values<F16>(q[j].z), e = q8_values<F16>(q[j].w);
+                        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y);
+                        const uint4 hi = make_uint4(c.x, c.y, e.x, e.y);
+                        sts128(dst + j * 16 * 128 + at0, odd ? hi : lo);
+                        sts128(dst + j * 16 * 128 + at1, odd ? lo : hi);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&a_full[stage]);
+                        mbar_arrive(&raw_empty[slot]);
+                    }
+                }
+        }
+    } else {
+        // ------------------------------------------------ promote and store
+        regs_inc<Cf::R_PROMOTE>();
+        const int pw = wg - 1 - Cf::DW, quarter = warp & 3;
+        const int row = quarter * 32 + lane;  // TMEM lane
+        const uint32_t sring =
+            smem_u32(smem + Cf::OFF_SCALE) + (uint32_t)(pw * SCALE_SLOTS * LANES + row) * 4u;
+        constexpr uintptr_t SB = MODE == kW4 ? 2 : 4;  // bytes of a scale
+        bool ok = true;
+        uint32_t set = 0, set_phase = 0;
+        int l0 = 0, c0 = 0;
+        uintptr_t sp = 0;    // this lane's next scale to copy
+        uint32_t sbyte = 0;  // the low bits of the address of the next scale to use
+        // The aligned word that holds the scale of group i, one copy group each.
+        auto fetch = [&](int i, int slot) {
+            if (i < ngroups)
+                cp_async_4_full(sring + (uint32_t)(slot * LANES) * 4u,
+                                reinterpret_cast<const void *>(sp & ~uintptr_t(3)));
+            sp += (uintptr_t)p.lanes * SB;
+            cp_async_commit();
+        };
+        auto start = [&](int t) {
+            tile_origin(t, p.lanes, p.cols, NT, l0, c0);
+            const int ln = min(l0 + row, p.lanes - 1);
+            sp = reinterpret_cast<uintptr_t>(p.scales) + ((uintptr_t)group0 * p.lanes + ln) * SB;
+            sbyte = (uint32_t)sp;
+            for (int a = 0; a < SCALE_AHEAD; ++a)
+                fetch(a, a);
+        };
+        if (unit < p.tiles)
+            start(unit);
+        float acc[Cf::CPT];
+        for (int t = unit; t < p.tiles && ok; t += units) {
+#pragma unroll
+            for (int j = 0; j < Cf::CPT; ++j)
+                acc[j] = 0.f;
+            for (int i = 0; i < ngroups; ++i) {
+                const int slot = i % SCALE_SLOTS;
+                fetch(i + SCALE_AHEAD, (i + SCALE_AHEAD) % SCALE_SLOTS);
+                cp_async_wait<SCALE_AHEAD>();
+                const uint32_t word = lds32(sring + (uint32_t)(slot * LANES) * 4u);
+                float s;
+                if constexpr (MODE == kW4) {
+                    s = to_f32<F16>((uint16_t)(word >> (8 * (sbyte & 2))));
+                    sbyte += 2u * (uint32_t)p.lanes;
+                } else {
+                    s = __uint_as_float(word);
+                }
+                if (!mbar_wait_bounded(&tfull[set], set_phase, p.limit_ns, abort)) {
+                    give_up(p.err, abort);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + set * NT +
+                                       (uint32_t)(pw * Cf::CPT);
+                float v[2][16];
+                tmem_ld_x16(taddr, v[0]);
+#pragma unroll
+                for (int c = 0; c < Cf::CPT / 16; ++c) {
+                    tmem_wait_ld();
+                    if (c + 1 < Cf::CPT / 16) {
+                        tmem_ld_x16(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&tempty[set]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2)
+                        fma2(acc[c * 16 + j], acc[c * 16 + j + 1], s, v[c & 1][j], v[c & 1][j + 1]);
+                }
+                if (++set == Cf::SETS) {
+                    set = 0;
+                    set_phase ^= 1;
+                }
+            }
+            if (!ok)
+                break;
+            if (S > 1) {
+                const uint32_t part =
+                    smem_u32(smem) + (uint32_t)(row * Cf::PITCH + pw * Cf::CPT) * 4u;
+#pragma unroll
+                for (int j = 0; j < Cf::CPT; j += 4)
+                    sts128(part + 4 * j,
+                           make_uint4(__float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                                      __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3])));
+                break;
+            }
+            const int gl = l0 + row, gc = c0 + pw * Cf::CPT;
+            if (t + units < p.tiles)
+                start(t + units);
+            if (gl < p.lanes) {
+                if constexpr (MODE == kW4) {  // a warp's lanes: 32 consecutive floats of a row of C
+                    float *cp = p.C + (int64_t)gc * p.lanes + gl;
+                    const int rows = p.cols - gc;
+#pragma unroll
+                    for (int j = 0; j < Cf::CPT; ++j, cp += p.lanes)
+                        if (j < rows)
+                            *cp = acc[j];
+                } else {
+                    float *cp = p.C + (int64_t)gl * p.cols + gc;
+                    const int cols = p.cols - gc;
+#pragma unroll
+                    for (int j = 0; j < Cf::CPT; j += 4) {
+                        if (p.c_vec && j + 3 < cols) {
+                            *reinterpret_cast<float4 *>(cp + j) =
+                                make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (j + e < cols)
+                                    cp[j + e] = acc[j + e];
+                        }
+                    }
+                }
+            }
+        }
+        cp_async_wait<0>();
+    }
+
+    if (S > 1) {
+        cluster_sync();  // every partial tile of the cluster is in shared memory
+        if (wg > Cf::DW) {
+            int l0, c0;
+            tile_origin(unit, p.lanes, p.cols, NT, l0, c0);
+            const int row = threadIdx.x & 127, pw = wg - 1 - Cf::DW;
+            const int cols = NT / S, first = (int)rank * cols;
+            const uint32_t mine = smem_u32(smem) + (uint32_t)(row * Cf::PITCH) * 4u;
+            const int gl = l0 + row;
+            for (int cc = pw * 4; cc < cols; cc += 4 * Cf::PW) {
+                const uint32_t off = (uint32_t)(first + cc) * 4u;
+                float4 acc = ld_shared_cluster_v4(mapa_shared(mine + off, 0));
+                for (int q = 1; q < S; ++q) {
+                    const float4 v = ld_shared_cluster_v4(mapa_shared(mine + off, (uint32_t)q));
+                    acc.x += v.x;
+                    acc.y += v.y;
+                    acc.z += v.z;
+                    acc.w += v.w;
+                }
+                const float a[4] = {acc.x, acc.y, acc.z, acc.w};
+                const int gc = c0 + first + cc;
+                if (gl < p.lanes) {
+                    if constexpr (MODE == kW4) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (gc + e < p.cols)
+                                p.C[(int64_t)(gc + e) * p.lanes + gl] = a[e];
+                    } else {
+                        float *cp = p.C + (int64_t)gl * p.cols + gc;
+                        if (p.c_vec && gc + 3 < p.cols) {
+                            *reinterpret_cast<float4 *>(cp) = acc;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (gc + e < p.cols)
+                                    cp[e] = a[e];
+                        }
+                    }
+                }
+            }
+        }
+        cluster_sync();  // no CTA leaves while a peer may still read its partial
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, Cf::TMEM_COLS);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// rows x cols values of `elem` bytes, rows ld values apart, boxes of box_rows x box_cols.
+static bool encode_map(EncodeTiledFn fn, CUtensorMap *map, CUtensorMapDataType type, int elem,
+                       const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
+                       uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle)
+{
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {ld * elem};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Mode MODE, bool F16, int NT>
+static cudaError_t launch_nt(Params p, const CUtensorMap &codes, const CUtensorMap &b, int sms,
+                             cudaStream_t stream)
+{
+    using Cf = Cfg<NT>;
+    auto kernel = lowbit_tc_kernel<MODE, F16, NT>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = set_smem_limit_once(kernel, (int)Cf::SMEM_BYTES, done);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = (int64_t)((p.lanes + LANES - 1) / LANES) * ((p.cols + NT - 1) / NT);
+    if (tiles > 0x3fffffff)
+        return cudaErrorInvalidValue;
+    p.tiles = (int)tiles;
+    // Few tiles: split the depth while every CTA keeps at least four blocks
+    // and all clusters are resident at once.
+    const int blocks = (p.depth + BLOCK - 1) / BLOCK;
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= sms && blocks >= splits * 2 * 4)
+        splits *= 2;
+    static std::atomic<int> resident[4][64] = {};
+    while (splits > 1) {
+        const int slot = splits == 2 ? 1 : splits == 4 ? 2 : 3;
+        const int fit = resident_clusters(kernel, splits, kThreads, Cf::SMEM_BYTES, resident[slot]);
+        if (fit <= 0 || tiles <= fit)
+            break;
+        splits /= 2;
+    }
+    p.splits = splits;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(splits > 1 ? tiles * splits : tiles < sms ? tiles : sms), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, codes, b, p);
+}
+
+static int columns_of(int cols, bool narrow)
+{
+    return cols <= 32 && narrow ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+}
+
+static Params params_of(const DeviceContext &d, bool mute)
+{
+    Params p = {};
+    p.err = d.err;
+    p.limit_ns = d.wait_limit_ns;
+    p.mute = mute ? 1 : 0;
+    return p;
+}
+
+template <bool F16>
+static cudaError_t w4_typed(const W4Launch &L, int64_t lda, const DeviceContext &d, bool mute,
+                            cudaStream_t stream)
+{
+    auto fn = reinterpret_cast<EncodeTiledFn>(d.encode_tiled);
+    const int nt = columns_of(L.M, true);
+    CUtensorMap codes, b;
+    if (!fn ||
+        !encode_map(fn, &codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.codes, (uint64_t)L.N,
+                    (uint64_t)w4_row_bytes(L.K), (uint64_t)w4_row_bytes(L.K), LANES, kW4BlockBytes,
+                    CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_map(fn, &b, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    2, L.A, (uint64_t)L.M, (uint64_t)L.K, (uint64_t)lda, (uint32_t)nt, BK,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    Params p = params_of(d, mute);
+    p.lanes = L.N;
+    p.cols = L.M;
+    p.depth = L.K;
+    p.group = L.group;
+    p.scales = L.scales;
+    p.zeros = L.zeros;
+    p.C = L.C;
+    return nt == 32    ? launch_nt<kW4, F16, 32>(p, codes, b, d.sms, stream)
+           : nt == 64  ? launch_nt<kW4, F16, 64>(p, codes, b, d.sms, stream)
+           : nt == 128 ? launch_nt<kW4, F16, 128>(p, codes, b, d.sms, stream)
+                       : launch_nt<kW4, F16, 256>(p, codes, b, d.sms, stream);
+}
+
+template <bool F16>
+static cudaError_t q8t_typed(const Q8tLaunch &L, int64_t ldy, const DeviceContext &d, bool mute,
+                             cudaStream_t stream)
+{
+    auto fn = reinterpret_cast<EncodeTiledFn>(d.encode_tiled);
+    const int nt = columns_of(L.N, false);
+    CUtensorMap codes, b;
+    if (!fn ||
+        !encode_map(fn, &codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.codes, (uint64_t)L.M,
+                    (uint64_t)q8_pitch(L.K), (uint64_t)q8_pitch(L.K), BK, LANES,
+                    CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_map(fn, &b, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    2, L.dY, (uint64_t)L.M, (uint64_t)L.N, (uint64_t)ldy, BK, 64,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    Params p = params_of(d, mute);
+    p.lanes = L.K;
+    p.cols = L.N;
+    p.depth = L.M;
+    p.group = kQ8Rows;
+    p.scales = L.scales;
+    p.C = L.C;
+    p.c_vec = L.N % 4 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 15) == 0;
+    return nt == 64    ? launch_nt<kQ8t, F16, 64>(p, codes, b, d.sms, stream)
+           : nt == 128 ? launch_nt<kQ8t, F16, 128>(p, codes, b, d.sms, stream)
+                       : launch_nt<kQ8t, F16, 256>(p, codes, b, d.sms, stream);
+}
+
+} // namespace lbt
+
+cudaError_t launch_w4_tc(const W4Launch &L, int64_t lda, const DeviceContext &d, bool mute,
+                         cudaStream_t stream)
+{
+    return L.f16 ? lbt::w4_typed<true>(L, lda, d, mute, stream)
+                 : lbt::w4_typed<false>(L, lda, d, mute, stream);
+}
+
+cudaError_t launch_q8t_tc(const Q8tLaunch &L, int64_t ldy, const DeviceContext &d, bool mute,
+                          cudaStream_t stream)
+{
+    return L.f16 ? lbt::q8t_typed<true>(L, ldy, d, mute, stream)
+                 : lbt::q8t_typed<false>(L, ldy, d, mute, stream);
+}
+
+} // namespace rtm
