@@ -67,6 +67,9 @@ enum Mode { kW4, kQ8t };
 
 template <int NT>
 struct Cfg {
+    static constexpr bool PAIR = NT == 256;       // two CTAs to a tile
+    static constexpr int TILE_LANES = PAIR ? 2 * LANES : LANES;
+    static constexpr int BN = PAIR ? NT / 2 : NT;  // columns staged by a CTA
     static constexpr int DW = NT == 256 ? 1 : 2;  // dequantising warpgroups
     static constexpr int PW = 3 - DW;             // promoting warpgroups
     // Registers a thread after the split: the four warpgroups share what the block
@@ -76,9 +79,9 @@ struct Cfg {
     static constexpr int CPT = NT / PW;           // columns of a promoting thread
     static constexpr int SETS = NT == 256 ? 2 : 4;
     static constexpr uint32_t TMEM_COLS = SETS * NT;
-    static constexpr uint32_t B_BYTES = NT * BK * 2;
+    static constexpr uint32_t B_BYTES = BN * BK * 2;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = NT == 256 ? 3 : 4;
+    static constexpr int STAGES = NT == 256 ? 5 : 4;
     static constexpr int RAW = NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 10 : 12;
     static constexpr uint32_t OFF_RAW = STAGES * STAGE_BYTES;
     static constexpr uint32_t OFF_SCALE = OFF_RAW + RAW * RAW_BYTES;
@@ -98,19 +101,19 @@ struct Params {
     float *C;
     int *err;
     unsigned long long limit_ns;
-    int splits;  // CTAs of a cluster, each summing a range of the depth
+    int splits;  // CTAs (pairs) of a cluster, each summing a range of the depth
     int tiles;
     int mute;    // failure-detection self-test: issue no loads
     int c_vec;   // q8t: rows of dW on 16-byte boundaries
 };
 
-// kind::f16, D fp32, M = 128, N = NT; w4: both operands K-major, q8t: both MN-major.
+// kind::f16, D fp32, M = 128 (256 for a pair), N = NT; w4: both operands K-major, q8t: both MN-major.
 template <Mode MODE, bool F16, int NT>
 __host__ __device__ constexpr uint32_t idesc()
 {
     constexpr uint32_t mn = MODE == kQ8t ? 1u : 0u, t = F16 ? 0u : 1u;
     return (1u << 4) | (t << 7) | (t << 10) | (mn << 15) | (mn << 16) |
-           ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(LANES >> 4) << 24);
+           ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(Cfg<NT>::TILE_LANES >> 4) << 24);
 }
 
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo)
@@ -123,6 +126,34 @@ __device__ __forceinline__ void give_up(int *err, volatile int *abort)
 {
     atomicCAS(err, 0, kDevErrTimeout);
     *abort = 1;
+}
+
+// mbar_wait_bounded with the clock and the abort flag read once in 64 polls: a
+// read of the global timer takes long enough (about a microsecond) to be felt
+// where, as here, a chain of short waits passes each group on (8192^3 weight
+// gradient @@).
+__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                       volatile int *abort)
+{
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity))
+                return true;
+        if (*abort)
+            return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0)
+            t0 = t;
+        else if (t - t0 > limit_ns)
+            return false;
+    }
+}
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                             volatile int *abort)
+{
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, limit_ns, abort);
 }
 
 template <int R>
@@ -235,15 +266,117 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
                  : "memory");
 }
 
-// Tiles in bands of 16 lane tiles, so that the tiles in flight share both operands in L2.
-__device__ __forceinline__ void tile_origin(int t, int lanes, int cols, int nt, int &l0, int &c0)
+// First lane and column of a tile, in bands of 2048 lanes, so that the tiles in
+// flight share both operands in L2.
+template <int NT>
+__device__ __forceinline__ void tile_origin(int t, int lanes, int cols, int &l0, int &c0)
 {
-    constexpr int BAND = 16;
-    const int tl = (lanes + LANES - 1) / LANES, tc = (cols + nt - 1) / nt;
+    constexpr int LT = Cfg<NT>::TILE_LANES, BAND = 2048 / LT;
+    const int tl = (lanes + LT - 1) / LT, tc = (cols + NT - 1) / NT;
     const int band = t / (BAND * tc), first = band * BAND;
     const int rows = min(tl - first, BAND), in = t - band * BAND * tc;
-    l0 = (first + in % rows) * LANES;
-    c0 = in / rows * nt;
+    l0 = (first + in % rows) * LT;
+    c0 = in / rows * NT;
+}
+
+// Arrive on the leading CTA's barrier. Nothing this CTA wrote is read through
+// the leader: the tensor core of this SM reads the stage (made visible to it by
+// fence.proxy.async) and tensor memory, so the arrival needs no release at
+// cluster scope. With one, by a thread that forwarded each stage, the pair ran
+// at 0.9 us a stage (8192^3: 1.64 ms).
+template <bool PAIR>
+__device__ __forceinline__ void arrive_leader(uint64_t *bar, uint32_t leader)
+{
+    if constexpr (PAIR)
+        mbar_arrive_cluster_tmem_free(mapa_shared(smem_u32(bar), leader));
+    else
+        mbar_arrive(bar);
+}
+
+// Arrive on `bar` (in both CTAs of a pair, or in `mask`) when the MMAs issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar, uint32_t mask)
+{
+    if constexpr (PAIR)
+        umma_commit_pair_multicast(bar, (uint16_t)mask);
+    else
+        umma_commit(bar);
+}
+
+// The MMA thread's loop; PG: 16-deep steps of a group (8, 4 or 2). The loop is
+// written for few instructions a step: the thread shares its scheduler with
+// three busy warps, and 480 cycles a step (256 x 256 x 16: 128 at the tensor
+// core's rate) went by when the steps, groups and descriptors were worked out
+// one by one.
+template <Mode MODE, bool F16, int NT, int PG>
+__device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint32_t tmem_base,
+                                          int unit, int units, int nstages, int depth,
+                                          uint32_t pair_mask, uint64_t *full, uint64_t *empty,
+                                          uint64_t *tfull, uint64_t *tempty, uint64_t *drain,
+                                          volatile int *abort)
+{
+    using Cf = Cfg<NT>;
+    constexpr bool PAIR = Cf::PAIR;
+    constexpr int STEPS = BK / UMMA_K;
+    // K-major: rows of 128 B, 8-row groups 1024 B apart, 32 B a step. MN-major:
+    // 64-wide atoms ATOM_BYTES apart, 16 rows of 128 B a step.
+    constexpr uint32_t LBO = MODE == kW4 ? 16 : ATOM_BYTES;
+    constexpr uint32_t ADVANCE = (MODE == kW4 ? UMMA_K * 2 : UMMA_K * 128) >> 4;
+    const uint64_t desc0 = sdesc_sw128(smem0, LBO, 1024);
+    const int tail = min(STEPS, (depth - (nstages - 1) * BK + UMMA_K - 1) / UMMA_K);
+    uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
+    bool any = false;
+    for (int t = unit; t < p.tiles; t += units) {
+        for (int i = 0; i < nstages; ++i) {
+            if (!wait_bounded(&full[stage], phase, p.limit_ns, abort)) {
+                give_up(p.err, abort);
+                goto out;
+            }
+            tc_fence_after();
+            const bool last = i == nstages - 1;
+            const int steps = last ? tail : STEPS;
+            const uint64_t adesc = desc0 + stage * (Cf::STAGE_BYTES >> 4);
+            const uint64_t bdesc = adesc + (A_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < STEPS; ++kk)
+                if (kk < steps) {
+                    const bool begin = PG == 8 ? kk == 0 && (i & 1) == 0 : kk % PG == 0;
+                    if (begin) {
+                        if (!wait_bounded(&tempty[set], set_phase ^ 1, p.limit_ns, abort)) {
+                            give_up(p.err, abort);
+                            goto out;
+                        }
+                        tc_fence_after();
+                    }
+                    if constexpr (PAIR)
+                        umma_f16_pair(tmem_base + set * NT, adesc + kk * ADVANCE,
+                                      bdesc + kk * ADVANCE, idesc<MODE, F16, NT>(), !begin);
+                    else
+                        umma_f16(tmem_base + set * NT, adesc + kk * ADVANCE, bdesc + kk * ADVANCE,
+                                 idesc<MODE, F16, NT>(), !begin);
+                    const bool end = PG == 8 ? kk == STEPS - 1 && (i & 1) == 1 : kk % PG == PG - 1;
+                    if (end || (last && kk == steps - 1)) {
+                        commit<PAIR>(&tfull[set], pair_mask);
+                        if (++set == Cf::SETS) {
+                            set = 0;
+                            set_phase ^= 1;
+                        }
+                    }
+                }
+            any = true;
+            commit<PAIR>(&empty[stage], pair_mask);
+            if (++stage == Cf::STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    }
+out:
+    if (any) {
+        commit<PAIR>(drain, pair_mask & (~pair_mask + 1));  // the even CTA
+        volatile int no_abort = 0;
+        wait_bounded(drain, 0, p.limit_ns, &no_abort);  // before TMEM is freed
+    }
 }
 
 template <Mode MODE, bool F16, int NT>
@@ -256,21 +389,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     uint64_t *raw_full = reinterpret_cast<uint64_t *>(smem + Cf::OFF_BARS);
     uint64_t *raw_empty = raw_full + Cf::RAW;
-    uint64_t *a_full = raw_empty + Cf::RAW;
-    uint64_t *b_full = a_full + Cf::STAGES;
-    uint64_t *empty = b_full + Cf::STAGES;
+    uint64_t *full = raw_empty + Cf::RAW;  // a stage: both operands
+    uint64_t *empty = full + Cf::STAGES;
     uint64_t *tfull = empty + Cf::STAGES;
     uint64_t *tempty = tfull + Cf::SETS;
     uint64_t *drain = tempty + Cf::SETS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert((2 * Cf::RAW + 3 * Cf::STAGES + 2 * Cf::SETS + 1) * 8 + 8 <= 512, "barriers");
+    static_assert((2 * Cf::RAW + 2 * Cf::STAGES + 2 * Cf::SETS + 1) * 8 + 8 <= 512, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wg = warp >> 2;
+    constexpr bool PAIR = Cf::PAIR;
+    constexpr int CTAS = PAIR ? 2 : 1;
     const int S = p.splits;
-    const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
-    const int unit = blockIdx.x / S, units = gridDim.x / S;
+    const uint32_t cta = PAIR || S > 1 ? cluster_ctarank() : 0u;
+    const uint32_t rank = cta / CTAS;               // of the depth split
+    const uint32_t leader = cta - cta % CTAS;       // the pair's even CTA, which issues the MMAs
+    const bool even = cta == leader;
+    const int lane_half = even ? 0 : LANES;         // this CTA's lanes of a pair's tile
+    const uint32_t pair_mask = 3u << leader;
+    const int unit = blockIdx.x / (S * CTAS), units = gridDim.x / (S * CTAS);
 
     // This CTA's depth: whole blocks, the last one possibly ragged.
     const int blocks = (p.depth + BLOCK - 1) / BLOCK;
@@ -288,13 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&raw_empty[i], 4);  // the warps that read the slot
         }
         for (int i = 0; i < Cf::STAGES; ++i) {
-            mbar_init(&a_full[i], 4);  // the warps that wrote the stage
-            mbar_init(&b_full[i], 1);
+            mbar_init(&full[i], 4 * CTAS + 1);  // the warps that write a stage, its bytes
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < Cf::SETS; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 4 * Cf::PW);
+            mbar_init(&tempty[i], 4 * Cf::PW * CTAS);
         }
         mbar_init(drain, 1);
         *abort = 0;
@@ -303,11 +441,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_b);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, Cf::TMEM_COLS);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(tmem_slot, Cf::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, Cf::TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        cluster_sync();  // the peer's barriers are initialised before any remote signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
@@ -319,18 +464,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int steps = MODE == kW4 ? (depth + BLOCK - 1) / BLOCK : nstages;
             for (int t = unit; t < p.tiles && !*abort; t += units) {
                 int l0, c0;
-                tile_origin(t, p.lanes, p.cols, NT, l0, c0);
+                tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
                 for (int i = 0; i < steps; ++i) {
-                    if (!mbar_wait_bounded(&raw_empty[slot], phase ^ 1, p.limit_ns, abort)) {
+                    if (!wait_bounded(&raw_empty[slot], phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         break;
                     }
                     const uint32_t dst = smem_u32(smem + Cf::OFF_RAW + slot * RAW_BYTES);
                     mbar_arrive_expect_tx(&raw_full[slot], RAW_BYTES);
                     if constexpr (MODE == kW4)
-                        tma_load_2d(dst, &tm_codes, &raw_full[slot], (block0 + i) * kW4BlockBytes, l0);
+                        tma_load_2d(dst, &tm_codes, &raw_full[slot], (block0 + i) * kW4BlockBytes,
+                                    l0 + lane_half);
                     else
-                        tma_load_2d(dst, &tm_codes, &raw_full[slot], l0, d0 + i * BK);
+                        tma_load_2d(dst, &tm_codes, &raw_full[slot], l0 + lane_half, d0 + i * BK);
                     issued |= 1u << slot;
                     parity = (parity & ~(1u << slot)) | (phase << slot);
                     if (++slot == Cf::RAW) {
@@ -344,100 +490,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < Cf::RAW; ++i)
                 if (issued & (1u << i))
-                    mbar_wait_bounded(&raw_full[i], (parity >> i) & 1u, p.limit_ns, &no_abort);
+                    wait_bounded(&raw_full[i], (parity >> i) & 1u, p.limit_ns, &no_abort);
         } else if (warp == 2 && lane == 0 && !p.mute) {
             // ------------------------------------------------ 2-byte operand
-            uint32_t stage = 0, phase = 0, issued = 0, parity = 0;
+            uint32_t stage = 0, phase = 0;
             for (int t = unit; t < p.tiles && !*abort; t += units) {
                 int l0, c0;
-                tile_origin(t, p.lanes, p.cols, NT, l0, c0);
+                tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
                 for (int i = 0; i < nstages; ++i) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                    if (!wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         break;
                     }
                     const uint32_t dst = smem_u32(smem + stage * Cf::STAGE_BYTES + A_BYTES);
-                    mbar_arrive_expect_tx(&b_full[stage], Cf::B_BYTES);
-                    if constexpr (MODE == kW4) {
-                        tma_load_2d(dst, &tm_b, &b_full[stage], d0 + i * BK, c0);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < NT / 64; ++j)
-                            tma_load_2d(dst + j * ATOM_BYTES, &tm_b, &b_full[stage], c0 + 64 * j,
-                                        d0 + i * BK);
-                    }
-                    issued |= 1u << stage;
-                    parity = (parity & ~(1u << stage)) | (phase << stage);
-                    if (++stage == Cf::STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            volatile int no_abort = 0;
-#pragma unroll 1
-            for (int i = 0; i < Cf::STAGES; ++i)
-                if (issued & (1u << i))
-                    mbar_wait_bounded(&b_full[i], (parity >> i) & 1u, p.limit_ns, &no_abort);
-        } else if (warp == 1 && lane == 0) {
-            // ------------------------------------------------ MMA issuer
-            uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
-            bool issued_any = false, ok = true;
-            const int per_group = p.group / UMMA_K;
-            for (int t = unit; t < p.tiles && ok; t += units) {
-                int in_group = 0;
-                for (int i = 0; i < nstages && ok; ++i) {
-                    if (!mbar_wait_bounded(&b_full[stage], phase, p.limit_ns, abort) ||
-                        !mbar_wait_bounded(&a_full[stage], phase, p.limit_ns, abort)) {
-                        give_up(p.err, abort);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * Cf::STAGE_BYTES);
-                    const uint32_t sb = sa + A_BYTES;
-                    const int steps = min(BK / UMMA_K, (depth - i * BK + UMMA_K - 1) / UMMA_K);
-                    for (int kk = 0; kk < steps; ++kk) {
-                        if (in_group == 0) {
-                            if (!mbar_wait_bounded(&tempty[set], set_phase ^ 1, p.limit_ns, abort)) {
-                                give_up(p.err, abort);
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                        }
-                        uint64_t adesc, bdesc;
+                    if constexpr (PAIR) {  // each CTA half the columns, both signal the even CTA
+                        if (even)
+                            mbar_arrive_expect_tx(&full[stage], 2 * Cf::B_BYTES);
+                        const uint32_t bar = mapa_shared(smem_u32(&full[stage]), leader);
+                        const int cc = c0 + (even ? 0 : Cf::BN);
                         if constexpr (MODE == kW4) {
-                            adesc = sdesc_sw128(sa + kk * UMMA_K * 2, 16, 1024);
-                            bdesc = sdesc_sw128(sb + kk * UMMA_K * 2, 16, 1024);
+                            tma_load_2d_pair(dst, &tm_b, bar, d0 + i * BK, cc);
                         } else {
-                            adesc = sdesc_sw128(sa + kk * UMMA_K * 128, ATOM_BYTES, 1024);
-                            bdesc = sdesc_sw128(sb + kk * UMMA_K * 128, ATOM_BYTES, 1024);
+#pragma unroll
+                            for (int j = 0; j < Cf::BN / 64; ++j)
+                                tma_load_2d_pair(dst + j * ATOM_BYTES, &tm_b, bar, cc + 64 * j,
+                                                 d0 + i * BK);
                         }
-                        umma_f16(tmem_base + set * NT, adesc, bdesc, idesc<MODE, F16, NT>(),
-                                 in_group != 0 ? 1u : 0u);
-                        issued_any = true;
-                        if (++in_group == per_group || (i == nstages - 1 && kk == steps - 1)) {
-                            umma_commit(&tfull[set]);
-                            in_group = 0;
-                            if (++set == Cf::SETS) {
-                                set = 0;
-                                set_phase ^= 1;
-                            }
+                    } else {
+                        mbar_arrive_expect_tx(&full[stage], Cf::B_BYTES);
+                        if constexpr (MODE == kW4) {
+                            tma_load_2d(dst, &tm_b, &full[stage], d0 + i * BK, c0);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < Cf::BN / 64; ++j)
+                                tma_load_2d(dst + j * ATOM_BYTES, &tm_b, &full[stage],
+                                            c0 + 64 * j, d0 + i * BK);
                         }
                     }
-                    umma_commit(&empty[stage]);
                     if (++stage == Cf::STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-            if (issued_any) {
-                umma_commit(drain);
-                volatile int no_abort = 0;
-                mbar_wait_bounded(drain, 0, p.limit_ns, &no_abort);  // before TMEM is freed
+            if (*abort) {  // copies that no MMA waited for get time to land
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) {
+                }
             }
+        } else if (warp == 1 && lane == 0 && even) {
+            // ------------------------------------------------ MMA issuer
+            if (MODE == kQ8t || p.group == 128)
+                issue_all<MODE, F16, NT, 8>(p, smem_u32(smem), tmem_base, unit, units, nstages, depth,
+                                         pair_mask, full, empty, tfull, tempty, drain, abort);
+            else if (p.group == 64)
+                issue_all<MODE, F16, NT, 4>(p, smem_u32(smem), tmem_base, unit, units, nstages, depth,
+                                         pair_mask, full, empty, tfull, tempty, drain, abort);
+            else
+                issue_all<MODE, F16, NT, 2>(p, smem_u32(smem), tmem_base, unit, units, nstages, depth,
+                                         pair_mask, full, empty, tfull, tempty, drain, abort);
         }
         __syncwarp();
     } else if (wg <= Cf::DW) {
@@ -456,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int seq = 0, sbase = 0;  // this CTA's raw slots and stages so far, over all tiles
             for (int t = unit; t < p.tiles && ok; t += units) {
                 int l0, c0;
-                tile_origin(t, p.lanes, p.cols, NT, l0, c0);
-                const int n = min(l0 + tid, p.lanes - 1);  // lanes past the end: any zero point
+                tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
+                const int n = min(l0 + lane_half + tid, p.lanes - 1);  // lanes past the end: any zero point
                 // The word that holds the zero point of (group, lane).
                 auto fetch = [&](int i, int slot) {
                     if (p.zeros && i < nblocks)
@@ -480,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int r = seq + i;  // raw slot number
                     const uint32_t slot = (uint32_t)(r % Cf::RAW), rphase = (uint32_t)(r / Cf::RAW) & 1u;
                     fetch(i + (ZERO_SLOTS - 1) * Cf::DW, (zslot + ZERO_SLOTS - 1) % ZERO_SLOTS);
-                    if (!mbar_wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
+                    if (!wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         ok = false;
                         break;
@@ -515,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int sn = sbase + 2 * i + h;
                         const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
                         const uint32_t phase = (uint32_t)(sn / Cf::STAGES) & 1u;
-                        if (!mbar_wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                        if (!wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
                             give_up(p.err, abort);
                             ok = false;
                             break;
@@ -535,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_proxy_async_shared();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&a_full[stage]);
+                            arrive_leader<PAIR>(&full[stage], leader);
                             // The slot is free once its words have been used, not when
                             // their loads were issued: an arrival between the loads and
                             // their first use let the next copy overtake them.
@@ -561,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = (d - seq % Cf::DW + Cf::DW) % Cf::DW; i < nstages; i += Cf::DW) {
                     const int sn = seq + i;
                     const uint32_t slot = (uint32_t)(sn % Cf::RAW), rphase = (uint32_t)(sn / Cf::RAW) & 1u;
-                    if (!mbar_wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
+                    if (!wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         ok = false;
                         break;
@@ -574,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         q[j] = lds128(src + j * 16 * 128);
                     const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
                     const uint32_t phase = (uint32_t)(sn / Cf::STAGES) & 1u;
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                    if (!wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         ok = false;
                         break;
@@ -595,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&a_full[stage]);
+                        arrive_leader<PAIR>(&full[stage], leader);
                         mbar_arrive(&raw_empty[slot]);
                     }
                 }
@@ -622,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async_commit();
         };
         auto start = [&](int t) {
-            tile_origin(t, p.lanes, p.cols, NT, l0, c0);
+            tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
+            l0 += lane_half;
             const int ln = min(l0 + row, p.lanes - 1);
             sp = reinterpret_cast<uintptr_t>(p.scales) + ((uintptr_t)group0 * p.lanes + ln) * SB;
             sbyte = (uint32_t)sp;
@@ -648,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     s = __uint_as_float(word);
                 }
-                if (!mbar_wait_bounded(&tfull[set], set_phase, p.limit_ns, abort)) {
+                if (!wait_bounded(&tfull[set], set_phase, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     ok = false;
                     break;
@@ -667,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(&tempty[set]);
+                            arrive_leader<PAIR>(&tempty[set], leader);
                     }
 #pragma unroll
                     for (int j = 0; j < 16; j += 2)
@@ -726,16 +838,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();  // every partial tile of the cluster is in shared memory
         if (wg > Cf::DW) {
             int l0, c0;
-            tile_origin(unit, p.lanes, p.cols, NT, l0, c0);
+            tile_origin<NT>(unit, p.lanes, p.cols, l0, c0);
+            l0 += lane_half;
             const int row = threadIdx.x & 127, pw = wg - 1 - Cf::DW;
             const int cols = NT / S, first = (int)rank * cols;
             const uint32_t mine = smem_u32(smem) + (uint32_t)(row * Cf::PITCH) * 4u;
             const int gl = l0 + row;
             for (int cc = pw * 4; cc < cols; cc += 4 * Cf::PW) {
                 const uint32_t off = (uint32_t)(first + cc) * 4u;
-                float4 acc = ld_shared_cluster_v4(mapa_shared(mine + off, 0));
+                float4 acc = ld_shared_cluster_v4(mapa_shared(mine + off, cta % CTAS));
                 for (int q = 1; q < S; ++q) {
-                    const float4 v = ld_shared_cluster_v4(mapa_shared(mine + off, (uint32_t)q));
+                    const float4 v = ld_shared_cluster_v4(
+                        mapa_shared(mine + off, (uint32_t)q * CTAS + cta % CTAS));
                     acc.x += v.x;
                     acc.y += v.y;
                     acc.z += v.z;
@@ -768,9 +882,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        cluster_sync();  // no CTA leaves while its peer may still signal or read it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, Cf::TMEM_COLS);
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem_base, Cf::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, Cf::TMEM_COLS);
     }
 }
 
@@ -803,33 +922,40 @@ static cudaError_t launch_nt(Params p, const CUtensorMap &codes, const CUtensorM
     cudaError_t e = set_smem_limit_once(kernel, (int)Cf::SMEM_BYTES, done);
     if (e != cudaSuccess)
         return e;
-    const int64_t tiles = (int64_t)((p.lanes + LANES - 1) / LANES) * ((p.cols + NT - 1) / NT);
-    if (tiles > 0x3fffffff)
+    constexpr int CTAS = Cf::PAIR ? 2 : 1;
+    const int64_t tiles = (int64_t)((p.lanes + Cf::TILE_LANES - 1) / Cf::TILE_LANES) *
+                          ((p.cols + NT - 1) / NT);
+    if (tiles > 0x1fffffff)
         return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
     // Few tiles: split the depth while every CTA keeps at least four blocks
-    // and all clusters are resident at once.
+    // and all clusters (of at most 8 CTAs) are resident at once.
     const int blocks = (p.depth + BLOCK - 1) / BLOCK;
     int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= sms && blocks >= splits * 2 * 4)
+    while (splits * CTAS < 8 && tiles * splits * CTAS * 2 <= sms && blocks >= splits * 2 * 4)
         splits *= 2;
-    static std::atomic<int> resident[4][64] = {};
-    while (splits > 1) {
-        const int slot = splits == 2 ? 1 : splits == 4 ? 2 : 3;
-        const int fit = resident_clusters(kernel, splits, kThreads, Cf::SMEM_BYTES, resident[slot]);
-        if (fit <= 0 || tiles <= fit)
+    static std::atomic<int> resident[4][64] = {};  // clusters of 1, 2, 4, 8
+    int fit = sms;
+    for (; splits * CTAS > 1; splits /= 2) {
+        const int size = splits * CTAS;
+        const int slot = size == 2 ? 1 : size == 4 ? 2 : 3;
+        fit = resident_clusters(kernel, size, kThreads, Cf::SMEM_BYTES, resident[slot]);
+        if (fit <= 0)
+            fit = sms / size;
+        if (tiles <= fit || splits == 1)
             break;
-        splits /= 2;
     }
+    if (splits * CTAS == 1)
+        fit = sms;
     p.splits = splits;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(splits > 1 ? tiles * splits : tiles < sms ? tiles : sms), 1, 1);
+    cfg.gridDim = dim3((unsigned)((tiles < fit ? tiles : fit) * splits * CTAS), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.x = (unsigned)(splits * CTAS);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -863,7 +989,7 @@ static cudaError_t w4_typed(const W4Launch &L, int64_t lda, const DeviceContext 
                     (uint64_t)w4_row_bytes(L.K), (uint64_t)w4_row_bytes(L.K), LANES, kW4BlockBytes,
                     CU_TENSOR_MAP_SWIZZLE_64B) ||
         !encode_map(fn, &b, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    2, L.A, (uint64_t)L.M, (uint64_t)L.K, (uint64_t)lda, (uint32_t)nt, BK,
+                    2, L.A, (uint64_t)L.M, (uint64_t)L.K, (uint64_t)lda, (uint32_t)(nt < 128 ? nt : 128), BK,
                     CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     Params p = params_of(d, mute);
