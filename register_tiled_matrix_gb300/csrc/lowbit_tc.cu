@@ -26,9 +26,8 @@
 //    lane's scale, add it to fp32 totals in registers, and at the end of the
 //    tile store them.
 // Scales and zero points are 4-byte asynchronous copies that each thread makes
-// for itself many groups ahead. Registers move between the warpgroups: 56 for
-// the issuing threads, 88 for the dequantising, 184 for the promoting ones,
-// which keep up to 128 totals.
+// for itself many groups ahead. Registers move between the warpgroups: few for
+// the issuing threads, most for the promoting ones, which keep up to 128 totals.
 //
 // With few tiles the depth is split over S CTAs of a cluster; their totals meet
 // in shared memory and are added in rank order through distributed shared
@@ -74,7 +73,8 @@ struct Cfg {
     static constexpr int PW = 3 - DW;             // promoting warpgroups
     // Registers a thread after the split: the four warpgroups share what the block
     // was launched with, 4 x 128.
-    static constexpr int R_ISSUE = 56, R_DEQUANT = 88, R_PROMOTE = 184;
+    static constexpr int R_ISSUE = 56, R_DEQUANT = NT == 256 ? 104 : NT == 128 ? 96 : 128;
+    static constexpr int R_PROMOTE = NT >= 128 ? 176 : 192;
     static_assert(R_ISSUE + DW * R_DEQUANT + PW * R_PROMOTE <= 512, "register split");
     static constexpr int CPT = NT / PW;           // columns of a promoting thread
     static constexpr int SETS = NT == 256 ? 2 : 4;
@@ -165,19 +165,6 @@ template <int R>
 __device__ __forceinline__ void regs_inc()
 {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-
-// Each thread of the warp reads its TMEM lane, 16 consecutive columns.
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, float (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]),
-          "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-        : "r"(taddr)
-        : "memory");
 }
 
 // acc += s * v, two at a time.
@@ -303,11 +290,18 @@ __device__ __forceinline__ void commit(uint64_t *bar, uint32_t mask)
         umma_commit(bar);
 }
 
-// The MMA thread's loop; PG: 16-deep steps of a group (8, 4 or 2). The loop is
-// written for few instructions a step: the thread shares its scheduler with
-// three busy warps, and 480 cycles a step (256 x 256 x 16: 128 at the tensor
-// core's rate) went by when the steps, groups and descriptors were worked out
-// one by one.
+// One lane of the converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(p));
+    return p != 0;
+}
+
+// The MMA warp's loop; PG: 16-deep steps of a group (8, 4 or 2). The warp shares
+// its scheduler with three busy warps, so the loop is kept short: every lane
+// runs it (descriptors and counters stay in uniform registers) and one issues.
 template <Mode MODE, bool F16, int NT, int PG>
 __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint32_t tmem_base,
                                           int unit, int units, int nstages, int depth,
@@ -323,10 +317,13 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
     constexpr uint32_t LBO = MODE == kW4 ? 16 : ATOM_BYTES;
     constexpr uint32_t ADVANCE = (MODE == kW4 ? UMMA_K * 2 : UMMA_K * 128) >> 4;
     const uint64_t desc0 = sdesc_sw128(smem0, LBO, 1024);
+    const bool elected = elect_one();
     const int tail = min(STEPS, (depth - (nstages - 1) * BK + UMMA_K - 1) / UMMA_K);
     uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
     bool any = false;
+#pragma unroll 1
     for (int t = unit; t < p.tiles; t += units) {
+#pragma unroll 1
         for (int i = 0; i < nstages; ++i) {
             if (!wait_bounded(&full[stage], phase, p.limit_ns, abort)) {
                 give_up(p.err, abort);
@@ -348,15 +345,18 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
                         }
                         tc_fence_after();
                     }
-                    if constexpr (PAIR)
-                        umma_f16_pair(tmem_base + set * NT, adesc + kk * ADVANCE,
-                                      bdesc + kk * ADVANCE, idesc<MODE, F16, NT>(), !begin);
-                    else
-                        umma_f16(tmem_base + set * NT, adesc + kk * ADVANCE, bdesc + kk * ADVANCE,
-                                 idesc<MODE, F16, NT>(), !begin);
+                    if (elected) {
+                        if constexpr (PAIR)
+                            umma_f16_pair(tmem_base + set * NT, adesc + kk * ADVANCE,
+                                          bdesc + kk * ADVANCE, idesc<MODE, F16, NT>(), !begin);
+                        else
+                            umma_f16(tmem_base + set * NT, adesc + kk * ADVANCE,
+                                     bdesc + kk * ADVANCE, idesc<MODE, F16, NT>(), !begin);
+                    }
                     const bool end = PG == 8 ? kk == STEPS - 1 && (i & 1) == 1 : kk % PG == PG - 1;
                     if (end || (last && kk == steps - 1)) {
-                        commit<PAIR>(&tfull[set], pair_mask);
+                        if (elected)
+                            commit<PAIR>(&tfull[set], pair_mask);
                         if (++set == Cf::SETS) {
                             set = 0;
                             set_phase ^= 1;
@@ -364,7 +364,8 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
                     }
                 }
             any = true;
-            commit<PAIR>(&empty[stage], pair_mask);
+            if (elected)
+                commit<PAIR>(&empty[stage], pair_mask);
             if (++stage == Cf::STAGES) {
                 stage = 0;
                 phase ^= 1;
@@ -373,7 +374,8 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
     }
 out:
     if (any) {
-        commit<PAIR>(drain, pair_mask & (~pair_mask + 1));  // the even CTA
+        if (elected)
+            commit<PAIR>(drain, pair_mask & (~pair_mask + 1));  // the even CTA
         volatile int no_abort = 0;
         wait_bounded(drain, 0, p.limit_ns, &no_abort);  // before TMEM is freed
     }
@@ -462,9 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------ codes
             uint32_t slot = 0, phase = 0, issued = 0, parity = 0;
             const int steps = MODE == kW4 ? (depth + BLOCK - 1) / BLOCK : nstages;
+#pragma unroll 1
             for (int t = unit; t < p.tiles && !*abort; t += units) {
                 int l0, c0;
                 tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
+#pragma unroll 1
                 for (int i = 0; i < steps; ++i) {
                     if (!wait_bounded(&raw_empty[slot], phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
@@ -494,9 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 2 && lane == 0 && !p.mute) {
             // ------------------------------------------------ 2-byte operand
             uint32_t stage = 0, phase = 0;
+#pragma unroll 1
             for (int t = unit; t < p.tiles && !*abort; t += units) {
                 int l0, c0;
                 tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
+#pragma unroll 1
                 for (int i = 0; i < nstages; ++i) {
                     if (!wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
@@ -538,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (globaltimer_ns() - t0 < 200000ull) {
                 }
             }
-        } else if (warp == 1 && lane == 0 && even) {
+        } else if (warp == 1 && even) {
             // ------------------------------------------------ MMA issuer
             if (MODE == kQ8t || p.group == 128)
                 issue_all<MODE, F16, NT, 8>(p, smem_u32(smem), tmem_base, unit, units, nstages, depth,
@@ -555,8 +561,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ dequantise
         // Warpgroup d takes every DW-th raw slot, in order.
         regs_dec<Cf::R_DEQUANT>();
+        // A stage is published (fence, arrival) after the next one's values have been
+        // worked out, so the stores are done by then.
         const int d = wg - 1, tid = threadIdx.x & 127;
         bool ok = true;
+        int written = -1;  // the stage stored and not yet published
+        auto publish = [&]() {
+            if (written >= 0) {
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0)
+                    arrive_leader<PAIR>(&full[written], leader);
+                written = -1;
+            }
+        };
         if constexpr (MODE == kW4) {
             const uint32_t zring = smem_u32(smem + Cf::OFF_ZERO) +
                                    (uint32_t)(d * ZERO_SLOTS * 4 * LANES + tid) * 4u;
@@ -565,68 +583,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int gs = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
             const int glast = (p.depth - 1) >> gs;
             int seq = 0, sbase = 0;  // this CTA's raw slots and stages so far, over all tiles
+#pragma unroll 1
             for (int t = unit; t < p.tiles && ok; t += units) {
                 int l0, c0;
                 tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
                 const int n = min(l0 + lane_half + tid, p.lanes - 1);  // lanes past the end: any zero point
-                // The word that holds the zero point of (group, lane).
-                auto fetch = [&](int i, int slot) {
-                    if (p.zeros && i < nblocks)
-                        for (int g = 0; g < gpb; ++g) {
-                            const int gg = group0 + i * gpb + g;
-                            if (gg <= glast) {
-                                const uintptr_t a = reinterpret_cast<uintptr_t>(
-                                    p.zeros + (int64_t)gg * p.lanes + n);
+                const int first = (d - seq % Cf::DW + Cf::DW) % Cf::DW;
+                // The words that hold the zero points of this lane in a block's groups:
+                // the next block to copy and the low address bits of the next to use.
+                int copied = first;
+                uintptr_t zp = reinterpret_cast<uintptr_t>(p.zeros) +
+                               (uintptr_t)(group0 + first * gpb) * p.lanes + n;
+                uint32_t zbits = (uint32_t)zp;
+                auto fetch = [&](int slot) {
+                    if (p.zeros && copied < nblocks)
+#pragma unroll 1
+                        for (int g = 0; g < gpb; ++g)
+                            if (group0 + copied * gpb + g <= glast)
                                 cp_async_4_full(zring + (uint32_t)((slot * 4 + g) * LANES) * 4u,
-                                                reinterpret_cast<const void *>(a & ~uintptr_t(3)));
-                            }
-                        }
+                                                reinterpret_cast<const void *>(
+                                                    (zp + (uintptr_t)g * p.lanes) & ~uintptr_t(3)));
+                    copied += Cf::DW;
+                    zp += (uintptr_t)(Cf::DW * gpb) * p.lanes;
                     cp_async_commit();
                 };
-                const int first = (d - seq % Cf::DW + Cf::DW) % Cf::DW;
+#pragma unroll 1
                 for (int a = 0; a < ZERO_SLOTS - 1; ++a)
-                    fetch(first + a * Cf::DW, a);
-                int zslot = 0;
-                for (int i = first; i < nblocks; i += Cf::DW) {
+                    fetch(a);
+                uint4 q[4];
+                // 64-byte rows, 64-byte swizzle: quarter c of row r at c ^ (r / 2 mod 4).
+                auto load = [&](int i) {
                     const int r = seq + i;  // raw slot number
-                    const uint32_t slot = (uint32_t)(r % Cf::RAW), rphase = (uint32_t)(r / Cf::RAW) & 1u;
-                    fetch(i + (ZERO_SLOTS - 1) * Cf::DW, (zslot + ZERO_SLOTS - 1) % ZERO_SLOTS);
-                    if (!wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
+                    const uint32_t slot = (uint32_t)(r % Cf::RAW);
+                    if (!wait_bounded(&raw_full[slot], (uint32_t)(r / Cf::RAW) & 1u, p.limit_ns,
+                                      abort)) {
                         give_up(p.err, abort);
-                        ok = false;
-                        break;
+                        return false;
                     }
-                    // 64-byte rows, 64-byte swizzle: quarter c of row r at c ^ (r / 2 mod 4).
                     const uint32_t src =
                         smem_u32(smem + Cf::OFF_RAW + slot * RAW_BYTES) + (uint32_t)tid * 64u;
-                    uint4 q[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         q[c] = lds128(src + (uint32_t)((c ^ ((tid >> 1) & 3)) << 4));
-                    uint32_t zz[4];
+                    return true;
+                };
+                if (first < nblocks)
+                    ok = load(first);
+                int zslot = 0;
+#pragma unroll 1
+                for (int i = first; ok && i < nblocks; i += Cf::DW) {
+                    fetch((zslot + ZERO_SLOTS - 1) % ZERO_SLOTS);
                     cp_async_wait<ZERO_SLOTS - 1>();
+                    uint32_t zz[4];
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         uint32_t z = 8u;
                         if (p.zeros) {
-                            const int g = (w * 32) >> gs;
-                            const int64_t gg = min(group0 + i * gpb + g, glast);
-                            const uintptr_t a =
-                                reinterpret_cast<uintptr_t>(p.zeros + gg * p.lanes + n);
-                            z = (lds32(zring + (uint32_t)((zslot * 4 + g) * LANES) * 4u) >>
-                                 (8 * (a & 3))) & 15u;
+                            const uint32_t g = (w * 32u) >> gs;
+                            z = (lds32(zring + (zslot * 4 + g) * (LANES * 4u)) >>
+                                 (8 * ((zbits + g * p.lanes) & 3))) & 15u;
                         }
                         zz[w] = magic2<F16>() | z | (z << 16);
                     }
+                    zbits += (uint32_t)(Cf::DW * gpb) * p.lanes;
                     zslot = (zslot + 1) % ZERO_SLOTS;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        uint4 v[8];  // word w of quarter c: k = 32 w + 8 c and up
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            v[c] = w4_values<F16>(h == 0 ? q[c].x : q[c].z, zz[2 * h]);
+                            v[4 + c] = w4_values<F16>(h == 0 ? q[c].y : q[c].w, zz[2 * h + 1]);
+                        }
+                        publish();
+                        if (h == 1) {
+                            // The words are used: free the slot, load the next one's. (An
+                            // arrival before the first use of the loaded words let the
+                            // next copy overtake the loads.)
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(&raw_empty[(seq + i) % Cf::RAW]);
+                            if (i + Cf::DW < nblocks && !load(i + Cf::DW)) {
+                                ok = false;
+                                break;
+                            }
+                        }
                         if (2 * i + h >= nstages)
                             break;
                         const int sn = sbase + 2 * i + h;
                         const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
-                        const uint32_t phase = (uint32_t)(sn / Cf::STAGES) & 1u;
-                        if (!wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                        if (!wait_bounded(&empty[stage], ((uint32_t)(sn / Cf::STAGES) & 1u) ^ 1,
+                                          p.limit_ns, abort)) {
                             give_up(p.err, abort);
                             ok = false;
                             break;
@@ -634,83 +681,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t dst =
                             smem_u32(smem + stage * Cf::STAGE_BYTES) + (uint32_t)tid * 128u;
 #pragma unroll
-                        for (int w = 0; w < 2; ++w)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint4 &qq = q[c];
-                                const uint32_t word = h == 0 ? (w == 0 ? qq.x : qq.y)
-                                                             : (w == 0 ? qq.z : qq.w);
-                                sts128(dst + (uint32_t)(((4 * w + c) ^ (tid & 7)) << 4),
-                                       w4_values<F16>(word, zz[2 * h + w]));
-                            }
-                        fence_proxy_async_shared();
-                        __syncwarp();
-                        if (lane == 0) {
-                            arrive_leader<PAIR>(&full[stage], leader);
-                            // The slot is free once its words have been used, not when
-                            // their loads were issued: an arrival between the loads and
-                            // their first use let the next copy overtake them.
-                            if (h == 0)
-                                mbar_arrive(&raw_empty[slot]);
-                        }
+                        for (int c = 0; c < 8; ++c)
+                            sts128(dst + (uint32_t)((c ^ (tid & 7)) << 4), v[c]);
+                        written = (int)stage;
                     }
-                    if (!ok)
-                        break;
                 }
                 seq += nblocks;
                 sbase += nstages;
                 cp_async_wait<0>();
             }
         } else {
-            // Thread: 16 channels (chunk) of rows row + 16 j of a 64-row slot.
-            const int chunk = tid & 7, row = tid >> 3;
-            const uint32_t atom = (uint32_t)(chunk >> 2) * ATOM_BYTES;
-            const uint32_t odd = (uint32_t)(chunk >> 2);  // the halves of a row store in
-                                                          // opposite order: 32 banks at once
-            int seq = 0;
-            for (int t = unit; t < p.tiles && ok; t += units, seq += nstages)
-                for (int i = (d - seq % Cf::DW + Cf::DW) % Cf::DW; i < nstages; i += Cf::DW) {
-                    const int sn = seq + i;
-                    const uint32_t slot = (uint32_t)(sn % Cf::RAW), rphase = (uint32_t)(sn / Cf::RAW) & 1u;
-                    if (!wait_bounded(&raw_full[slot], rphase, p.limit_ns, abort)) {
-                        give_up(p.err, abort);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t src =
-                        smem_u32(smem + Cf::OFF_RAW + slot * RAW_BYTES) + (uint32_t)tid * 16u;
-                    uint4 q[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        q[j] = lds128(src + j * 16 * 128);
-                    const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
-                    const uint32_t phase = (uint32_t)(sn / Cf::STAGES) & 1u;
-                    if (!wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
-                        give_up(p.err, abort);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t dst =
-                        smem_u32(smem + stage * Cf::STAGE_BYTES) + atom + (uint32_t)row * 128u;
-                    const uint32_t at0 = ((2u * (chunk & 3) + odd) ^ (row & 7u)) << 4;
-                    const uint32_t at1 = ((2u * (chunk & 3) + (odd ^ 1u)) ^ (row & 7u)) << 4;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // rows 16 apart share the swizzle phase
-                        const uint2 a = q8_values<F16>(q[j].x), b = q8_values<F16>(q[j].y);
-                        const uint2 c = q8_values<F16>(q[j].z), e = q8_values<F16>(q[j].w);
-                        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y);
-                        const uint4 hi = make_uint4(c.x, c.y, e.x, e.y);
-                        sts128(dst + j * 16 * 128 + at0, odd ? hi : lo);
-                        sts128(dst + j * 16 * 128 + at1, odd ? lo : hi);
-                    }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        arrive_leader<PAIR>(&full[stage], leader);
-                        mbar_arrive(&raw_empty[slot]);
-                    }
+            // Thread: 16 channels (chunk) of rows row + 16 j of a 64-row slot. The
+            // chunks of the second 64 channels take the neighbouring row, whose swizzle
+            // is off by one: a store's eight threads then cover all banks.
+            const int chunk = tid & 7, row = (tid >> 3) ^ (chunk >> 2);
+            const uint32_t src0 = smem_u32(smem + Cf::OFF_RAW) + (uint32_t)(row * 128 + chunk * 16);
+            const uint32_t dst0 =
+                smem_u32(smem) + (uint32_t)(chunk >> 2) * ATOM_BYTES + (uint32_t)row * 128u;
+            const uint32_t at0 = ((2u * (chunk & 3)) ^ (row & 7u)) << 4, at1 = at0 ^ 16u;
+            const int tiles = unit < p.tiles ? (p.tiles - unit + units - 1) / units : 0;
+            const int total = tiles * nstages;  // stages of this CTA, tile after tile
+            uint4 q[4];
+            auto load = [&](int sn) {
+                const uint32_t slot = (uint32_t)(sn % Cf::RAW);
+                if (!wait_bounded(&raw_full[slot], (uint32_t)(sn / Cf::RAW) & 1u, p.limit_ns,
+                                  abort)) {
+                    give_up(p.err, abort);
+                    return false;
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[j] = lds128(src0 + slot * RAW_BYTES + j * 16 * 128);
+                return true;
+            };
+            if (d < total)
+                ok = load(d);
+#pragma unroll 1
+            for (int sn = d; ok && sn < total; sn += Cf::DW) {
+                uint4 v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint2 a = q8_values<F16>(q[j].x), b = q8_values<F16>(q[j].y);
+                    const uint2 c = q8_values<F16>(q[j].z), e = q8_values<F16>(q[j].w);
+                    v[2 * j] = make_uint4(a.x, a.y, b.x, b.y);
+                    v[2 * j + 1] = make_uint4(c.x, c.y, e.x, e.y);
+                }
+                publish();
+                // The words are used: free the slot, load the next one's.
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&raw_empty[sn % Cf::RAW]);
+                if (sn + Cf::DW < total && !load(sn + Cf::DW))
+                    break;
+                const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
+                if (!wait_bounded(&empty[stage], ((uint32_t)(sn / Cf::STAGES) & 1u) ^ 1,
+                                  p.limit_ns, abort)) {
+                    give_up(p.err, abort);
+                    break;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // rows 16 apart share the swizzle phase
+                    const uint32_t dst = dst0 + stage * Cf::STAGE_BYTES + j * 16 * 128;
+                    sts128(dst + at0, v[2 * j]);
+                    sts128(dst + at1, v[2 * j + 1]);
+                }
+                written = (int)stage;
+            }
         }
+        publish();
     } else {
         // ------------------------------------------------ promote and store
         regs_inc<Cf::R_PROMOTE>();
@@ -738,16 +776,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ln = min(l0 + row, p.lanes - 1);
             sp = reinterpret_cast<uintptr_t>(p.scales) + ((uintptr_t)group0 * p.lanes + ln) * SB;
             sbyte = (uint32_t)sp;
+#pragma unroll 1
             for (int a = 0; a < SCALE_AHEAD; ++a)
                 fetch(a, a);
         };
         if (unit < p.tiles)
             start(unit);
         float acc[Cf::CPT];
+#pragma unroll 1
         for (int t = unit; t < p.tiles && ok; t += units) {
 #pragma unroll
             for (int j = 0; j < Cf::CPT; ++j)
                 acc[j] = 0.f;
+#pragma unroll 1
             for (int i = 0; i < ngroups; ++i) {
                 const int slot = i % SCALE_SLOTS;
                 fetch(i + SCALE_AHEAD, (i + SCALE_AHEAD) % SCALE_SLOTS);
@@ -768,22 +809,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + set * NT +
                                        (uint32_t)(pw * Cf::CPT);
-                float v[2][16];
-                tmem_ld_x16(taddr, v[0]);
 #pragma unroll
-                for (int c = 0; c < Cf::CPT / 16; ++c) {
+                for (int c = 0; c < Cf::CPT; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + c, v);
                     tmem_wait_ld();
-                    if (c + 1 < Cf::CPT / 16) {
-                        tmem_ld_x16(taddr + (c + 1) * 16, v[(c + 1) & 1]);
-                    } else {
+                    if (c + 32 == Cf::CPT) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
                             arrive_leader<PAIR>(&tempty[set], leader);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2)
-                        fma2(acc[c * 16 + j], acc[c * 16 + j + 1], s, v[c & 1][j], v[c & 1][j + 1]);
+                    for (int j = 0; j < 32; j += 2)
+                        fma2(acc[c + j], acc[c + j + 1], s, __uint_as_float(v[j]),
+                             __uint_as_float(v[j + 1]));
                 }
                 if (++set == Cf::SETS) {
                     set = 0;
