@@ -128,33 +128,63 @@ __device__ __forceinline__ void give_up(int *err, volatile int *abort)
     *abort = 1;
 }
 
-// mbar_wait_bounded with the clock and the abort flag read once in 64 polls: a
-// read of the global timer takes long enough (about a microsecond) to be felt
-// where, as here, a chain of short waits passes each group on (8192^3 weight
-// gradient @@).
-__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
-                                       volatile int *abort)
+// Barriers by their shared-memory address: the roles keep one address each and
+// step through their rings by adding to it.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
 {
-    uint64_t t0 = 0;
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity))
-                return true;
-        if (*abort)
-            return false;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0)
-            t0 = t;
-        else if (t - t0 > limit_ns)
-            return false;
-    }
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
 }
-__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+
+__device__ __forceinline__ void arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Bounded wait: false when the limit passed or another warp gave up. The clock
+// and the abort flag are read once in 64 polls.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                              volatile int *abort)
 {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, limit_ns, abort);
+    if (try_wait(bar, parity))
+        return true;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1;; ++n) {
+        if (try_wait(bar, parity))
+            return true;
+        if (n % 64 == 0) {
+            if (*abort)
+                return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0)
+                t0 = t;
+            else if (t - t0 > limit_ns)
+                return false;
+        }
+    }
 }
+
+// A place in a ring of N barriers 8 bytes apart: its index and how often (mod 2)
+// the ring has gone round.
+template <int N>
+struct Place {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void advance(uint32_t by = 1)
+    {
+        at += by;
+        if (at >= N) {
+            at -= N;
+            phase ^= 1;
+        }
+    }
+};
 
 template <int R>
 __device__ __forceinline__ void regs_dec()
@@ -272,12 +302,12 @@ __device__ __forceinline__ void tile_origin(int t, int lanes, int cols, int &l0,
 // cluster scope. With one, by a thread that forwarded each stage, the pair ran
 // at 0.9 us a stage (8192^3: 1.64 ms).
 template <bool PAIR>
-__device__ __forceinline__ void arrive_leader(uint64_t *bar, uint32_t leader)
+__device__ __forceinline__ void arrive_leader(uint32_t bar)
 {
     if constexpr (PAIR)
-        mbar_arrive_cluster_tmem_free(mapa_shared(smem_u32(bar), leader));
+        mbar_arrive_cluster_tmem_free(bar);
     else
-        mbar_arrive(bar);
+        arrive(bar);
 }
 
 // Arrive on `bar` (in both CTAs of a pair, or in `mask`) when the MMAs issued so far are done.
@@ -325,7 +355,7 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
     for (int t = unit; t < p.tiles; t += units) {
 #pragma unroll 1
         for (int i = 0; i < nstages; ++i) {
-            if (!wait_bounded(&full[stage], phase, p.limit_ns, abort)) {
+            if (!wait_bounded(smem_u32(&full[stage]), phase, p.limit_ns, abort)) {
                 give_up(p.err, abort);
                 goto out;
             }
@@ -339,7 +369,7 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
                 if (kk < steps) {
                     const bool begin = PG == 8 ? kk == 0 && (i & 1) == 0 : kk % PG == 0;
                     if (begin) {
-                        if (!wait_bounded(&tempty[set], set_phase ^ 1, p.limit_ns, abort)) {
+                        if (!wait_bounded(smem_u32(&tempty[set]), set_phase ^ 1, p.limit_ns, abort)) {
                             give_up(p.err, abort);
                             goto out;
                         }
@@ -377,7 +407,7 @@ out:
         if (elected)
             commit<PAIR>(drain, pair_mask & (~pair_mask + 1));  // the even CTA
         volatile int no_abort = 0;
-        wait_bounded(drain, 0, p.limit_ns, &no_abort);  // before TMEM is freed
+        wait_bounded(smem_u32(drain), 0, p.limit_ns, &no_abort);  // before TMEM is freed
     }
 }
 
@@ -470,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
 #pragma unroll 1
                 for (int i = 0; i < steps; ++i) {
-                    if (!wait_bounded(&raw_empty[slot], phase ^ 1, p.limit_ns, abort)) {
+                    if (!wait_bounded(smem_u32(&raw_empty[slot]), phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         break;
                     }
@@ -494,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < Cf::RAW; ++i)
                 if (issued & (1u << i))
-                    wait_bounded(&raw_full[i], (parity >> i) & 1u, p.limit_ns, &no_abort);
+                    wait_bounded(smem_u32(&raw_full[i]), (parity >> i) & 1u, p.limit_ns, &no_abort);
         } else if (warp == 2 && lane == 0 && !p.mute) {
             // ------------------------------------------------ 2-byte operand
             uint32_t stage = 0, phase = 0;
@@ -504,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
 #pragma unroll 1
                 for (int i = 0; i < nstages; ++i) {
-                    if (!wait_bounded(&empty[stage], phase ^ 1, p.limit_ns, abort)) {
+                    if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         break;
                     }
@@ -564,89 +594,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A stage is published (fence, arrival) after the next one's values have been
         // worked out, so the stores are done by then.
         const int d = wg - 1, tid = threadIdx.x & 127;
+        const uint32_t base = smem_u32(smem);
+        const uint32_t raw_full_at = smem_u32(raw_full), raw_empty_at = smem_u32(raw_empty);
+        const uint32_t empty_at = smem_u32(empty);
+        const uint32_t full_at =
+            PAIR ? mapa_shared(smem_u32(full), leader) : smem_u32(full);
         bool ok = true;
-        int written = -1;  // the stage stored and not yet published
+        uint32_t written = 0;  // the stage stored and not yet published: its barrier
         auto publish = [&]() {
-            if (written >= 0) {
+            if (written) {
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0)
-                    arrive_leader<PAIR>(&full[written], leader);
-                written = -1;
+                    arrive_leader<PAIR>(written);
+                written = 0;
             }
         };
+        Place<Cf::RAW> raw;  // the slot being converted
+        raw.at = d;
+        uint4 q[4];
         if constexpr (MODE == kW4) {
-            const uint32_t zring = smem_u32(smem + Cf::OFF_ZERO) +
-                                   (uint32_t)(d * ZERO_SLOTS * 4 * LANES + tid) * 4u;
-            const int gpb = BLOCK / p.group;  // groups of a block: 1, 2 or 4
-            const int nblocks = block1 - block0;
+            const uint32_t zring =
+                base + Cf::OFF_ZERO + (uint32_t)(d * ZERO_SLOTS * 4 * LANES + tid) * 4u;
             const int gs = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+            const int gpb = BLOCK >> gs;  // groups of a block: 1, 2 or 4
+            const int nblocks = block1 - block0;
             const int glast = (p.depth - 1) >> gs;
-            int seq = 0, sbase = 0;  // this CTA's raw slots and stages so far, over all tiles
+            // 64-byte rows, 64-byte swizzle: quarter c of row r at c ^ (r / 2 mod 4).
+            const uint32_t src0 = base + Cf::OFF_RAW + (uint32_t)(tid * 64 + ((tid & 6) << 3));
+            const uint32_t dst0 = base + (uint32_t)(tid * 128 + ((tid & 7) << 4));
+            auto load = [&]() {
+                if (!wait_bounded(raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
+                    give_up(p.err, abort);
+                    return false;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    q[c] = lds128((src0 + raw.at * RAW_BYTES) ^ (uint32_t)(c << 4));
+                return true;
+            };
+            Place<Cf::STAGES> stage;
+            int first = d;           // this warpgroup's first block of the tile
+            uint32_t tile_stage = 0;  // stages of the tiles before
 #pragma unroll 1
             for (int t = unit; t < p.tiles && ok; t += units) {
                 int l0, c0;
                 tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
-                const int n = min(l0 + lane_half + tid, p.lanes - 1);  // lanes past the end: any zero point
-                const int first = (d - seq % Cf::DW + Cf::DW) % Cf::DW;
+                const int n = min(l0 + lane_half + tid, p.lanes - 1);  // past the end: any zero point
                 // The words that hold the zero points of this lane in a block's groups:
                 // the next block to copy and the low address bits of the next to use.
                 int copied = first;
                 uintptr_t zp = reinterpret_cast<uintptr_t>(p.zeros) +
                                (uintptr_t)(group0 + first * gpb) * p.lanes + n;
-                uint32_t zbits = (uint32_t)zp;
-                auto fetch = [&](int slot) {
-                    if (p.zeros && copied < nblocks)
+                uint32_t zbits = (uint32_t)zp, zslot = 0;
+                auto fetch = [&](uint32_t slot) {
+                    if (copied < nblocks)
 #pragma unroll 1
                         for (int g = 0; g < gpb; ++g)
                             if (group0 + copied * gpb + g <= glast)
-                                cp_async_4_full(zring + (uint32_t)((slot * 4 + g) * LANES) * 4u,
+                                cp_async_4_full(zring + (slot * 4 + g) * (LANES * 4u),
                                                 reinterpret_cast<const void *>(
                                                     (zp + (uintptr_t)g * p.lanes) & ~uintptr_t(3)));
                     copied += Cf::DW;
                     zp += (uintptr_t)(Cf::DW * gpb) * p.lanes;
                     cp_async_commit();
                 };
+                if (p.zeros)
 #pragma unroll 1
-                for (int a = 0; a < ZERO_SLOTS - 1; ++a)
-                    fetch(a);
-                uint4 q[4];
-                // 64-byte rows, 64-byte swizzle: quarter c of row r at c ^ (r / 2 mod 4).
-                auto load = [&](int i) {
-                    const int r = seq + i;  // raw slot number
-                    const uint32_t slot = (uint32_t)(r % Cf::RAW);
-                    if (!wait_bounded(&raw_full[slot], (uint32_t)(r / Cf::RAW) & 1u, p.limit_ns,
-                                      abort)) {
-                        give_up(p.err, abort);
-                        return false;
-                    }
-                    const uint32_t src =
-                        smem_u32(smem + Cf::OFF_RAW + slot * RAW_BYTES) + (uint32_t)tid * 64u;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        q[c] = lds128(src + (uint32_t)((c ^ ((tid >> 1) & 3)) << 4));
-                    return true;
-                };
+                    for (int a = 0; a < ZERO_SLOTS - 1; ++a)
+                        fetch(a);
                 if (first < nblocks)
-                    ok = load(first);
-                int zslot = 0;
+                    ok = load();
+                int i = first;
 #pragma unroll 1
-                for (int i = first; ok && i < nblocks; i += Cf::DW) {
-                    fetch((zslot + ZERO_SLOTS - 1) % ZERO_SLOTS);
-                    cp_async_wait<ZERO_SLOTS - 1>();
+                for (; ok && i < nblocks; i += Cf::DW) {
                     uint32_t zz[4];
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t z = 8u;
-                        if (p.zeros) {
-                            const uint32_t g = (w * 32u) >> gs;
-                            z = (lds32(zring + (zslot * 4 + g) * (LANES * 4u)) >>
-                                 (8 * ((zbits + g * p.lanes) & 3))) & 15u;
-                        }
-                        zz[w] = magic2<F16>() | z | (z << 16);
+                    for (int w = 0; w < 4; ++w)
+                        zz[w] = magic2<F16>() | 0x00080008u;
+                    if (p.zeros) {
+                        fetch((zslot + ZERO_SLOTS - 1) % ZERO_SLOTS);
+                        cp_async_wait<ZERO_SLOTS - 1>();
+                        auto zero = [&](uint32_t g) {
+                            const uint32_t word = lds32(zring + (zslot * 4 + g) * (LANES * 4u));
+                            return magic2<F16>() |
+                                   ((word >> (8 * ((zbits + g * p.lanes) & 3))) & 15u) * 0x00010001u;
+                        };
+                        zz[0] = zero(0);
+                        zz[1] = gs == 5 ? zero(1) : zz[0];
+                        zz[2] = gs < 7 ? zero(64u >> gs) : zz[0];
+                        zz[3] = gs == 5 ? zero(3) : zz[2];
+                        zbits += (uint32_t)(Cf::DW * gpb) * p.lanes;
+                        zslot = (zslot + 1) % ZERO_SLOTS;
                     }
-                    zbits += (uint32_t)(Cf::DW * gpb) * p.lanes;
-                    zslot = (zslot + 1) % ZERO_SLOTS;
+                    if constexpr (Cf::DW == 2) {
+                        const uint32_t sn = tile_stage + 2 * i;
+                        stage.at = sn % Cf::STAGES;
+                        stage.phase = sn / Cf::STAGES & 1;
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint4 v[8];  // word w of quarter c: k = 32 w + 8 c and up
@@ -662,32 +707,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // next copy overtake the loads.)
                             __syncwarp();
                             if (lane == 0)
-                                mbar_arrive(&raw_empty[(seq + i) % Cf::RAW]);
-                            if (i + Cf::DW < nblocks && !load(i + Cf::DW)) {
+                                arrive(raw_empty_at + raw.at * 8);
+                            raw.advance(Cf::DW);
+                            if (i + Cf::DW < nblocks && !load()) {
                                 ok = false;
                                 break;
                             }
                         }
                         if (2 * i + h >= nstages)
                             break;
-                        const int sn = sbase + 2 * i + h;
-                        const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
-                        if (!wait_bounded(&empty[stage], ((uint32_t)(sn / Cf::STAGES) & 1u) ^ 1,
-                                          p.limit_ns, abort)) {
+                        if (!wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns,
+                                          abort)) {
                             give_up(p.err, abort);
                             ok = false;
                             break;
                         }
-                        const uint32_t dst =
-                            smem_u32(smem + stage * Cf::STAGE_BYTES) + (uint32_t)tid * 128u;
+                        const uint32_t dst = dst0 + stage.at * Cf::STAGE_BYTES;
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
-                            sts128(dst + (uint32_t)((c ^ (tid & 7)) << 4), v[c]);
-                        written = (int)stage;
+                            sts128(dst ^ (uint32_t)(c << 4), v[c]);
+                        written = full_at + stage.at * 8;
+                        stage.advance();
                     }
                 }
-                seq += nblocks;
-                sbase += nstages;
+                first = i - nblocks;  // the blocks of all tiles alternate
+                tile_stage += nstages;
                 cp_async_wait<0>();
             }
         } else {
@@ -695,27 +739,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             // chunks of the second 64 channels take the neighbouring row, whose swizzle
             // is off by one: a store's eight threads then cover all banks.
             const int chunk = tid & 7, row = (tid >> 3) ^ (chunk >> 2);
-            const uint32_t src0 = smem_u32(smem + Cf::OFF_RAW) + (uint32_t)(row * 128 + chunk * 16);
-            const uint32_t dst0 =
-                smem_u32(smem) + (uint32_t)(chunk >> 2) * ATOM_BYTES + (uint32_t)row * 128u;
-            const uint32_t at0 = ((2u * (chunk & 3)) ^ (row & 7u)) << 4, at1 = at0 ^ 16u;
+            const uint32_t src0 = base + Cf::OFF_RAW + (uint32_t)(row * 128 + chunk * 16);
+            const uint32_t dst0 = base + (uint32_t)(chunk >> 2) * ATOM_BYTES +
+                                  (uint32_t)row * 128u + (((2u * (chunk & 3)) ^ (row & 7u)) << 4);
             const int tiles = unit < p.tiles ? (p.tiles - unit + units - 1) / units : 0;
             const int total = tiles * nstages;  // stages of this CTA, tile after tile
-            uint4 q[4];
-            auto load = [&](int sn) {
-                const uint32_t slot = (uint32_t)(sn % Cf::RAW);
-                if (!wait_bounded(&raw_full[slot], (uint32_t)(sn / Cf::RAW) & 1u, p.limit_ns,
-                                  abort)) {
+            auto load = [&]() {
+                if (!wait_bounded(raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     return false;
                 }
+                const uint32_t src = src0 + raw.at * RAW_BYTES;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    q[j] = lds128(src0 + slot * RAW_BYTES + j * 16 * 128);
+                    q[j] = lds128(src + j * 16 * 128);
                 return true;
             };
+            Place<Cf::STAGES> stage;
+            stage.at = d;
             if (d < total)
-                ok = load(d);
+                ok = load();
 #pragma unroll 1
             for (int sn = d; ok && sn < total; sn += Cf::DW) {
                 uint4 v[8];
@@ -730,22 +773,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The words are used: free the slot, load the next one's.
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&raw_empty[sn % Cf::RAW]);
-                if (sn + Cf::DW < total && !load(sn + Cf::DW))
+                    arrive(raw_empty_at + raw.at * 8);
+                raw.advance(Cf::DW);
+                if (sn + Cf::DW < total && !load())
                     break;
-                const uint32_t stage = (uint32_t)(sn % Cf::STAGES);
-                if (!wait_bounded(&empty[stage], ((uint32_t)(sn / Cf::STAGES) & 1u) ^ 1,
-                                  p.limit_ns, abort)) {
+                if (!wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     break;
                 }
+                const uint32_t dst = dst0 + stage.at * Cf::STAGE_BYTES;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // rows 16 apart share the swizzle phase
-                    const uint32_t dst = dst0 + stage * Cf::STAGE_BYTES + j * 16 * 128;
-                    sts128(dst + at0, v[2 * j]);
-                    sts128(dst + at1, v[2 * j + 1]);
+                    sts128(dst + j * 16 * 128, v[2 * j]);
+                    sts128((dst ^ 16u) + j * 16 * 128, v[2 * j + 1]);
                 }
-                written = (int)stage;
+                written = full_at + stage.at * 8;
+                stage.advance(Cf::DW);
             }
         }
         publish();
@@ -757,6 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sring =
             smem_u32(smem + Cf::OFF_SCALE) + (uint32_t)(pw * SCALE_SLOTS * LANES + row) * 4u;
         constexpr uintptr_t SB = MODE == kW4 ? 2 : 4;  // bytes of a scale
+        const uint32_t tfull_at = smem_u32(tfull);
+        const uint32_t tempty_at =
+            PAIR ? mapa_shared(smem_u32(tempty), leader) : smem_u32(tempty);
         bool ok = true;
         uint32_t set = 0, set_phase = 0;
         int l0 = 0, c0 = 0;
@@ -801,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     s = __uint_as_float(word);
                 }
-                if (!wait_bounded(&tfull[set], set_phase, p.limit_ns, abort)) {
+                if (!wait_bounded(tfull_at + set * 8, set_phase, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     ok = false;
                     break;
@@ -818,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            arrive_leader<PAIR>(&tempty[set], leader);
+                            arrive_leader<PAIR>(tempty_at + set * 8);
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
