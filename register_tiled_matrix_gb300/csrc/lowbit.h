@@ -66,6 +66,9 @@ cudaError_t launch_w4_tc(const W4Launch &L, int64_t lda, const DeviceContext &d,
                          cudaStream_t stream);
 cudaError_t launch_q8t_tc(const Q8tLaunch &L, int64_t ldy, const DeviceContext &d, bool mute,
                           cudaStream_t stream);
+// w4_rows.cu: few rows of A (M <= kW4RowsMax), any alignment.
+constexpr int kW4RowsMax = 16;
+cudaError_t launch_w4_rows(const W4Launch &L, int sms, cudaStream_t stream);
 // lowbit_simt.cu: any alignment.
 cudaError_t launch_w4_simt(const W4Launch &L, cudaStream_t stream);
 cudaError_t launch_q8t_simt(const Q8tLaunch &L, cudaStream_t stream);

@@ -201,6 +201,8 @@ int w4_product(int64_t M, int64_t N, int64_t K, int f16, const uint16_t *A, cons
     L.scales = scales;
     L.zeros = zeros;
     L.C = C;
+    if (M <= rtm::kW4RowsMax)
+        return finish(rtm::launch_w4_rows(L, d.sms, s));
     if (d.encode_tiled && rows16(A, K))
         return finish(rtm::launch_w4_tc(L, K, d, false, s));
     const int64_t need = padded_bytes(M, K);
@@ -344,7 +346,7 @@ int64_t gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (!size_ok(M, K) || !size_ok(K, N) || !size_ok(M, N))
         return GEMM_ERR_INVALID_ARG;
-    return N > 0 ? padded_bytes(M, K) : 0;
+    return N > 0 && M > rtm::kW4RowsMax ? padded_bytes(M, K) : 0;
 }
 
 int64_t gemm_q8t_workspace_bytes(int64_t M, int64_t N, int64_t K)

@@ -210,36 +210,6 @@ __device__ __forceinline__ void fma2(float &a0, float &a1, float s, float v0, fl
         : "f"(v0), "f"(v1), "f"(s));
 }
 
-template <bool F16>
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    if constexpr (F16)
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    else
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// 2^7 in bf16 and 2^10 in fp16 have ulp 1: a small integer in the low mantissa
-// bits adds itself, exactly.
-template <bool F16>
-__device__ __forceinline__ constexpr uint32_t magic2()
-{
-    return F16 ? 0x64006400u : 0x43004300u;
-}
-
-// Eight 4-bit codes minus their zero point, in order; zz = magic + z, twice.
-template <bool F16>
-__device__ __forceinline__ uint4 w4_values(uint32_t word, uint32_t zz)
-{
-    uint32_t v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        v[j] = sub2<F16>(((word >> (4 * j)) & 0x000f000fu) | magic2<F16>(), zz);
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 // Four signed bytes, in order. fp16: 1024 + (q + 128) - 1152. bf16 has seven
 // mantissa bits, so the sign bit goes to the subtrahend: with u = q mod 128 and
 // the sign bit on the exponent's lowest bit, (128 + u) - (sign ? 256 : 128).
@@ -257,23 +227,6 @@ __device__ __forceinline__ uint2 q8_values(uint32_t word)
                           sub2<false>(__byte_perm(u, 0x43434343u, 0x4342),
                                       __byte_perm(s, 0x43434343u, 0x4342)));
     }
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)

@@ -37,4 +37,51 @@ __device__ __forceinline__ uint32_t pack2_f32(float lo, float hi)
 // consecutive pair 2 j, 2 j + 1.
 __host__ __device__ constexpr int w4_shift(int i) { return 4 * (i >> 1) + 16 * (i & 1); }
 
+template <bool F16>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    if constexpr (F16)
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// 2^7 in bf16 and 2^10 in fp16 have ulp 1: a small integer in the low mantissa
+// bits adds itself, exactly.
+template <bool F16>
+__device__ __forceinline__ constexpr uint32_t magic2()
+{
+    return F16 ? 0x64006400u : 0x43004300u;
+}
+
+// Eight 4-bit codes minus their zero point, in order; zz = magic + z, twice.
+template <bool F16>
+__device__ __forceinline__ uint4 w4_values(uint32_t word, uint32_t zz)
+{
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        v[j] = sub2<F16>(((word >> (4 * j)) & 0x000f000fu) | magic2<F16>(), zz);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 } // namespace rtm

@@ -28,7 +28,7 @@ SOURCES = ["api.cu", "sgemm_simt.cu", "sgemm_ladder.cu", "gemm_tc.cu", "gemm_tc2
            "gemm_tc_t.cu", "sgemm_short.cu", "fp32_peak.cu", "sgemm_tma.cu",
            "sgemm_tma_rect.cu", "gemm_tc_any_t.cu",
            "lowbit_api.cu", "lowbit_quant.cu", "lowbit_simt.cu",
-           "lowbit_tc.cu"]
+           "lowbit_tc.cu", "w4_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "-Xptxas", "-v",
