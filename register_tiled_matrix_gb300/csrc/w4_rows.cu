@@ -50,181 +50,213 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight consecutive values of a row of A from k, zeros from `left` values on.
-// V: values per load (8, 2 or 1), the most that rows of K values allow.
+// Eight consecutive values of a row of A to shared memory, zeros from `left`
+// values on. V: values a copy moves, the most that rows of K values allow (8, 2);
+// single values (1) have no asynchronous copy and go through registers.
 template <int V>
-__device__ __forceinline__ uint4 load_values(const uint16_t *p, int left)
+__device__ __forceinline__ void copy_values(uint32_t dst, const uint16_t *p, int left)
 {
-    if (left <= 0)
-        return make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (V == 8)  // K % 8 == 0: all or none
-        return __ldg(reinterpret_cast<const uint4 *>(p));
-    uint32_t w[4] = {};
+    if constexpr (V == 8) {  // K % 8 == 0: all or none
+        cp_async_16(dst, left > 0 ? p : nullptr, left > 0 ? 16u : 0u);
+    } else if constexpr (V == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (V == 2) {
-            w[i] = 2 * i < left ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
-        } else {
+        for (int i = 0; i < 4; ++i)
+            cp_async_4(dst + 4 * i, 2 * i < left ? p + 2 * i : nullptr, 2 * i < left ? 4u : 0u);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             const uint32_t lo = 2 * i < left ? __ldg(p + 2 * i) : 0;
             const uint32_t hi = 2 * i + 1 < left ? __ldg(p + 2 * i + 1) : 0;
             w[i] = lo | hi << 16;
         }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3])
+                     : "memory");
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A warp's ring in shared memory: per block of k and 16 columns the lanes' codes
-// (16 bytes of rows r and r + 8) and the words that hold their scales and zero
-// points. Each lane copies and reads its own bytes.
-template <int T>
-struct Ring {
-    static constexpr int DEPTH = T == 1 ? 6 : 4;
-    static constexpr uint32_t META = T * 2 * 512;             // codes come first
-    static constexpr uint32_t SLOT = META + T * 2 * 2 * 128;  // 1.5 KB for each 16 columns
-    static constexpr uint32_t BYTES = kWarps * DEPTH * SLOT;
-};
+constexpr int DEPTH = 4;  // blocks in a warp's ring, and the unrolling of its loop
 
-template <bool F16, int T, int NB, int V>
-__global__ void __launch_bounds__(kThreads, T * NB == 1 ? 3 : T * NB == 4 && V < 8 ? 1 : 2)
-    w4_rows_kernel(const W4Launch p, int gs)
+// Shared memory of a warp: the scale and zero point of four groups of each
+// column, ready for use, and a ring of blocks. A block holds 16 bytes a lane for
+// rows r and r + 8 of each 16 columns, then its 128 values of the rows of A (256
+// bytes each; odd rows with their 64-byte halves exchanged, so that two rows'
+// quarters fall on different banks). Each lane copies and reads its own bytes.
+template <int T>
+struct Warp {
+    static constexpr uint32_t META = 4 * T * 16 * 8;
+    static constexpr uint32_t CODES = T * 1024;
+};
+inline __host__ __device__ constexpr uint32_t slot_bytes(int t, int rows) { return t * 1024 + rows * 256; }
+inline __host__ __device__ constexpr uint32_t warp_bytes(int t, int rows)
 {
-    using R = Ring<T>;
-    extern __shared__ __align__(16) uint8_t ring[];
+    return 4 * t * 16 * 8 + DEPTH * slot_bytes(t, rows);
+}
+
+// GS: log2 of the group. V: see copy_values.
+template <bool F16, int T, int NB, int V, int GS>
+__global__ void __launch_bounds__(kThreads, NB == 1 ? (T == 1 ? 3 : 2) : 1)
+    w4_rows_kernel(const W4Launch p)
+{
+    constexpr int GROUP = 1 << GS;
+    constexpr int GPB = kW4Block / GROUP;  // groups of a block
+    constexpr int SPAN = 4 / GPB;          // blocks of this warp that four groups cover
+    using S = Warp<T>;
+    extern __shared__ __align__(256) uint8_t shared[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
     const int n0 = blockIdx.x * (16 * T), m0 = blockIdx.y * (8 * NB);
     const int blocks = (p.K + kW4Block - 1) / kW4Block;
-    const int G = (p.K + p.group - 1) >> gs;
-    const int per_block = 7 - gs;  // log2 of the groups of a block
-    const uint32_t mine = smem_u32(ring) + warp * R::DEPTH * R::SLOT;
+    const int G = (p.K + GROUP - 1) / GROUP;
+    const int xrows = min(p.M, 8 * NB);
+    const uint32_t slot = slot_bytes(T, xrows);
+    const uint32_t mine = smem_u32(shared) + warp * warp_bytes(T, xrows);
+    const uint32_t meta = mine + r * 8;
+    const uint32_t ring = mine + S::META;
+    const uint32_t xring = ring + S::CODES + r * 256 + ((c * 16) ^ ((r & 1) * 64));
     const int64_t pitch = w4_row_bytes(p.K);
     // Columns past the end read the last one's bytes; they are not stored.
-    const uint8_t *row[T][2];
-    uint32_t col[T][2];
+    const uint8_t *row[T][2];  // of the next block to copy
+    int col[T][2];
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            col[t][h] = (uint32_t)min(n0 + 16 * t + 8 * h + r, p.N - 1);
-            row[t][h] = p.codes + col[t][h] * pitch + c * 16;
+            col[t][h] = min(n0 + 16 * t + 8 * h + r, p.N - 1);
+            row[t][h] = p.codes + col[t][h] * pitch + (int64_t)warp * kW4BlockBytes + c * 16;
         }
-    // Each of a row's four lanes holds one group's scale and zero point of a
-    // block (of 1, 2 or 4 groups); the others get it by a lane exchange. A scale
-    // (2 bytes) and a zero point (1 byte) are copied with the aligned word around them.
-    const int own = c & ((1 << per_block) - 1);
-    auto fetch = [&](int b, int slot) {
+    // Rows of A: lanes of rows past M (in this block of rows) copy and read nothing.
+    const uint16_t *a[NB];
+    bool in[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int m = m0 + 8 * j + r;
+        in[j] = 8 * j + r < xrows && m < p.M;
+        a[j] = p.A + (int64_t)m * p.K + 8 * c + (int64_t)warp * kW4Block;
+    }
+    auto fetch = [&](int b, int at) {
         if (b < blocks) {
-            const uint32_t dst = mine + slot * R::SLOT;
-            const int64_t at = (int64_t)min((b << per_block) + own, G - 1) * p.N;
 #pragma unroll
             for (int t = 0; t < T; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int i = 2 * t + h;
-                    cp_async_16_full(dst + i * 512 + lane * 16, row[t][h] + (int64_t)b * kW4BlockBytes);
-                    const uintptr_t sp = reinterpret_cast<uintptr_t>(p.scales + at + col[t][h]);
-                    cp_async_4_full(dst + R::META + i * 256 + lane * 4,
-                                    reinterpret_cast<const void *>(sp & ~uintptr_t(3)));
-                    if (p.zeros) {
-                        const uintptr_t zp = reinterpret_cast<uintptr_t>(p.zeros + at + col[t][h]);
-                        cp_async_4_full(dst + R::META + i * 256 + 128 + lane * 4,
-                                        reinterpret_cast<const void *>(zp & ~uintptr_t(3)));
-                    }
+                    cp_async_16_full(ring + at * slot + (2 * t + h) * 512 + lane * 16, row[t][h]);
+                    row[t][h] += kWarps * kW4BlockBytes;
                 }
+            const int left = p.K - b * kW4Block - 8 * c;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                if (in[j])
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t dst = (xring + at * slot + j * 2048) ^ (w * 64);
+                        copy_values<V>(dst, a[j] + 32 * w, left - 32 * w);
+                    }
+                a[j] += kWarps * kW4Block;
+            }
         }
         cp_async_commit();
     };
-    uint4 x[NB][4];  // A at the block's four words; each is loaded a block ahead of its use
-    auto load_x = [&](int b, int w) {
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            const int m = m0 + 8 * j + r, k = b * kW4Block + 32 * w + 8 * c;
-            x[j][w] = load_values<V>(p.A + (int64_t)m * p.K + k, m < p.M ? p.K - k : 0);
-        }
-    };
-    float total[T][NB][4] = {}, sum[T][NB][4] = {};
-    int b = warp, slot = 0;
-#pragma unroll 1
-    for (int a = 0; a < R::DEPTH - 1; ++a)
-        fetch(b + a * kWarps, a);
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-        load_x(b, w);
-#pragma unroll 1
-    for (; b < blocks; b += kWarps) {
-        cp_async_wait<R::DEPTH - 2>();
-        const uint32_t src = mine + slot * R::SLOT;
-        uint4 q[T][2];
-        uint32_t scale[T][2], zero[T][2], zz[T][2];
-        const int gl = (b << per_block) + own;
-        const int64_t at = (int64_t)min(gl, G - 1) * p.N;
+    // Lane c of a row's four loads the scale and zero point of the c-th of the four
+    // groups that begin with block b, one span ahead of their use.
+    uint16_t scale[T][2];
+    uint8_t zero[T][2];
+    auto load_meta = [&](int b) {
+        const int g = (b + c / GPB * kWarps) * GPB + c % GPB;
+        const int64_t at = (int64_t)g * p.N;
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int i = 2 * t + h;
-                q[t][h] = lds128(src + i * 512 + lane * 16);
-                const uint32_t sp =
-                    (uint32_t)reinterpret_cast<uintptr_t>(p.scales) + 2 * (uint32_t)(at + col[t][h]);
-                scale[t][h] = lds32(src + R::META + i * 256 + lane * 4) >> (8 * (sp & 2));
-                if (gl >= G)
-                    scale[t][h] = 0;  // codes of k >= K: sums of zeros
-                zero[t][h] = 8;
-                if (p.zeros) {
-                    const uint32_t zp =
-                        (uint32_t)reinterpret_cast<uintptr_t>(p.zeros) + (uint32_t)(at + col[t][h]);
-                    zero[t][h] =
-                        (lds32(src + R::META + i * 256 + 128 + lane * 4) >> (8 * (zp & 3))) & 15u;
-                }
+                // codes of k >= K: sums of zeros
+                scale[t][h] = g < G ? __ldg(p.scales + at + col[t][h]) : (uint16_t)0;
+                zero[t][h] = p.zeros && g < G ? __ldg(p.zeros + at + col[t][h]) : (uint8_t)8;
             }
+    };
+    auto store_meta = [&]() {
+        __syncwarp();  // the last span's values have been read
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if ((w * 32 & (p.group - 1)) == 0)
+        for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int t = 0; t < T; ++t)
+            for (int h = 0; h < 2; ++h)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
+                                 meta + (c * T * 16 + 16 * t + 8 * h) * 8),
+                             "r"(__float_as_uint(to_f32<F16>(scale[t][h]))),
+                             "r"(magic2<F16>() | (zero[t][h] & 15u) * 0x00010001u)
+                             : "memory");
+        __syncwarp();
+    };
+    float total[T][NB][4] = {};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        zz[t][h] = magic2<F16>() |
-                                   __shfl_sync(0xffffffffu, zero[t][h],
-                                               (lane & 28) | ((w * 32) >> gs)) * 0x00010001u;
+    for (int i = 0; i < DEPTH - 1; ++i)
+        fetch(warp + i * kWarps, i);
+    load_meta(warp);
+#pragma unroll 1
+    for (int b0 = warp; b0 < blocks; b0 += DEPTH * kWarps) {
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const uint4 &qa = q[t][0], &qb = q[t][1];
-                const uint4 va = w4_values<F16>(w == 0 ? qa.x : w == 1 ? qa.y : w == 2 ? qa.z : qa.w,
-                                                zz[t][0]);
-                const uint4 vb = w4_values<F16>(w == 0 ? qb.x : w == 1 ? qb.y : w == 2 ? qb.z : qb.w,
-                                                zz[t][1]);
+        for (int i = 0; i < DEPTH; ++i) {
+            const int b = b0 + i * kWarps;
+            if (b >= blocks)
+                break;
+            if (i % SPAN == 0) {
+                store_meta();
+                load_meta(b + SPAN * kWarps);
+            }
+            cp_async_wait<DEPTH - 2>();
+            uint4 q[T][2];
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    q[t][h] = lds128(ring + i * slot + (2 * t + h) * 512 + lane * 16);
+            float sum[T][NB][4], s[T][2];
+            uint32_t zz[T][2];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const bool begin = w * 32 % GROUP == 0, end = (w + 1) * 32 % GROUP == 0;
+                const int group = i % SPAN * GPB + w * 32 / GROUP;  // of the span's four
+                uint4 x[NB];
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    mma16816<F16>(sum[t][j], va.x, vb.x, va.y, vb.y, x[j][w].x, x[j][w].y);
-                    mma16816<F16>(sum[t][j], va.z, vb.z, va.w, vb.w, x[j][w].z, x[j][w].w);
+                    x[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (in[j])
+                        x[j] = lds128((xring + i * slot + j * 2048) ^ (w * 64));
                 }
-            }
-            load_x(b + kWarps, w);
-            if (((w + 1) * 32 & (p.group - 1)) == 0)
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
-                    float s[2];
+                    if (begin)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        s[h] = to_f32<F16>((uint16_t)__shfl_sync(0xffffffffu, scale[t][h],
-                                                                 (lane & 28) | ((w * 32) >> gs)));
+                        for (int h = 0; h < 2; ++h)
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                         : "=f"(s[t][h]), "=r"(zz[t][h])
+                                         : "r"(meta + (group * T * 16 + 16 * t + 8 * h) * 8)
+                                         : "memory");
+                    const uint4 &qa = q[t][0], &qb = q[t][1];
+                    const uint4 va = w4_values<F16>(
+                        w == 0 ? qa.x : w == 1 ? qa.y : w == 2 ? qa.z : qa.w, zz[t][0]);
+                    const uint4 vb = w4_values<F16>(
+                        w == 0 ? qb.x : w == 1 ? qb.y : w == 2 ? qb.z : qb.w, zz[t][1]);
 #pragma unroll
-                    for (int j = 0; j < NB; ++j)
+                    for (int j = 0; j < NB; ++j) {
+                        if (begin)
+                            sum[t][j][0] = sum[t][j][1] = sum[t][j][2] = sum[t][j][3] = 0.f;
+                        mma16816<F16>(sum[t][j], va.x, vb.x, va.y, vb.y, x[j].x, x[j].y);
+                        mma16816<F16>(sum[t][j], va.z, vb.z, va.w, vb.w, x[j].z, x[j].w);
+                        if (end)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            total[t][j][e] = fmaf(s[e >> 1], sum[t][j][e], total[t][j][e]);
-                            sum[t][j][e] = 0.f;
-                        }
+                            for (int e = 0; e < 4; ++e)
+                                total[t][j][e] = fmaf(s[t][e >> 1], sum[t][j][e], total[t][j][e]);
+                    }
                 }
+            }
+            // Into the slot of the block before this one.
+            fetch(b + (DEPTH - 1) * kWarps, (i + DEPTH - 1) % DEPTH);
         }
-        // The slot read in the block before this one (its words are long used).
-        fetch(b + (R::DEPTH - 1) * kWarps, slot == 0 ? R::DEPTH - 1 : slot - 1);
-        slot = slot + 1 == R::DEPTH ? 0 : slot + 1;
     }
     cp_async_wait<0>();
     __syncthreads();
-    float(*red)[16 * T][8 * NB + 1] = reinterpret_cast<float(*)[16 * T][8 * NB + 1]>(ring);
+    float(*red)[16 * T][8 * NB + 1] = reinterpret_cast<float(*)[16 * T][8 * NB + 1]>(shared);
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -244,45 +276,48 @@ __global__ void __launch_bounds__(kThreads, T * NB == 1 ? 3 : T * NB == 4 && V <
     }
 }
 
-template <bool F16, int T, int NB, int V>
-static cudaError_t launch_kernel(const W4Launch &L, dim3 grid, int gs, cudaStream_t stream)
+template <bool F16, int T, int NB, int V, int GS>
+static cudaError_t launch_kernel(const W4Launch &L, cudaStream_t stream)
 {
-    using R = Ring<T>;
-    static_assert(kWarps * 16 * T * (8 * NB + 1) * 4 <= R::BYTES, "the totals fit the ring");
-    auto kernel = w4_rows_kernel<F16, T, NB, V>;
+    static_assert(kWarps * 16 * T * (8 * NB + 1) * 4 <= kWarps * warp_bytes(T, 1), "the totals fit");
+    auto kernel = w4_rows_kernel<F16, T, NB, V, GS>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = set_smem_limit_once(kernel, (int)R::BYTES, done, 100);
+    const cudaError_t e =
+        set_smem_limit_once(kernel, kWarps * (int)warp_bytes(T, 8 * NB), done, 100);
     if (e != cudaSuccess)
         return e;
-    kernel<<<grid, kThreads, R::BYTES, stream>>>(L, gs);
+    const dim3 grid((unsigned)((L.N + 16 * T - 1) / (16 * T)),
+                    (unsigned)((L.M + 8 * NB - 1) / (8 * NB)));
+    const int rows = L.M < 8 * NB ? L.M : 8 * NB;
+    kernel<<<grid, kThreads, kWarps * warp_bytes(T, rows), stream>>>(L);
     return cudaGetLastError();
 }
 
+template <bool F16, int T, int NB, int V>
+static cudaError_t launch_g(const W4Launch &L, cudaStream_t stream)
+{
+    return L.group == 32   ? launch_kernel<F16, T, NB, V, 5>(L, stream)
+           : L.group == 64 ? launch_kernel<F16, T, NB, V, 6>(L, stream)
+                           : launch_kernel<F16, T, NB, V, 7>(L, stream);
+}
+
 template <bool F16, int T, int NB>
-static cudaError_t launch_v(const W4Launch &L, dim3 grid, int gs, cudaStream_t stream)
+static cudaError_t launch_v(const W4Launch &L, cudaStream_t stream)
 {
     const uintptr_t a = reinterpret_cast<uintptr_t>(L.A);
-    if (L.K % 8 == 0 && a % 16 == 0)
-        return launch_kernel<F16, T, NB, 8>(L, grid, gs, stream);
-    if (L.K % 2 == 0 && a % 4 == 0)
-        return launch_kernel<F16, T, NB, 2>(L, grid, gs, stream);
-    return launch_kernel<F16, T, NB, 1>(L, grid, gs, stream);
+    return L.K % 8 == 0 && a % 16 == 0  ? launch_g<F16, T, NB, 8>(L, stream)
+           : L.K % 2 == 0 && a % 4 == 0 ? launch_g<F16, T, NB, 2>(L, stream)
+                                        : launch_g<F16, T, NB, 1>(L, stream);
 }
 
 template <bool F16>
 static cudaError_t launch_f(const W4Launch &L, int sms, cudaStream_t stream)
 {
-    const int gs = L.group == 32 ? 5 : L.group == 64 ? 6 : 7;
-    const bool two = L.M > 8;
-    const int nb = two ? 2 : 1;
+    if (L.M > 8)
+        return launch_v<F16, 2, 2>(L, stream);
     // 32 columns a block while that still gives every SM two blocks.
-    const int t = (L.N + 31) / 32 >= 2 * sms ? 2 : 1;
-    const dim3 grid((unsigned)((L.N + 16 * t - 1) / (16 * t)), (unsigned)((L.M + 8 * nb - 1) / (8 * nb)));
-    if (t == 2)
-        return two ? launch_v<F16, 2, 2>(L, grid, gs, stream)
-                   : launch_v<F16, 2, 1>(L, grid, gs, stream);
-    return two ? launch_v<F16, 1, 2>(L, grid, gs, stream)
-               : launch_v<F16, 1, 1>(L, grid, gs, stream);
+    return (L.N + 31) / 32 >= 2 * sms ? launch_v<F16, 2, 1>(L, stream)
+                                      : launch_v<F16, 1, 1>(L, stream);
 }
 
 } // namespace w4r
