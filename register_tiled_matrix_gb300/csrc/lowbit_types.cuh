@@ -56,6 +56,15 @@ __device__ __forceinline__ constexpr uint32_t magic2()
     return F16 ? 0x64006400u : 0x43004300u;
 }
 
+// (a & mask) | bits in one instruction: written out because the compiler makes two
+// of it when mask and bits are both constants.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+    return d;
+}
+
 // Eight 4-bit codes minus their zero point, in order; zz = magic + z, twice.
 template <bool F16>
 __device__ __forceinline__ uint4 w4_values(uint32_t word, uint32_t zz)
@@ -63,7 +72,7 @@ __device__ __forceinline__ uint4 w4_values(uint32_t word, uint32_t zz)
     uint32_t v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        v[j] = sub2<F16>(((word >> (4 * j)) & 0x000f000fu) | magic2<F16>(), zz);
+        v[j] = sub2<F16>(and_or(word >> (4 * j), 0x000f000fu, magic2<F16>()), zz);
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 

@@ -50,6 +50,35 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Eight 4-bit codes minus their zero point, in order. nz: -(magic + z), twice.
+// fp16 has mantissa bits to spare: a code four bits up adds 16 times itself to
+// 1024, and one fused multiply-add takes it down and subtracts 64 + z (nz16),
+// exactly, which saves two of the three shifts.
+template <bool F16>
+__device__ __forceinline__ uint4 values_of(uint32_t word, uint32_t nz, uint32_t nz16)
+{
+    auto low = [&](uint32_t w) {
+        const uint32_t v = and_or(w, 0x000f000fu, magic2<F16>());
+        uint32_t d;
+        if constexpr (F16)
+            asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(nz));
+        else
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0x3f803f80u), "r"(nz));
+        return d;
+    };
+    auto up = [&](uint32_t w) {
+        uint32_t d;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+            : "=r"(d)
+            : "r"(and_or(w, 0x00f000f0u, 0x64006400u)), "r"(0x2c002c00u), "r"(nz16));
+        return d;
+    };
+    if constexpr (F16)
+        return make_uint4(low(word), up(word), low(word >> 8), up(word >> 8));
+    else
+        return make_uint4(low(word), low(word >> 4), low(word >> 8), low(word >> 12));
+}
+
 // Eight consecutive values of a row of A to shared memory, zeros from `left`
 // values on. V: values a copy moves, the most that rows of K values allow (8, 2);
 // single values (1) have no asynchronous copy and go through registers.
@@ -113,11 +142,13 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? (T == 1 ? 3 : 2) : 1)
     const uint32_t slot = slot_bytes(T, xrows);
     const uint32_t mine = smem_u32(shared) + warp * warp_bytes(T, xrows);
     const uint32_t meta = mine + r * 8;
-    const uint32_t ring = mine + S::META;
-    const uint32_t xring = ring + S::CODES + r * 256 + ((c * 16) ^ ((r & 1) * 64));
+    const uint32_t ring = mine + S::META, codes = ring + lane * 16;
+    // A's values for words 0 and 2 are at xring, + 128; for words 1 and 3 at xother, + 128.
+    const uint32_t xring = ring + S::CODES + r * 256 + c * 16 + (r & 1) * 64;
+    const uint32_t xother = xring ^ 64u;
     const int64_t pitch = w4_row_bytes(p.K);
     // Columns past the end read the last one's bytes; they are not stored.
-    const uint8_t *row[T][2];  // of the next block to copy
+    const uint8_t *row[T][2];  // at this warp's first block of the loop's round
     int col[T][2];
 #pragma unroll
     for (int t = 0; t < T; ++t)
@@ -135,26 +166,30 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? (T == 1 ? 3 : 2) : 1)
         in[j] = 8 * j + r < xrows && m < p.M;
         a[j] = p.A + (int64_t)m * p.K + 8 * c + (int64_t)warp * kW4Block;
     }
-    auto fetch = [&](int b, int at) {
+    // Copies this warp's block `ahead` of the round (block b) to slot `at`.
+    auto fetch = [&](int b, int ahead, int at) {
         if (b < blocks) {
 #pragma unroll
             for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    cp_async_16_full(ring + at * slot + (2 * t + h) * 512 + lane * 16, row[t][h]);
-                    row[t][h] += kWarps * kW4BlockBytes;
-                }
+                for (int h = 0; h < 2; ++h)
+                    cp_async_16_full(codes + at * slot + (2 * t + h) * 512,
+                                     row[t][h] + ahead * (kWarps * kW4BlockBytes));
             const int left = p.K - b * kW4Block - 8 * c;
+            const bool whole = (b + 1) * (int64_t)kW4Block <= p.K;
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
+            for (int j = 0; j < NB; ++j)
                 if (in[j])
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const uint32_t dst = (xring + at * slot + j * 2048) ^ (w * 64);
-                        copy_values<V>(dst, a[j] + 32 * w, left - 32 * w);
+                        const uint32_t dst =
+                            (w & 1 ? xother : xring) + at * slot + j * 2048 + (w & 2) * 64;
+                        const uint16_t *src = a[j] + ahead * (kWarps * kW4Block) + 32 * w;
+                        if (V == 8 && whole)
+                            cp_async_16_full(dst, src);
+                        else
+                            copy_values<V>(dst, src, left - 32 * w);
                     }
-                a[j] += kWarps * kW4Block;
-            }
         }
         cp_async_commit();
     };
@@ -183,14 +218,20 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? (T == 1 ? 3 : 2) : 1)
                 asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
                                  meta + (c * T * 16 + 16 * t + 8 * h) * 8),
                              "r"(__float_as_uint(to_f32<F16>(scale[t][h]))),
-                             "r"(magic2<F16>() | (zero[t][h] & 15u) * 0x00010001u)
+                             "r"(magic2<F16>() | 0x80008000u | (zero[t][h] & 15u) * 0x00010001u)
                              : "memory");
         __syncwarp();
     };
+    uint4 x[NB][4];  // lanes of rows past M keep zeros
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            x[j][w] = make_uint4(0u, 0u, 0u, 0u);
     float total[T][NB][4] = {};
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i)
-        fetch(warp + i * kWarps, i);
+        fetch(warp + i * kWarps, i, i);
     load_meta(warp);
 #pragma unroll 1
     for (int b0 = warp; b0 < blocks; b0 += DEPTH * kWarps) {
@@ -209,40 +250,39 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? (T == 1 ? 3 : 2) : 1)
             for (int t = 0; t < T; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    q[t][h] = lds128(ring + i * slot + (2 * t + h) * 512 + lane * 16);
+                    q[t][h] = lds128(codes + i * slot + (2 * t + h) * 512);
             float sum[T][NB][4], s[T][2];
-            uint32_t zz[T][2];
+            uint32_t nz[T][2], nz16[T][2];  // -(magic + z); fp16: -(64 + z)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const bool begin = w * 32 % GROUP == 0, end = (w + 1) * 32 % GROUP == 0;
                 const int group = i % SPAN * GPB + w * 32 / GROUP;  // of the span's four
-                uint4 x[NB];
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    x[j] = make_uint4(0u, 0u, 0u, 0u);
+                for (int j = 0; j < NB; ++j)
                     if (in[j])
-                        x[j] = lds128((xring + i * slot + j * 2048) ^ (w * 64));
-                }
+                        x[j][w] = lds128((w & 1 ? xother : xring) + i * slot + j * 2048 + (w & 2) * 64);
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
                     if (begin)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int h = 0; h < 2; ++h) {
                             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                         : "=f"(s[t][h]), "=r"(zz[t][h])
+                                         : "=f"(s[t][h]), "=r"(nz[t][h])
                                          : "r"(meta + (group * T * 16 + 16 * t + 8 * h) * 8)
                                          : "memory");
+                            nz16[t][h] = F16 ? (nz[t][h] << 4 & 0x00f000f0u) | 0xd400d400u : 0u;
+                        }
                     const uint4 &qa = q[t][0], &qb = q[t][1];
-                    const uint4 va = w4_values<F16>(
-                        w == 0 ? qa.x : w == 1 ? qa.y : w == 2 ? qa.z : qa.w, zz[t][0]);
-                    const uint4 vb = w4_values<F16>(
-                        w == 0 ? qb.x : w == 1 ? qb.y : w == 2 ? qb.z : qb.w, zz[t][1]);
+                    const uint4 va = values_of<F16>(
+                        w == 0 ? qa.x : w == 1 ? qa.y : w == 2 ? qa.z : qa.w, nz[t][0], nz16[t][0]);
+                    const uint4 vb = values_of<F16>(
+                        w == 0 ? qb.x : w == 1 ? qb.y : w == 2 ? qb.z : qb.w, nz[t][1], nz16[t][1]);
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
                         if (begin)
                             sum[t][j][0] = sum[t][j][1] = sum[t][j][2] = sum[t][j][3] = 0.f;
-                        mma16816<F16>(sum[t][j], va.x, vb.x, va.y, vb.y, x[j].x, x[j].y);
-                        mma16816<F16>(sum[t][j], va.z, vb.z, va.w, vb.w, x[j].z, x[j].w);
+                        mma16816<F16>(sum[t][j], va.x, vb.x, va.y, vb.y, x[j][w].x, x[j][w].y);
+                        mma16816<F16>(sum[t][j], va.z, vb.z, va.w, vb.w, x[j][w].z, x[j][w].w);
                         if (end)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -251,8 +291,16 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? (T == 1 ? 3 : 2) : 1)
                 }
             }
             // Into the slot of the block before this one.
-            fetch(b + (DEPTH - 1) * kWarps, (i + DEPTH - 1) % DEPTH);
+            fetch(b + (DEPTH - 1) * kWarps, i + DEPTH - 1, (i + DEPTH - 1) % DEPTH);
         }
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                row[t][h] += DEPTH * kWarps * kW4BlockBytes;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            a[j] += DEPTH * kWarps * kW4Block;
     }
     cp_async_wait<0>();
     __syncthreads();
@@ -316,7 +364,7 @@ static cudaError_t launch_f(const W4Launch &L, int sms, cudaStream_t stream)
     if (L.M > 8)
         return launch_v<F16, 2, 2>(L, stream);
     // 32 columns a block while that still gives every SM two blocks.
-    return (L.N + 31) / 32 >= 2 * sms ? launch_v<F16, 2, 1>(L, stream)
+    return (L.N + 31) / 32 >= 2 * sms && L.M <= 4 ? launch_v<F16, 2, 1>(L, stream)
                                       : launch_v<F16, 1, 1>(L, stream);
 }
 
