@@ -344,6 +344,9 @@ def _type_name(dtype: torch.dtype) -> str:
 
 
 def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device=None) -> None:
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and (t.device == device if device is not None else t.is_cuda) and t.is_cuda):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -363,12 +366,31 @@ def _matrix(name: str, t: torch.Tensor) -> Tuple[int, int]:
     return t.shape
 
 
-def _empty(shape, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """Memory of the stream the call runs on, so that it is reused in that stream's order."""
+def _empty(like: torch.Tensor, shape, dtype: torch.dtype,
+           stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory on like's device, of the stream the call runs on, so that it is reused in
+    that stream's order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _call(entry: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> None:
+    """entry(*args, stream) with `device` current (switched to only when it is not)."""
+    f = getattr(_lib or load_library(), entry)
+    if device == torch.cuda.current_device():
+        status = f(*args, _stream_handle(stream, device))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _stream_handle(stream, device))
+    if status:
+        _check(status)
+
+
+def _plain(t, dtype: torch.dtype, device: int) -> bool:
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device
+            and t.is_contiguous())
 
 
 def _w4_check(codes, scales, zeros, K: int, group: int, device) -> int:
@@ -395,14 +417,12 @@ def gemm_w4_quantize(W: torch.Tensor, group: int = 128, zeros: bool = True,
     name = _type_name(W.dtype)
     if group not in W4_GROUPS:
         raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
-    with _on_device(W):
-        codes = _empty((N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), torch.uint8, W.device, stream)
-        meta = ((K + group - 1) // group, N)
-        scales = _empty(meta, W.dtype, W.device, stream)
-        zp = _empty(meta, torch.uint8, W.device, stream) if zeros else None
-        _check(getattr(_library(), f"gemm_{name}_w4_quantize")(
-            K, N, group, W.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-            zp.data_ptr() if zeros else 0, _stream_handle(stream, W.get_device())))
+    codes = _empty(W, (N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), torch.uint8, stream)
+    meta = ((K + group - 1) // group, N)
+    scales = _empty(W, meta, W.dtype, stream)
+    zp = _empty(W, meta, torch.uint8, stream) if zeros else None
+    _call(f"gemm_{name}_w4_quantize", W.get_device(), stream, K, N, group, W.data_ptr(),
+          codes.data_ptr(), scales.data_ptr(), zp.data_ptr() if zeros else 0)
     return codes, scales, zp
 
 
@@ -411,10 +431,8 @@ def gemm_w4_pack(q: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) ->
     quantised elsewhere)."""
     K, N = _matrix("q", q)
     _need("q", q, torch.uint8, (K, N))
-    with _on_device(q):
-        codes = _empty((N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), torch.uint8, q.device, stream)
-        _check(_library().gemm_w4_pack(K, N, q.data_ptr(), codes.data_ptr(),
-                                       _stream_handle(stream, q.get_device())))
+    codes = _empty(q, (N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), torch.uint8, stream)
+    _call("gemm_w4_pack", q.get_device(), stream, K, N, q.data_ptr(), codes.data_ptr())
     return codes
 
 
@@ -423,50 +441,58 @@ def gemm_w4_dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: Optiona
                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The K x N weight (q - z) * s in the scales' type."""
     N = _w4_check(codes, scales, zeros, K, group, scales.device)
-    with _on_device(codes):
-        if out is None:
-            out = _empty((K, N), scales.dtype, codes.device, stream)
-        else:
-            _need("out", out, scales.dtype, (K, N), codes.device)
-        _check(getattr(_library(), f"gemm_{_type_name(scales.dtype)}_w4_dequantize")(
-            K, N, group, codes.data_ptr(), scales.data_ptr(),
-            0 if zeros is None else zeros.data_ptr(), out.data_ptr(),
-            _stream_handle(stream, codes.get_device())))
+    if out is None:
+        out = _empty(codes, (K, N), scales.dtype, stream)
+    else:
+        _need("out", out, scales.dtype, (K, N), codes.device)
+    _call(f"gemm_{_type_name(scales.dtype)}_w4_dequantize", codes.get_device(), stream, K, N, group,
+          codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(),
+          out.data_ptr())
     return out
 
 
-def _workspace(workspace: Optional[torch.Tensor], rows16: bool, nbytes: Callable[..., int], size,
-               device, stream) -> Tuple[int, int, Optional[torch.Tensor]]:
+def _workspace(workspace: Optional[torch.Tensor], operand: torch.Tensor, entry: str, size,
+               stream) -> Tuple[int, int, Optional[torch.Tensor]]:
     """(pointer, bytes, tensor) of the caller's workspace, or of one made for this call
     when the 2-byte operand's rows are off 16-byte boundaries."""
     if workspace is None:
-        need = 0 if rows16 else int(nbytes(*size))
+        need = 0 if _rows_on_16_bytes(operand) else int(getattr(_library(), entry)(*size))
         if need <= 0:
             return 0, 0, None
-        workspace = _empty((need,), torch.uint8, device, stream)
-    elif (not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+        workspace = _empty(operand, (need,), torch.uint8, stream)
+    elif (not workspace.is_cuda or workspace.device != operand.device
+          or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {operand.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _w4_product(entry: str, dtype: torch.dtype, A, codes, scales, zeros, group, out, workspace,
                 stream) -> torch.Tensor:
-    M, K = _matrix("A", A)
-    device = A.device
-    _need("A", A, dtype, (M, K))
-    _need("scales", scales, dtype, scales.shape, device)
-    N = _w4_check(codes, scales, zeros, K, group, device)
-    with _on_device(A):
-        lib = _library()
-        if out is None:
-            out = _empty((M, N), torch.float32, device, stream)
-        else:
-            _need("out", out, torch.float32, (M, N), device)
-        ptr, nbytes, workspace = _workspace(workspace, _rows_on_16_bytes(A),
-                                            lib.gemm_w4_workspace_bytes, (M, N, K), device, stream)
-        _check(getattr(lib, entry)(M, N, K, A.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                   0 if zeros is None else zeros.data_ptr(), group, out.data_ptr(),
-                                   ptr, nbytes, _stream_handle(stream, A.get_device())))
+    # One look at everything a valid call passes (a decoded token's call takes little
+    # longer than its kernel); what fails it is looked at part by part for its message.
+    device = A.get_device() if type(A) is torch.Tensor else -1
+    fine = (device >= 0 and group in W4_GROUPS and _plain(A, dtype, device)
+            and _plain(codes, torch.uint8, device) and _plain(scales, dtype, device)
+            and A.dim() == 2 and codes.dim() == 2)
+    if fine:
+        M, K = A.shape
+        N, row = codes.shape
+        meta = ((K + group - 1) // group, N)
+        fine = (row == (K + W4_BLOCK - 1) // W4_BLOCK * 64 and scales.shape == meta
+                and (zeros is None or (_plain(zeros, torch.uint8, device) and zeros.shape == meta)))
+    if not fine:
+        M, K = _matrix("A", A)
+        _need("A", A, dtype, (M, K))
+        _need("scales", scales, dtype, scales.shape, A.device)
+        N = _w4_check(codes, scales, zeros, K, group, A.device)
+    if out is None:
+        out = _empty(A, (M, N), torch.float32, stream)
+    else:
+        _need("out", out, torch.float32, (M, N), A.device)
+    ptr, nbytes, workspace = _workspace(workspace, A, "gemm_w4_workspace_bytes", (M, N, K), stream)
+    _call(entry, A.get_device(), stream, M, N, K, A.data_ptr(), codes.data_ptr(),
+          scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(), group, out.data_ptr(), ptr,
+          nbytes)
     return out
 
 
@@ -503,12 +529,10 @@ def gemm_q8_quantize(X: torch.Tensor, stream: Optional[torch.cuda.Stream] = None
     for each column of 128 rows. codes: int8, M x ceil16(K); scales: fp32."""
     M, K = _matrix("X", X)
     name = _type_name(X.dtype)
-    with _on_device(X):
-        codes = _empty((M, (K + 15) // 16 * 16), torch.int8, X.device, stream)
-        scales = _empty(((M + Q8_ROWS - 1) // Q8_ROWS, K), torch.float32, X.device, stream)
-        _check(getattr(_library(), f"gemm_{name}_q8_quantize")(
-            M, K, X.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-            _stream_handle(stream, X.get_device())))
+    codes = _empty(X, (M, (K + 15) // 16 * 16), torch.int8, stream)
+    scales = _empty(X, ((M + Q8_ROWS - 1) // Q8_ROWS, K), torch.float32, stream)
+    _call(f"gemm_{name}_q8_quantize", X.get_device(), stream, M, K, X.data_ptr(),
+          codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -523,14 +547,12 @@ def gemm_q8_dequantize(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int
     """The saved M x K activation, codes * scales, in `dtype` (bf16 or fp16)."""
     name = _type_name(dtype)
     _q8_check(codes, scales, M, K, scales.device)
-    with _on_device(codes):
-        if out is None:
-            out = _empty((M, K), dtype, codes.device, stream)
-        else:
-            _need("out", out, dtype, (M, K), codes.device)
-        _check(getattr(_library(), f"gemm_{name}_q8_dequantize")(
-            M, K, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
-            _stream_handle(stream, codes.get_device())))
+    if out is None:
+        out = _empty(codes, (M, K), dtype, stream)
+    else:
+        _need("out", out, dtype, (M, K), codes.device)
+    _call(f"gemm_{name}_q8_dequantize", codes.get_device(), stream, M, K, codes.data_ptr(),
+          scales.data_ptr(), out.data_ptr())
     return out
 
 
@@ -538,20 +560,15 @@ def _q8t_product(entry: str, dtype: torch.dtype, codes, scales, dY, out, workspa
                  stream) -> torch.Tensor:
     M, N = _matrix("dY", dY)
     K = _matrix("scales", scales)[1]
-    device = dY.device
     _need("dY", dY, dtype, (M, N))
-    _q8_check(codes, scales, M, K, device)
-    with _on_device(dY):
-        lib = _library()
-        if out is None:
-            out = _empty((K, N), torch.float32, device, stream)
-        else:
-            _need("out", out, torch.float32, (K, N), device)
-        ptr, nbytes, workspace = _workspace(workspace, _rows_on_16_bytes(dY),
-                                            lib.gemm_q8t_workspace_bytes, (M, N, K), device, stream)
-        _check(getattr(lib, entry)(M, N, K, codes.data_ptr(), scales.data_ptr(), dY.data_ptr(),
-                                   out.data_ptr(), ptr, nbytes,
-                                   _stream_handle(stream, dY.get_device())))
+    _q8_check(codes, scales, M, K, dY.device)
+    if out is None:
+        out = _empty(dY, (K, N), torch.float32, stream)
+    else:
+        _need("out", out, torch.float32, (K, N), dY.device)
+    ptr, nbytes, workspace = _workspace(workspace, dY, "gemm_q8t_workspace_bytes", (M, N, K), stream)
+    _call(entry, dY.get_device(), stream, M, N, K, codes.data_ptr(), scales.data_ptr(),
+          dY.data_ptr(), out.data_ptr(), ptr, nbytes)
     return out
 
 

@@ -125,7 +125,7 @@ inline __host__ __device__ constexpr uint32_t warp_bytes(int t, int rows)
 
 // GS: log2 of the group. V: see copy_values.
 template <bool F16, int T, int NB, int V, int GS>
-__global__ void __launch_bounds__(kThreads, NB == 1 ? (T == 1 ? 3 : 2) : 1)
+__global__ void __launch_bounds__(kThreads, NB == 2 ? 1 : T == 1 && V == 8 && GS == 7 ? 3 : 2)
     w4_rows_kernel(const W4Launch p)
 {
     constexpr int GROUP = 1 << GS;
@@ -341,38 +341,42 @@ static cudaError_t launch_kernel(const W4Launch &L, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <bool F16, int T, int NB, int V>
-static cudaError_t launch_g(const W4Launch &L, cudaStream_t stream)
-{
-    return L.group == 32   ? launch_kernel<F16, T, NB, V, 5>(L, stream)
-           : L.group == 64 ? launch_kernel<F16, T, NB, V, 6>(L, stream)
-                           : launch_kernel<F16, T, NB, V, 7>(L, stream);
-}
-
-template <bool F16, int T, int NB>
+template <bool F16, int T, int NB, int GS>
 static cudaError_t launch_v(const W4Launch &L, cudaStream_t stream)
 {
     const uintptr_t a = reinterpret_cast<uintptr_t>(L.A);
-    return L.K % 8 == 0 && a % 16 == 0  ? launch_g<F16, T, NB, 8>(L, stream)
-           : L.K % 2 == 0 && a % 4 == 0 ? launch_g<F16, T, NB, 2>(L, stream)
-                                        : launch_g<F16, T, NB, 1>(L, stream);
+    return L.K % 8 == 0 && a % 16 == 0  ? launch_kernel<F16, T, NB, 8, GS>(L, stream)
+           : L.K % 2 == 0 && a % 4 == 0 ? launch_kernel<F16, T, NB, 2, GS>(L, stream)
+                                        : launch_kernel<F16, T, NB, 1, GS>(L, stream);
 }
 
-template <bool F16>
+template <bool F16, int GS>
 static cudaError_t launch_f(const W4Launch &L, int sms, cudaStream_t stream)
 {
     if (L.M > 8)
-        return launch_v<F16, 2, 2>(L, stream);
-    // 32 columns a block while that still gives every SM two blocks.
-    return (L.N + 31) / 32 >= 2 * sms && L.M <= 4 ? launch_v<F16, 2, 1>(L, stream)
-                                      : launch_v<F16, 1, 1>(L, stream);
+        return launch_v<F16, 2, 2, GS>(L, stream);
+    // 32 columns a block (A's values are read once for both halves) where that
+    // still gives every SM two blocks and few rows of A leave the shared memory:
+    // 1 x 32768 x 8192 34.8 us against 38.7 us with 16. Finer groups need the
+    // registers for their scales.
+    if constexpr (GS == 7)
+        if ((L.N + 31) / 32 >= 2 * sms && L.M <= 4)
+            return launch_v<F16, 2, 1, GS>(L, stream);
+    return launch_v<F16, 1, 1, GS>(L, stream);
 }
 
 } // namespace w4r
 
 cudaError_t launch_w4_rows(const W4Launch &L, int sms, cudaStream_t stream)
 {
-    return L.f16 ? w4r::launch_f<true>(L, sms, stream) : w4r::launch_f<false>(L, sms, stream);
+    using namespace w4r;
+    if (L.f16)
+        return L.group == 32   ? launch_f<true, 5>(L, sms, stream)
+               : L.group == 64 ? launch_f<true, 6>(L, sms, stream)
+                               : launch_f<true, 7>(L, sms, stream);
+    return L.group == 32   ? launch_f<false, 5>(L, sms, stream)
+           : L.group == 64 ? launch_f<false, 6>(L, sms, stream)
+                           : launch_f<false, 7>(L, sms, stream);
 }
 
 } // namespace rtm
