@@ -411,10 +411,18 @@ GEMM_API int gemm_f16_w4_dequantize(int64_t K, int64_t N, int group, const uint8
  * fp16 and W in 4 bits:
  *     C[i][j] = sum_g scales[g][j] * sum_{k in g} A[i][k] * (q[k][j] - zeros[g][j])
  * Any M (1: a single token), N and K, A and scales 2-byte, codes 16-byte, C
- * 4-byte aligned. `workspace` may be null; gemm_w4_workspace_bytes says how
- * many bytes (16-byte aligned, overlapping nothing) the call can use, whatever
- * the pointers. The contents of the workspace on return are unspecified; two
- * calls in flight must not share one.
+ * 4-byte aligned. For M <= 16 blocks of eight warps own 16 or 32 columns of W,
+ * which they read once, k split over the warps (mma.sync: the product is bound
+ * by the weights). Larger M run on the tcgen05 tensor cores: codes are
+ * converted to integers of A's type as they are staged, and each group's sum is
+ * scaled as it is added to the total; k is split over the CTAs of a cluster
+ * where there are few tiles. Results repeat exactly from call to call. The
+ * tensor-core path needs the rows of A on 16-byte boundaries (K % 8 == 0, A
+ * 16-byte aligned); otherwise A is first copied with padded rows into
+ * `workspace` (16-byte aligned, gemm_w4_workspace_bytes(M, N, K) bytes,
+ * overlapping nothing; 0 for M <= 16), and where it is null or too small the
+ * product runs on the FP32 pipes, many times slower. The contents of the
+ * workspace on return are unspecified; two calls in flight must not share one.
  */
 GEMM_API int64_t gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 GEMM_API int gemm_bf16w4f32(int64_t M, int64_t N, int64_t K, const uint16_t *A,
@@ -449,8 +457,10 @@ GEMM_API int gemm_f16w4f32(int64_t M, int64_t N, int64_t K, const uint16_t *A,
  * gemm_q8tbf16f32 / gemm_q8tf16f32 — the weight gradient of Y = X.W from the
  * saved X: dW = X^T.dY (K x N, fp32), dY (M x N) bf16 or fp16,
  *     dW[k][j] = sum_b scales[b][k] * sum_{m in b} codes[m][k] * dY[m][j]
- * Any M, N, K; codes 16-byte, scales and dW 4-byte, dY 2-byte aligned.
- * gemm_q8t_workspace_bytes and `workspace` as for gemm_bf16w4f32.
+ * Any M, N, K; codes 16-byte, scales and dW 4-byte, dY 2-byte aligned. The
+ * kernel of gemm_bf16w4f32's larger M with tokens as the depth; dY's rows off
+ * 16-byte boundaries are copied into `workspace` (gemm_q8t_workspace_bytes)
+ * the same way, with the same fallback without one.
  */
 GEMM_API int64_t gemm_q8_codes_bytes(int64_t M, int64_t K);
 GEMM_API int gemm_bf16_q8_quantize(int64_t M, int64_t K, const uint16_t *X, int8_t *codes,
@@ -468,6 +478,26 @@ GEMM_API int gemm_q8tbf16f32(int64_t M, int64_t N, int64_t K, const int8_t *code
 GEMM_API int gemm_q8tf16f32(int64_t M, int64_t N, int64_t K, const int8_t *codes,
                             const float *scales, const uint16_t *dY, float *dW, void *workspace,
                             int64_t workspace_bytes, void *stream);
+
+/*
+ * gemm_bf16w4f32_selftest_timeout / gemm_q8tbf16f32_selftest_timeout —
+ * failure-detection checks of the bounded waits of the tensor-core kernel that
+ * computes the two products: the kernel the shape selects runs on the given
+ * buffers with its loads muted and every wait limited to `wait_limit_ns` ([1e6,
+ * 1e10]); each role gives up, the kernel frees its tensor memory, records
+ * GEMM_ERR_TIMEOUT in the device error word and returns. C (dW) is left
+ * unspecified. GEMM_ERR_INVALID_ARG for arguments the products refuse, M <= 16
+ * (w4: another kernel, without such waits) or rows of A (dY) off 16-byte
+ * boundaries.
+ */
+GEMM_API int gemm_bf16w4f32_selftest_timeout(int64_t M, int64_t N, int64_t K, const uint16_t *A,
+                                             const uint8_t *codes, const uint16_t *scales,
+                                             const uint8_t *zeros, int group, float *C,
+                                             int64_t wait_limit_ns, void *stream);
+GEMM_API int gemm_q8tbf16f32_selftest_timeout(int64_t M, int64_t N, int64_t K,
+                                              const int8_t *codes, const float *scales,
+                                              const uint16_t *dY, float *dW,
+                                              int64_t wait_limit_ns, void *stream);
 
 /*
  * gemm_get_device_error — synchronises `stream`, then returns and clears the

@@ -24,6 +24,7 @@ from .binding import (  # noqa: F401
     gemm_bf16f32_workspace_bytes,
     gemm_bf16f32_ws,
     gemm_bf16w4f32,
+    gemm_bf16w4f32_selftest_timeout,
     gemm_f16f32,
     gemm_f16f32_ws,
     gemm_f16w4f32,
@@ -37,6 +38,7 @@ from .binding import (  # noqa: F401
     gemm_q8_quantize,
     gemm_q8t_workspace_bytes,
     gemm_q8tbf16f32,
+    gemm_q8tbf16f32_selftest_timeout,
     gemm_q8tf16f32,
     gemm_w4_dequantize,
     gemm_w4_pack,

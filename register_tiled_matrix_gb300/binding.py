@@ -91,6 +91,10 @@ def load_library() -> ctypes.CDLL:
                                (f"gemm_q8t{t}f32", [i64] * 3 + [p] * 5 + [i64, p])):
                 f = getattr(lib, name)
                 f.argtypes, f.restype = args, c_int
+        lib.gemm_bf16w4f32_selftest_timeout.argtypes = [i64] * 3 + [p] * 4 + [c_int, p, i64, p]
+        lib.gemm_bf16w4f32_selftest_timeout.restype = c_int
+        lib.gemm_q8tbf16f32_selftest_timeout.argtypes = [i64] * 3 + [p] * 4 + [i64, p]
+        lib.gemm_q8tbf16f32_selftest_timeout.restype = c_int
         lib.gemm_fp32_pipe_peak.argtypes = [i64, ctypes.c_int, p, ctypes.POINTER(ctypes.c_double),
                                             p]
         lib.gemm_fp32_pipe_peak.restype = ctypes.c_int
@@ -595,6 +599,30 @@ def gemm_q8t_workspace_bytes(M: int, N: int, K: int) -> int:
     n = int(load_library().gemm_q8t_workspace_bytes(int(M), int(N), int(K)))
     _check(n if n < 0 else 0)
     return n
+
+
+def gemm_bf16w4f32_selftest_timeout(A, codes, scales, zeros, group: int, out: torch.Tensor,
+                                    wait_limit_ns: int) -> None:
+    """Launch the 4-bit tensor-core kernel with its loads muted so every bounded wait runs out."""
+    M, K = _matrix("A", A)
+    _need("A", A, torch.bfloat16, (M, K))
+    N = _w4_check(codes, scales, zeros, K, group, A.device)
+    _need("out", out, torch.float32, (M, N), A.device)
+    _call("gemm_bf16w4f32_selftest_timeout", A.get_device(), None, M, N, K, A.data_ptr(),
+          codes.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr(), group,
+          out.data_ptr(), int(wait_limit_ns))
+
+
+def gemm_q8tbf16f32_selftest_timeout(codes, scales, dY, out: torch.Tensor,
+                                     wait_limit_ns: int) -> None:
+    """Launch the 8-bit weight-gradient kernel with its loads muted so every bounded wait runs out."""
+    M, N = _matrix("dY", dY)
+    K = _matrix("scales", scales)[1]
+    _need("dY", dY, torch.bfloat16, (M, N))
+    _q8_check(codes, scales, M, K, dY.device)
+    _need("out", out, torch.float32, (K, N), dY.device)
+    _call("gemm_q8tbf16f32_selftest_timeout", dY.get_device(), None, M, N, K, codes.data_ptr(),
+          scales.data_ptr(), dY.data_ptr(), out.data_ptr(), int(wait_limit_ns))
 
 
 def gemm_bf16f32_selftest_timeout(A: torch.Tensor, B: torch.Tensor, out: torch.Tensor,

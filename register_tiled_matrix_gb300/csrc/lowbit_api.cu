@@ -273,9 +273,53 @@ int q8t_product(int64_t M, int64_t N, int64_t K, int f16, const int8_t *codes, c
     return finish(rtm::launch_q8t_simt(L, s));
 }
 
+// wait_limit_ns > 0: the failure-detection self-test of the tensor-core kernel.
+int device_with_limit(rtm::DeviceContext *d, int64_t wait_limit_ns)
+{
+    const int st = rtm::device_context(d);
+    if (wait_limit_ns > 0)
+        d->wait_limit_ns = (uint64_t)wait_limit_ns;
+    return st == GEMM_OK && !d->encode_tiled ? GEMM_ERR_LAUNCH : st;
+}
+
+bool limit_ok(int64_t ns) { return ns >= 1000000 && ns <= 10000000000LL; }
+
 } // namespace
 
 extern "C" {
+
+int gemm_bf16w4f32_selftest_timeout(int64_t M, int64_t N, int64_t K, const uint16_t *A,
+                                    const uint8_t *codes, const uint16_t *scales,
+                                    const uint8_t *zeros, int group, float *C,
+                                    int64_t wait_limit_ns, void *stream)
+{
+    if (!limit_ok(wait_limit_ns) || M <= rtm::kW4RowsMax || N < 1 || K < 1 || !size_ok(M, K) ||
+        !size_ok(K, N) || !size_ok(M, N) || !group_ok(group) || !A || !codes || !scales || !C ||
+        !rows16(A, K) || misaligned(codes, 16) || misaligned(scales, 2) || misaligned(C, 4))
+        return GEMM_ERR_INVALID_ARG;
+    rtm::DeviceContext d;
+    const int st = device_with_limit(&d, wait_limit_ns);
+    if (st != GEMM_OK)
+        return st;
+    rtm::W4Launch L{(int)M, (int)N, (int)K, group, 0, A, codes, scales, zeros, C};
+    return finish(rtm::launch_w4_tc(L, K, d, true, static_cast<cudaStream_t>(stream)));
+}
+
+int gemm_q8tbf16f32_selftest_timeout(int64_t M, int64_t N, int64_t K, const int8_t *codes,
+                                     const float *scales, const uint16_t *dY, float *dW,
+                                     int64_t wait_limit_ns, void *stream)
+{
+    if (!limit_ok(wait_limit_ns) || M < 1 || N < 1 || K < 1 || !size_ok(M, K) || !size_ok(K, N) ||
+        !size_ok(M, N) || !codes || !scales || !dY || !dW || !rows16(dY, N) ||
+        misaligned(codes, 16) || misaligned(scales, 4) || misaligned(dW, 4))
+        return GEMM_ERR_INVALID_ARG;
+    rtm::DeviceContext d;
+    const int st = device_with_limit(&d, wait_limit_ns);
+    if (st != GEMM_OK)
+        return st;
+    rtm::Q8tLaunch L{(int)M, (int)N, (int)K, 0, codes, scales, dY, dW};
+    return finish(rtm::launch_q8t_tc(L, N, d, true, static_cast<cudaStream_t>(stream)));
+}
 
 int64_t gemm_w4_codes_bytes(int64_t K, int64_t N)
 {

@@ -73,7 +73,7 @@ struct Cfg {
     static constexpr int PW = 3 - DW;             // promoting warpgroups
     // Registers a thread after the split: the four warpgroups share what the block
     // was launched with, 4 x 128.
-    static constexpr int R_ISSUE = 56, R_DEQUANT = NT == 256 ? 104 : NT == 128 ? 96 : 128;
+    static constexpr int R_ISSUE = 56, R_DEQUANT = NT == 256 ? 104 : NT == 128 ? 112 : 128;
     static constexpr int R_PROMOTE = NT >= 128 ? 176 : 192;
     static_assert(R_ISSUE + DW * R_DEQUANT + PW * R_PROMOTE <= 512, "register split");
     static constexpr int CPT = NT / PW;           // columns of a promoting thread
@@ -135,6 +135,22 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+
+// Whether the phase has completed, without waiting. A look at a barrier takes 130
+// to 190 cycles here (shared memory is busy), more than issuing a stage's MMAs
+// leaves; so the roles look ahead, before the work they have in hand, and wait
+// only where the answer was no.
+__device__ __forceinline__ bool peek(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}\n"
                  : "=r"(done)
                  : "r"(bar), "r"(parity)
@@ -302,57 +318,61 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
     const uint64_t desc0 = sdesc_sw128(smem0, LBO, 1024);
     const bool elected = elect_one();
     const int tail = min(STEPS, (depth - (nstages - 1) * BK + UMMA_K - 1) / UMMA_K);
-    uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
-    bool any = false;
+    Place<Cf::STAGES> stage;
+    Place<Cf::SETS> set;
+    const uint32_t full_at = smem_u32(full), tempty_at = smem_u32(tempty);
+    bool any = false, full_seen = false, empty_seen = false;  // what the look ahead said
 #pragma unroll 1
     for (int t = unit; t < p.tiles; t += units) {
 #pragma unroll 1
         for (int i = 0; i < nstages; ++i) {
-            if (!wait_bounded(smem_u32(&full[stage]), phase, p.limit_ns, abort)) {
+            if (!full_seen &&
+                !wait_bounded(full_at + stage.at * 8, stage.phase, p.limit_ns, abort)) {
                 give_up(p.err, abort);
                 goto out;
             }
             tc_fence_after();
             const bool last = i == nstages - 1;
             const int steps = last ? tail : STEPS;
-            const uint64_t adesc = desc0 + stage * (Cf::STAGE_BYTES >> 4);
+            const uint64_t adesc = desc0 + stage.at * (Cf::STAGE_BYTES >> 4);
             const uint64_t bdesc = adesc + (A_BYTES >> 4);
+            Place<Cf::STAGES> next = stage;
+            next.advance();
+            full_seen = peek(full_at + next.at * 8, next.phase);
 #pragma unroll
             for (int kk = 0; kk < STEPS; ++kk)
                 if (kk < steps) {
                     const bool begin = PG == 8 ? kk == 0 && (i & 1) == 0 : kk % PG == 0;
                     if (begin) {
-                        if (!wait_bounded(smem_u32(&tempty[set]), set_phase ^ 1, p.limit_ns, abort)) {
+                        if (!empty_seen && !wait_bounded(tempty_at + set.at * 8, set.phase ^ 1,
+                                                         p.limit_ns, abort)) {
                             give_up(p.err, abort);
                             goto out;
                         }
                         tc_fence_after();
+                        Place<Cf::SETS> after = set;
+                        after.advance();
+                        empty_seen = peek(tempty_at + after.at * 8, after.phase ^ 1);
                     }
                     if (elected) {
                         if constexpr (PAIR)
-                            umma_f16_pair(tmem_base + set * NT, adesc + kk * ADVANCE,
+                            umma_f16_pair(tmem_base + set.at * NT, adesc + kk * ADVANCE,
                                           bdesc + kk * ADVANCE, idesc<MODE, F16, NT>(), !begin);
                         else
-                            umma_f16(tmem_base + set * NT, adesc + kk * ADVANCE,
+                            umma_f16(tmem_base + set.at * NT, adesc + kk * ADVANCE,
                                      bdesc + kk * ADVANCE, idesc<MODE, F16, NT>(), !begin);
                     }
                     const bool end = PG == 8 ? kk == STEPS - 1 && (i & 1) == 1 : kk % PG == PG - 1;
                     if (end || (last && kk == steps - 1)) {
                         if (elected)
-                            commit<PAIR>(&tfull[set], pair_mask);
-                        if (++set == Cf::SETS) {
-                            set = 0;
-                            set_phase ^= 1;
-                        }
+                            commit<PAIR>(tfull + set.at, pair_mask);
+                        set.advance();
                     }
                 }
             any = true;
             if (elected)
-                commit<PAIR>(&empty[stage], pair_mask);
-            if (++stage == Cf::STAGES) {
-                stage = 0;
-                phase ^= 1;
-            }
+                commit<PAIR>(empty + stage.at, pair_mask);
+            stage = next;
         }
     }
 out:
@@ -647,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        const bool free = peek(empty_at + stage.at * 8, stage.phase ^ 1);
                         uint4 v[8];  // word w of quarter c: k = 32 w + 8 c and up
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -669,8 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (2 * i + h >= nstages)
                             break;
-                        if (!wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns,
-                                          abort)) {
+                        if (!free && !wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1,
+                                                   p.limit_ns, abort)) {
                             give_up(p.err, abort);
                             ok = false;
                             break;
@@ -714,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = load();
 #pragma unroll 1
             for (int sn = d; ok && sn < total; sn += Cf::DW) {
+                const bool free = peek(empty_at + stage.at * 8, stage.phase ^ 1);
                 uint4 v[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -730,7 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 raw.advance(Cf::DW);
                 if (sn + Cf::DW < total && !load())
                     break;
-                if (!wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, abort)) {
+                if (!free &&
+                    !wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     break;
                 }
@@ -756,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tfull_at = smem_u32(tfull);
         const uint32_t tempty_at =
             PAIR ? mapa_shared(smem_u32(tempty), leader) : smem_u32(tempty);
-        bool ok = true;
+        bool ok = true, seen = false;
         uint32_t set = 0, set_phase = 0;
         int l0 = 0, c0 = 0;
         uintptr_t sp = 0;    // this lane's next scale to copy
@@ -800,12 +823,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     s = __uint_as_float(word);
                 }
-                if (!wait_bounded(tfull_at + set * 8, set_phase, p.limit_ns, abort)) {
+                if (!seen && !wait_bounded(tfull_at + set * 8, set_phase, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                if constexpr (PAIR)  // (the other tiles' groups come too slowly for it to help)
+                    seen = set + 1 == Cf::SETS ? peek(tfull_at, set_phase ^ 1)
+                                               : peek(tfull_at + (set + 1) * 8, set_phase);
                 const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + set * NT +
                                        (uint32_t)(pw * Cf::CPT);
 #pragma unroll

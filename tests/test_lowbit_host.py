@@ -105,3 +105,13 @@ def test_reference_packs_and_unpacks(K):
     codes = ref.w4_pack(q)
     assert codes.shape == (5, (K + 127) // 128 * 64)
     assert torch.equal(ref.w4_unpack(codes, K), q)
+
+
+def test_selftest_arguments(lib):
+    f = lib.gemm_bf16w4f32_selftest_timeout
+    assert f(64, 64, 256, A, B, C, D, 128, E, 10, None) == -1            # limit too short
+    assert f(16, 64, 256, A, B, C, D, 128, E, 10 ** 8, None) == -1       # another kernel
+    assert f(64, 64, 250, A, B, C, D, 128, E, 10 ** 8, None) == -1       # rows off 16 bytes
+    g = lib.gemm_q8tbf16f32_selftest_timeout
+    assert g(64, 64, 64, A, B, C, E, 10 ** 11, None) == -1
+    assert g(64, 60, 64, A, B, C, E, 10 ** 8, None) == -1

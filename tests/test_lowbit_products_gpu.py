@@ -382,3 +382,73 @@ def test_refusals():
                                     W.s_d.data_ptr(), W.z_d.data_ptr(), 128, out.data_ptr(), 0, 0, 0)
         if status:
             raise rtm.GemmError(status, rtm.status_string(status))
+
+
+@pytest.mark.parametrize("M,N,K,group", [(200, 136, 8192, 32), (48, 520, 4096, 64), (100, 136, 8192, 128),
+                                         (700, 1030, 2048, 128), (3, 300, 8192, 64)])
+def test_w4_repeats_exactly(M, N, K, group):
+    """Many calls give the same bits, with other work between them: nothing is read
+    before it has arrived or after its place has been given away."""
+    W = Weight(K, N, group, True, torch.bfloat16, 1)
+    A = randn(M, K, torch.bfloat16, 2).to(DEV)
+    want = W.product(A)
+    a, w = A.double().cpu(), W.values()
+    ref.assert_within(want, a @ w, ref.product_bound(K, a, w))
+    for i in range(60):
+        if i % 3 == 0:
+            torch.randn(2_000_000, device=DEV)
+        assert torch.equal(W.product(A), want)
+    done()
+
+
+@pytest.mark.parametrize("M,N,K", [(9000, 264, 520), (9000, 64, 64), (5000, 1030, 700), (4096, 100, 256)])
+def test_q8t_repeats_exactly(M, N, K):
+    X, dY = Saved(M, K, 1), randn(M, N, torch.bfloat16, 2).to(DEV)
+    want = X.gradient(dY)
+    for i in range(60):
+        if i % 3 == 0:
+            torch.randn(2_000_000, device=DEV)
+        assert torch.equal(X.gradient(dY), want)
+    done()
+
+
+@pytest.mark.parametrize("M", [17, 60, 128, 300])
+def test_timeout_is_reported_and_the_context_stays_usable(M):
+    """With the loads muted every bounded wait runs out: one status, and the next call is right."""
+    W = Weight(1024, 300, 64, True, torch.bfloat16, 1)
+    A = randn(M, 1024, torch.bfloat16, 2).to(DEV)
+    want = W.product(A)
+    rtm.gemm_bf16w4f32_selftest_timeout(A, W.codes_d, W.s_d, W.z_d, W.group,
+                                        torch.empty_like(want), 20_000_000)
+    assert rtm.STATUS[rtm.get_device_error()] == "GEMM_ERR_TIMEOUT"
+    assert torch.equal(W.product(A), want)
+    X, dY = Saved(400, 130, 3), randn(400, 8 * M, torch.bfloat16, 4).to(DEV)
+    want = X.gradient(dY)
+    rtm.gemm_q8tbf16f32_selftest_timeout(X.codes_d, X.s_d, dY, torch.empty_like(want), 20_000_000)
+    assert rtm.STATUS[rtm.get_device_error()] == "GEMM_ERR_TIMEOUT"
+    assert torch.equal(X.gradient(dY), want)
+    done()
+
+
+def test_workspace_given_or_refused():
+    """Rows off 16-byte boundaries: with a workspace, with one too small and with none
+    (the binding's own) the sums differ in order only; one over an operand is refused."""
+    M, N, K = 300, 77, 131
+    W, A = Weight(K, N, 64, True, torch.float16, 1), randn(M, K, torch.float16, 2).to(DEV)
+    need = rtm.gemm_w4_workspace_bytes(M, N, K)
+    assert need == (M * 136 * 2 + 255) // 256 * 256 and rtm.gemm_w4_workspace_bytes(16, N, K) == 0
+    a, w = A.double().cpu(), W.values()
+    bound = ref.product_bound(K, a, w)
+    for nbytes in (need, 16):
+        C = W.product(A, workspace=torch.empty(nbytes, dtype=torch.uint8, device=DEV))
+        done()
+        ref.assert_within(C, a @ w, bound)
+    with pytest.raises(rtm.GemmError):
+        out = torch.empty(M + need, N, device=DEV)
+        W.product(A, out=out[:M], workspace=out)
+    X, dY = Saved(M, 90, 3), randn(M, N, torch.float16, 4).to(DEV)
+    x, d = X.values().t(), dY.double().cpu()
+    for nbytes in (rtm.gemm_q8t_workspace_bytes(M, N, 90), 16):
+        dW = X.gradient(dY, workspace=torch.empty(nbytes, dtype=torch.uint8, device=DEV))
+        done()
+        ref.assert_within(dW, x @ d, ref.product_bound(M, x, d))
