@@ -375,9 +375,9 @@ def _empty(like: torch.Tensor, shape, dtype: torch.dtype,
     """Memory on like's device, of the stream the call runs on, so that it is reused in
     that stream's order."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _call(entry: str, device: int, stream: Optional[torch.cuda.Stream], *args) -> None:

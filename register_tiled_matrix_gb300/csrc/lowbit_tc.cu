@@ -187,6 +187,14 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
     }
 }
 
+// The same for a warp that waits as one, `seen` if a look ahead said yes: all of
+// its lanes go on or none does, so none leaves a loop that its mates stay in.
+__device__ __forceinline__ bool wait_warp(bool seen, uint32_t bar, uint32_t parity,
+                                          uint64_t limit_ns, volatile int *abort)
+{
+    return __all_sync(0xffffffffu, seen || wait_bounded(bar, parity, limit_ns, abort));
+}
+
 // A place in a ring of N barriers 8 bytes apart: its index and how often (mod 2)
 // the ring has gone round.
 template <int N>
@@ -326,8 +334,7 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
     for (int t = unit; t < p.tiles; t += units) {
 #pragma unroll 1
         for (int i = 0; i < nstages; ++i) {
-            if (!full_seen &&
-                !wait_bounded(full_at + stage.at * 8, stage.phase, p.limit_ns, abort)) {
+            if (!wait_warp(full_seen, full_at + stage.at * 8, stage.phase, p.limit_ns, abort)) {
                 give_up(p.err, abort);
                 goto out;
             }
@@ -344,8 +351,8 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
                 if (kk < steps) {
                     const bool begin = PG == 8 ? kk == 0 && (i & 1) == 0 : kk % PG == 0;
                     if (begin) {
-                        if (!empty_seen && !wait_bounded(tempty_at + set.at * 8, set.phase ^ 1,
-                                                         p.limit_ns, abort)) {
+                        if (!wait_warp(empty_seen, tempty_at + set.at * 8, set.phase ^ 1, p.limit_ns,
+                                       abort)) {
                             give_up(p.err, abort);
                             goto out;
                         }
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t src0 = base + Cf::OFF_RAW + (uint32_t)(tid * 64 + ((tid & 6) << 3));
             const uint32_t dst0 = base + (uint32_t)(tid * 128 + ((tid & 7) << 4));
             auto load = [&]() {
-                if (!wait_bounded(raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
+                if (!wait_warp(false, raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     return false;
                 }
@@ -690,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (2 * i + h >= nstages)
                             break;
-                        if (!free && !wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1,
-                                                   p.limit_ns, abort)) {
+                        if (!wait_warp(free, empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns,
+                                       abort)) {
                             give_up(p.err, abort);
                             ok = false;
                             break;
@@ -719,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tiles = unit < p.tiles ? (p.tiles - unit + units - 1) / units : 0;
             const int total = tiles * nstages;  // stages of this CTA, tile after tile
             auto load = [&]() {
-                if (!wait_bounded(raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
+                if (!wait_warp(false, raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     return false;
                 }
@@ -752,8 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 raw.advance(Cf::DW);
                 if (sn + Cf::DW < total && !load())
                     break;
-                if (!free &&
-                    !wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, abort)) {
+                if (!wait_warp(free, empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     break;
                 }
@@ -823,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     s = __uint_as_float(word);
                 }
-                if (!seen && !wait_bounded(tfull_at + set * 8, set_phase, p.limit_ns, abort)) {
+                if (!wait_warp(seen, tfull_at + set * 8, set_phase, p.limit_ns, abort)) {
                     give_up(p.err, abort);
                     ok = false;
                     break;
