@@ -187,12 +187,16 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
     }
 }
 
-// The same for a warp that waits as one, `seen` if a look ahead said yes: all of
-// its lanes go on or none does, so none leaves a loop that its mates stay in.
-__device__ __forceinline__ bool wait_warp(bool seen, uint32_t bar, uint32_t parity,
-                                          uint64_t limit_ns, volatile int *abort)
+// The same for a warp that waits as one. It returns in every case: after a wait
+// that gave up (recorded in the error word and the abort flag, which ends the
+// other waits too) the roles run through their loops on whatever is there, in
+// bounds, so no lane leaves a loop that its mates stay in, and the result is
+// unspecified. A vote of the lanes after each wait cost 3 to 8 %.
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, uint64_t limit_ns, int *err,
+                                        volatile int *abort)
 {
-    return __all_sync(0xffffffffu, seen || wait_bounded(bar, parity, limit_ns, abort));
+    if (!wait_bounded(bar, parity, limit_ns, abort))
+        give_up(err, abort);
 }
 
 // A place in a ring of N barriers 8 bytes apart: its index and how often (mod 2)
@@ -329,15 +333,13 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
     Place<Cf::STAGES> stage;
     Place<Cf::SETS> set;
     const uint32_t full_at = smem_u32(full), tempty_at = smem_u32(tempty);
-    bool any = false, full_seen = false, empty_seen = false;  // what the look ahead said
+    bool full_seen = false, empty_seen = false;  // what the look ahead said
 #pragma unroll 1
     for (int t = unit; t < p.tiles; t += units) {
 #pragma unroll 1
         for (int i = 0; i < nstages; ++i) {
-            if (!wait_warp(full_seen, full_at + stage.at * 8, stage.phase, p.limit_ns, abort)) {
-                give_up(p.err, abort);
-                goto out;
-            }
+            if (!full_seen)
+                wait_on(full_at + stage.at * 8, stage.phase, p.limit_ns, p.err, abort);
             tc_fence_after();
             const bool last = i == nstages - 1;
             const int steps = last ? tail : STEPS;
@@ -351,11 +353,8 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
                 if (kk < steps) {
                     const bool begin = PG == 8 ? kk == 0 && (i & 1) == 0 : kk % PG == 0;
                     if (begin) {
-                        if (!wait_warp(empty_seen, tempty_at + set.at * 8, set.phase ^ 1, p.limit_ns,
-                                       abort)) {
-                            give_up(p.err, abort);
-                            goto out;
-                        }
+                        if (!empty_seen)
+                            wait_on(tempty_at + set.at * 8, set.phase ^ 1, p.limit_ns, p.err, abort);
                         tc_fence_after();
                         Place<Cf::SETS> after = set;
                         after.advance();
@@ -376,14 +375,12 @@ __device__ __forceinline__ void issue_all(const Params &p, uint32_t smem0, uint3
                         set.advance();
                     }
                 }
-            any = true;
             if (elected)
                 commit<PAIR>(empty + stage.at, pair_mask);
             stage = next;
         }
     }
-out:
-    if (any) {
+    if (nstages > 0 && unit < p.tiles) {
         if (elected)
             commit<PAIR>(drain, pair_mask & (~pair_mask + 1));  // the even CTA
         volatile int no_abort = 0;
@@ -579,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t empty_at = smem_u32(empty);
         const uint32_t full_at =
             PAIR ? mapa_shared(smem_u32(full), leader) : smem_u32(full);
-        bool ok = true;
         uint32_t written = 0;  // the stage stored and not yet published: its barrier
         auto publish = [&]() {
             if (written) {
@@ -604,20 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t src0 = base + Cf::OFF_RAW + (uint32_t)(tid * 64 + ((tid & 6) << 3));
             const uint32_t dst0 = base + (uint32_t)(tid * 128 + ((tid & 7) << 4));
             auto load = [&]() {
-                if (!wait_warp(false, raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
-                    give_up(p.err, abort);
-                    return false;
-                }
+                wait_on(raw_full_at + raw.at * 8, raw.phase, p.limit_ns, p.err, abort);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     q[c] = lds128((src0 + raw.at * RAW_BYTES) ^ (uint32_t)(c << 4));
-                return true;
             };
             Place<Cf::STAGES> stage;
             int first = d;           // this warpgroup's first block of the tile
             uint32_t tile_stage = 0;  // stages of the tiles before
 #pragma unroll 1
-            for (int t = unit; t < p.tiles && ok; t += units) {
+            for (int t = unit; t < p.tiles; t += units) {
                 int l0, c0;
                 tile_origin<NT>(t, p.lanes, p.cols, l0, c0);
                 const int n = min(l0 + lane_half + tid, p.lanes - 1);  // past the end: any zero point
@@ -644,10 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int a = 0; a < ZERO_SLOTS - 1; ++a)
                         fetch(a);
                 if (first < nblocks)
-                    ok = load();
+                    load();
                 int i = first;
 #pragma unroll 1
-                for (; ok && i < nblocks; i += Cf::DW) {
+                for (; i < nblocks; i += Cf::DW) {
                     uint32_t zz[4];
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
@@ -690,19 +682,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0)
                                 arrive(raw_empty_at + raw.at * 8);
                             raw.advance(Cf::DW);
-                            if (i + Cf::DW < nblocks && !load()) {
-                                ok = false;
-                                break;
-                            }
+                            if (i + Cf::DW < nblocks)
+                                load();
                         }
                         if (2 * i + h >= nstages)
                             break;
-                        if (!wait_warp(free, empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns,
-                                       abort)) {
-                            give_up(p.err, abort);
-                            ok = false;
-                            break;
-                        }
+                        if (!free)
+                            wait_on(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, p.err,
+                                    abort);
                         const uint32_t dst = dst0 + stage.at * Cf::STAGE_BYTES;
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
@@ -726,22 +713,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tiles = unit < p.tiles ? (p.tiles - unit + units - 1) / units : 0;
             const int total = tiles * nstages;  // stages of this CTA, tile after tile
             auto load = [&]() {
-                if (!wait_warp(false, raw_full_at + raw.at * 8, raw.phase, p.limit_ns, abort)) {
-                    give_up(p.err, abort);
-                    return false;
-                }
+                wait_on(raw_full_at + raw.at * 8, raw.phase, p.limit_ns, p.err, abort);
                 const uint32_t src = src0 + raw.at * RAW_BYTES;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     q[j] = lds128(src + j * 16 * 128);
-                return true;
             };
             Place<Cf::STAGES> stage;
             stage.at = d;
             if (d < total)
-                ok = load();
+                load();
 #pragma unroll 1
-            for (int sn = d; ok && sn < total; sn += Cf::DW) {
+            for (int sn = d; sn < total; sn += Cf::DW) {
                 const bool free = peek(empty_at + stage.at * 8, stage.phase ^ 1);
                 uint4 v[8];
 #pragma unroll
@@ -757,12 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0)
                     arrive(raw_empty_at + raw.at * 8);
                 raw.advance(Cf::DW);
-                if (sn + Cf::DW < total && !load())
-                    break;
-                if (!wait_warp(free, empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, abort)) {
-                    give_up(p.err, abort);
-                    break;
-                }
+                if (sn + Cf::DW < total)
+                    load();
+                if (!free)
+                    wait_on(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, p.err, abort);
                 const uint32_t dst = dst0 + stage.at * Cf::STAGE_BYTES;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // rows 16 apart share the swizzle phase
@@ -785,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tfull_at = smem_u32(tfull);
         const uint32_t tempty_at =
             PAIR ? mapa_shared(smem_u32(tempty), leader) : smem_u32(tempty);
-        bool ok = true, seen = false;
+        bool seen = false;
         uint32_t set = 0, set_phase = 0;
         int l0 = 0, c0 = 0;
         uintptr_t sp = 0;    // this lane's next scale to copy
@@ -812,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             start(unit);
         float acc[Cf::CPT];
 #pragma unroll 1
-        for (int t = unit; t < p.tiles && ok; t += units) {
+        for (int t = unit; t < p.tiles; t += units) {
 #pragma unroll
             for (int j = 0; j < Cf::CPT; ++j)
                 acc[j] = 0.f;
@@ -829,11 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     s = __uint_as_float(word);
                 }
-                if (!wait_warp(seen, tfull_at + set * 8, set_phase, p.limit_ns, abort)) {
-                    give_up(p.err, abort);
-                    ok = false;
-                    break;
-                }
+                if (!seen)
+                    wait_on(tfull_at + set * 8, set_phase, p.limit_ns, p.err, abort);
                 tc_fence_after();
                 if constexpr (PAIR)  // (the other tiles' groups come too slowly for it to help)
                     seen = set + 1 == Cf::SETS ? peek(tfull_at, set_phase ^ 1)
@@ -861,8 +839,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     set_phase ^= 1;
                 }
             }
-            if (!ok)
-                break;
             if (S > 1) {
                 const uint32_t part =
                     smem_u32(smem) + (uint32_t)(row * Cf::PITCH + pw * Cf::CPT) * 4u;
