@@ -33,7 +33,14 @@ constexpr int TN = 64;       // columns of a 4-bit tile
 constexpr int PITCH = 66;    // 2-byte values per tile row in shared memory: the four
                              // quarters of a block (8 rows apart) fall 8 banks apart
 
-enum { kWeights, kCodes };   // what a 4-bit tile is made from
+// Rounding and conversion by addition, on the full-rate pipe (the conversion
+// instructions issue at a quarter of it or less: both directions at 8192 x 8192
+// took 90 us with them). 1.5 * 2^23 has ulp 1: adding it rounds a small value to
+// the nearest integer, halves to even, and leaves that integer in the low bits.
+// 2^23 with an integer in its low bits is the way back.
+constexpr float kRound = 12582912.f;
+constexpr uint32_t kTwo23 = 0x4b000000u;
+constexpr float kTwo23f = 8388608.f;
 
 // Rows k0 .. k0+127, columns n0 .. n0+63 of W into shared memory, zeros outside.
 template <typename E, bool VEC>
@@ -117,14 +124,15 @@ __global__ void __launch_bounds__(kThreads)
         float z = 8.f;
         if constexpr (ZEROS)
             z = fminf(fmaxf(rintf(__fmul_rn(-lo, inv)), 0.f), 15.f);
+        const float least = kRound - z, most = least + 15.f;  // codes 0 and 15, before z is added
+        const uint32_t zi = (uint32_t)z;
 #pragma unroll
         for (int w = 0; w < WORDS; ++w) {
             uint32_t word = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float q =
-                    fminf(fmaxf(__fadd_rn(rintf(__fmul_rn(v[w][i], inv)), z), 0.f), 15.f);
-                word |= (uint32_t)q << w4_shift(i);
+                const float q = __fadd_rn(__fmul_rn(v[w][i], inv), kRound);
+                word |= (__float_as_uint(fminf(fmaxf(q, least), most)) + zi & 15u) << w4_shift(i);
             }
             out[g * WORDS + w] = word;
         }
@@ -132,7 +140,7 @@ __global__ void __launch_bounds__(kThreads)
         if (c == 0 && n < N && k < K) {
             scales[k / GROUP * N + n] = sbits;
             if constexpr (ZEROS)
-                zeros[k / GROUP * N + n] = (uint8_t)z;
+                zeros[k / GROUP * N + n] = (uint8_t)zi;
         }
     }
     if (n < N)
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads)
         const uint4 v = __ldg(reinterpret_cast<const uint4 *>(codes + n * w4_row_bytes(K) +
                                                               kb * kW4BlockBytes + c * 16));
         const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-        float s = 0.f, z = 8.f;
+        float s = 0.f, z = kTwo23f + 8.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             if (w % (GROUP / 32) == 0) {
@@ -188,12 +196,12 @@ __global__ void __launch_bounds__(kThreads)
                 if (k < K) {
                     s = to_f32<F16>(__ldg(scales + k / GROUP * N + n));
                     if (zeros)
-                        z = (float)(__ldg(zeros + k / GROUP * N + n) & 15);
+                        z = __uint_as_float(kTwo23 | (__ldg(zeros + k / GROUP * N + n) & 15u));
                 }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float q = (float)((words[w] >> w4_shift(i)) & 15u);
+                const float q = __uint_as_float(and_or(words[w] >> w4_shift(i), 15u, kTwo23));
                 tile[w * 32 + 8 * c + i][col] = from_f32<F16>((q - z) * s);
             }
         }
@@ -281,12 +289,15 @@ __global__ void __launch_bounds__(kThreads)
     }
     const uint32_t tw[4] = {top.x, top.y, top.z, top.w};
     float inv[8];
+    uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};  // of two columns each: 0 where the scale is NaN
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float amax = to_f32<F16>((uint16_t)(tw[j >> 1] >> (16 * (j & 1))));
         float s = __fmul_rn(amax, 1.0f / 127.0f);
         s = amax < 0x1p-100f ? 0.f : amax <= 3.402823466e38f ? s : __int_as_float(0x7fffffff);
-        inv[j] = s > 0.f ? __frcp_rn(s) : 0.f;  // zero and NaN scales: codes 0
+        inv[j] = s > 0.f ? __frcp_rn(s) : 0.f;  // codes 0 for scales of 0 and NaN
+        if (!(s >= 0.f))
+            keep[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
         if (r0 == 0 && col + j < K)
             scales[mb * K + col + j] = s;
     }
@@ -298,15 +309,20 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t m = m0 + r0 + 16 * p;
         if (m >= M)
             break;
-        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-        uint32_t b[2] = {0u, 0u};
+        const uint32_t w[4] = {v[p].x & keep[0], v[p].y & keep[1], v[p].z & keep[2],
+                               v[p].w & keep[3]};
+        uint32_t q[8];  // the code in the low byte
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x = to_f32<F16>((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-            const int q = min(max(__float2int_rn(__fmul_rn(x, inv[j])), -127), 127);
-            b[j >> 2] |= ((uint32_t)q & 255u) << (8 * (j & 3));
+            const float r = __fadd_rn(__fmul_rn(x, inv[j]), kRound);
+            q[j] = __float_as_uint(fminf(fmaxf(r, kRound - 127.f), kRound + 127.f));
         }
-        *reinterpret_cast<uint2 *>(codes + m * pitch + col) = make_uint2(b[0], b[1]);
+        auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+        };
+        *reinterpret_cast<uint2 *>(codes + m * pitch + col) =
+            make_uint2(four(q[0], q[1], q[2], q[3]), four(q[4], q[5], q[6], q[7]));
     }
 }
 
@@ -339,8 +355,11 @@ __global__ void __launch_bounds__(kThreads)
             break;
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = (float)(int8_t)((j < 4 ? v[p].x : v[p].y) >> (8 * (j & 3))) * s[j];
+        for (int j = 0; j < 8; ++j) {  // code + 128 in the low byte of 2^23
+            const uint32_t u = __byte_perm((j < 4 ? v[p].x : v[p].y) ^ 0x80808080u, kTwo23,
+                                           0x7440 | (j & 3));
+            x[j] = (__uint_as_float(u) - (kTwo23f + 128.f)) * s[j];
+        }
         uint16_t *dst = X + m * K + col;
         if constexpr (VEC) {
             *reinterpret_cast<uint4 *>(dst) =
