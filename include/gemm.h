@@ -360,8 +360,8 @@ GEMM_API int gemm_f16f32_ws(int64_t M, int64_t N, int64_t K,
  * so both products are those of the stored values, (q - z) * s or q * s, with
  * fp32 accumulation: only the order of the sums differs from the definition.
  * Layout, ownership, streams, degenerate shapes, thread safety and CUDA graphs
- * are as for the products above (row-major, packed, asynchronous); one matrix
- * has at most 2^40 elements, and what a call writes must not overlap what it
+ * are as for the products above (row-major, packed, asynchronous); one
+ * dimension is at most 2^31 - 256, one matrix at most 2^40 elements, and what a call writes must not overlap what it
  * reads or, for the two-output conversions, its other outputs.
  *
  * 4-bit weights (w4). W (K x N) in groups of `group` (32, 64 or 128)

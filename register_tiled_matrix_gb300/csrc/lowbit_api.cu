@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxDim = 0x7fffff00;  // sizes rounded up to a tile stay below 2^31
 constexpr int64_t kMaxElements = (int64_t)1 << 40;  // of one matrix
 
 bool size_ok(int64_t rows, int64_t cols)

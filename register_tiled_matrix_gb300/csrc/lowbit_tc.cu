@@ -26,7 +26,8 @@
 //    lane's scale, add it to fp32 totals in registers, and at the end of the
 //    tile store them.
 // Scales and zero points are 4-byte asynchronous copies that each thread makes
-// for itself many groups ahead. Registers move between the warpgroups: few for
+// for itself many groups ahead (the aligned word around a value of 2 bytes or
+// one: it holds a byte of the array, so it lies in the array's pages). Registers move between the warpgroups: few for
 // the issuing threads, most for the promoting ones, which keep up to 128 totals.
 //
 // With few tiles the depth is split over S CTAs of a cluster; their totals meet
@@ -53,7 +54,7 @@ constexpr int LANES = 128;
 constexpr int BK = 64;        // depth of a stage: 64 2-byte values = a 128-byte swizzle row
 constexpr int BLOCK = 128;    // depth of a raw w4 slot, and the granularity of a split
 constexpr int UMMA_K = 16;
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;  // four warpgroups: issuing, and three that convert or promote
 constexpr uint32_t A_BYTES = LANES * BK * 2;   // 16 KB
 constexpr uint32_t ATOM_BYTES = 64 * BK * 2;   // 8 KB: 64 columns x 64 depth, MN-major
 constexpr uint32_t RAW_BYTES = 8192;           // w4: 128 lanes x 64 B; q8: 64 rows x 128 B
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dst0 = base + (uint32_t)(chunk >> 2) * ATOM_BYTES +
                                   (uint32_t)row * 128u + (((2u * (chunk & 3)) ^ (row & 7u)) << 4);
             const int tiles = unit < p.tiles ? (p.tiles - unit + units - 1) / units : 0;
-            const int total = tiles * nstages;  // stages of this CTA, tile after tile
+            const int64_t total = (int64_t)tiles * nstages;  // stages of this CTA, tile after tile
             auto load = [&]() {
                 wait_on(raw_full_at + raw.at * 8, raw.phase, p.limit_ns, p.err, abort);
                 const uint32_t src = src0 + raw.at * RAW_BYTES;
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (d < total)
                 load();
 #pragma unroll 1
-            for (int sn = d; sn < total; sn += Cf::DW) {
+            for (int64_t sn = d; sn < total; sn += Cf::DW) {
                 const bool free = peek(empty_at + stage.at * 8, stage.phase ^ 1);
                 uint4 v[8];
 #pragma unroll

@@ -32,6 +32,7 @@ def test_w4_product_arguments(lib, fn):
     f = getattr(lib, fn)
     assert f(-1, 8, 8, A, B, C, D, 128, E, 0, 0, None) == -1
     assert f(8, 8, 1 << 31, A, B, C, D, 128, E, 0, 0, None) == -1
+    assert f(8, 8, (1 << 31) - 255, A, B, C, D, 128, E, 0, 0, None) == -1
     for group in (0, 16, 96, 256):
         assert f(8, 8, 256, A, B, C, D, group, E, 0, 0, None) == -1
     assert f(0, 8, 8, 0, 0, 0, 0, 128, 0, 0, 0, None) == 0
