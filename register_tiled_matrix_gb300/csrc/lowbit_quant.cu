@@ -4,6 +4,11 @@
 // block reads its tile once in 16-byte loads, keeps it on chip (shared memory
 // where the tile changes orientation, registers elsewhere) and writes once.
 //
+// At 8192 x 8192: w4 quantise 50 us (0.50 of the measured copy rate: some 15
+// instructions a weight, two bytes at a time from shared memory) and dequantise
+// 37 us (0.67), q8 quantise 47 us (0.63: three blocks of 76 registers to an SM,
+// each waiting for its tile before it converts) and dequantise 34 us (0.88).
+//
 // 4-bit weights, W (K x N) in groups of `group` k of one column n:
 //     hi = max(0, max w), lo = min(0, min w)
 //     with zero points:    s = round_type((hi - lo) * (1/15)), z = rint(-lo / s)

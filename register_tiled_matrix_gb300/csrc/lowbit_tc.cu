@@ -35,6 +35,16 @@
 // memory, so results repeat exactly. Without a split the CTAs are persistent,
 // and the stores of one tile overlap the multiplications of the next.
 //
+// What bounds it: 4096 x 8192 x 8192 (w4) takes 0.41 ms and an 8192^3 weight
+// gradient 0.85 ms, 1330 and 1290 TFLOP/s, 0.69 and 0.67 of the measured bf16
+// rate; at 4096^3 the tensor pipe is active half of the time and no unit more. A
+// stage passes through four roles, each a chain of shared-memory round trips of
+// 130 to 190 cycles, and costs some 850 cycles where its MMAs take 512. Tried and
+// slower: one CTA of 128 x 256 (twice the L2 reads of the 2-byte operand: 0.77 and
+// 1.58 ms), a forwarding thread with cluster-scope releases in the odd CTA (1.64
+// ms), an MMA loop rolled over the steps (1.14 ms), two CTAs an SM at NT <= 64
+// (64 x 8192 x 8192 38 us against 31).
+//
 // Every wait is bounded: a thread that gives up records GEMM_ERR_TIMEOUT in the
 // device error word, and all threads still reach the barriers at the end.
 #include <cstdint>
@@ -976,11 +986,15 @@ static cudaError_t launch_nt(Params p, const CUtensorMap &codes, const CUtensorM
     if (tiles > 0x1fffffff)
         return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
-    // Few tiles: split the depth while every CTA keeps at least four blocks
-    // and all clusters (of at most 8 CTAs) are resident at once.
+    // Few tiles: split the depth while every CTA keeps at least two blocks (a pair
+    // four) and all clusters (of at most 8 CTAs) are resident at once. Single CTAs
+    // of two blocks against four: w4 24 x 1024 x 1024 7.6 and 8.8 us, 64 x 4096 x
+    // 1024 9.8 and 10.7 us; pairs: w4 300 x 1000 x 504 16.2 and 14.0 us, q8t with
+    // 1024 tokens of 1024 x 512 18.0 and 17.1 us.
+    constexpr int LEAST = Cf::PAIR ? 4 : 2;
     const int blocks = (p.depth + BLOCK - 1) / BLOCK;
     int splits = 1;
-    while (splits * CTAS < 8 && tiles * splits * CTAS * 2 <= sms && blocks >= splits * 2 * 4)
+    while (splits * CTAS < 8 && tiles * splits * CTAS * 2 <= sms && blocks >= splits * 2 * LEAST)
         splits *= 2;
     static std::atomic<int> resident[4][64] = {};  // clusters of 1, 2, 4, 8
     int fit = sms;
