@@ -115,6 +115,7 @@ struct Params {
     int splits;  // CTAs (pairs) of a cluster, each summing a range of the depth
     int tiles;
     int mute;    // failure-detection self-test: issue no loads
+    uint32_t nil;  // 0, which the compiler cannot know (free_slot)
     int c_vec;   // q8t: rows of dW on 16-byte boundaries
 };
 
@@ -273,6 +274,20 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
                  "r"(v.z), "r"(v.w)
                  : "memory");
+}
+
+// Gives a raw slot back to the copies once this warp has its words q, one load
+// instruction each. Neither the order of the source nor the arrival's release holds
+// back a load whose registers no instruction has asked for yet, and the next copy
+// overtook such loads (whole blocks of the slot's next codes appeared). So the
+// arrival asks for them: its address is made of a word of each load, masked by
+// `nil`, and the vote asks for every lane's.
+__device__ __forceinline__ void free_slot(uint32_t bar, const uint4 (&q)[4], uint32_t nil, int lane)
+{
+    const uint32_t words = q[0].x ^ q[1].x ^ q[2].x ^ q[3].x;
+    const uint32_t none = __any_sync(0xffffffffu, (words & nil) != 0) ? 8u : 0u;
+    if (lane == 0)
+        arrive(bar + none);
 }
 
 // First lane and column of a tile, in bands of 2048 lanes, so that the tiles in
@@ -686,12 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         publish();
                         if (h == 1) {
-                            // The words are used: free the slot, load the next one's. (An
-                            // arrival before the first use of the loaded words let the
-                            // next copy overtake the loads.)
-                            __syncwarp();
-                            if (lane == 0)
-                                arrive(raw_empty_at + raw.at * 8);
+                            free_slot(raw_empty_at + raw.at * 8, q, p.nil, lane);
                             raw.advance(Cf::DW);
                             if (i + Cf::DW < nblocks)
                                 load();
@@ -746,10 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[2 * j + 1] = make_uint4(c.x, c.y, e.x, e.y);
                 }
                 publish();
-                // The words are used: free the slot, load the next one's.
-                __syncwarp();
-                if (lane == 0)
-                    arrive(raw_empty_at + raw.at * 8);
+                free_slot(raw_empty_at + raw.at * 8, q, p.nil, lane);
                 raw.advance(Cf::DW);
                 if (sn + Cf::DW < total)
                     load();
