@@ -594,7 +594,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_all<MODE, F16, NT, 2>(p, smem_u32(smem), tmem_base, unit, units, nstages, depth,
                                          pair_mask, full, empty, tfull, tempty, drain, abort);
         }
-        __syncwarp();
     } else if (wg <= Cf::DW) {
         // ------------------------------------------------ dequantise
         // Warpgroup d takes every DW-th raw slot, in order.
@@ -835,6 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!seen)
                     wait_on(tfull_at + set * 8, set_phase, p.limit_ns, p.err, abort);
+                __syncwarp();  // the lanes left the wait each for itself; the load is the warp's
                 tc_fence_after();
                 if constexpr (PAIR)  // (the other tiles' groups come too slowly for it to help)
                     seen = set + 1 == Cf::SETS ? peek(tfull_at, set_phase ^ 1)
@@ -903,6 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         cp_async_wait<0>();
     }
+    __syncwarp();  // the barriers below are the whole warp's
 
     if (S > 1) {
         cluster_sync();  // every partial tile of the cluster is in shared memory

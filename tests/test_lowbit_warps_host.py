@@ -1,0 +1,31 @@
+"""Instructions of the low-bit tensor-core kernel that a whole warp must execute together
+follow a __syncwarp() where its lanes may have left a wait each for itself. Read
+from the source: no run can show that the compiler will go on reuniting them."""
+
+import os
+import re
+
+import pytest
+
+pytestmark = pytest.mark.cpu
+SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                      "register_tiled_matrix_gb300", "csrc", "lowbit_tc.cu")
+
+
+def kernel():
+    text = re.sub(r"//[^\n]*", "", open(SOURCE).read())
+    return text[text.index("lowbit_tc_kernel("):text.index("CUresult (*EncodeTiledFn)")]
+
+
+def test_tensor_memory_loads():
+    text = kernel()
+    load = text.index("tmem_ld_32x32b_x32(")
+    wait = text.rindex("wait_on(", 0, load)
+    assert "__syncwarp();" in text[wait:load]
+
+
+def test_barriers_after_the_roles():
+    text = kernel()
+    roles = text.index("if (wg == 0)")
+    between = text[text.rindex("cp_async_wait<0>();"):text.index("cluster_sync();", roles)]
+    assert "__syncwarp();" in between
