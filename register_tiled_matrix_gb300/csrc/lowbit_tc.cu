@@ -577,11 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (*abort) {  // copies that no MMA waited for get time to land
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 200000ull) {
-                }
-            }
         } else if (warp == 1 && even) {
             // ------------------------------------------------ MMA issuer
             if (MODE == kQ8t || p.group == 128)
@@ -953,6 +948,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    // No copy into this CTA's shared memory may outlive it. The MMAs waited for every
+    // stage's bytes, unless a role gave up: then copies that nobody waited for get
+    // the time of a wait to land. (A pair's CTAs leave together, below.)
+    if (threadIdx.x == 0 && *abort) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < p.limit_ns) {
+        }
+    }
+    __syncwarp();
     if constexpr (PAIR)
         cluster_sync();  // no CTA leaves while its peer may still signal or read it
     if (warp == 1) {

@@ -29,3 +29,12 @@ def test_barriers_after_the_roles():
     roles = text.index("if (wg == 0)")
     between = text[text.rindex("cp_async_wait<0>();"):text.index("cluster_sync();", roles)]
     assert "__syncwarp();" in between
+
+
+def test_copies_do_not_outlive_their_block():
+    """After a timeout a CTA stays, once all its roles are through, for as long as a wait may
+    take (a copy that is late cannot be made to order)."""
+    text = kernel()
+    end = text[text.rindex("__syncthreads();"):]
+    stay = re.search(r"if \(threadIdx.x == 0 && \*abort\) \{[^}]*< p\.limit_ns\)", end)
+    assert stay and stay.start() < end.index("cluster_sync();")
