@@ -384,6 +384,7 @@ GEMM_API int gemm_f16f32_ws(int64_t M, int64_t N, int64_t K,
  * w) over a group: s = (hi - lo) * (1/15) rounded to W's type, z = rint(-lo *
  * (1/s)) clamped to 0..15; without zero points s = max|w| * (1/7) rounded, z =
  * 8. q = clamp(rint(w * (1/s)) + z, 0, 15), every step in fp32, halves to even.
+ * Where hi - lo is beyond fp32, s = hi * (1/15) - lo * (1/15) rounded.
  * A scale that rounds below 2^-126 is 0, with q = z (0 with zero points, 8
  * without). A group with a weight that is not finite gets a NaN scale.
  *

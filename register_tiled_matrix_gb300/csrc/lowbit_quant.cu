@@ -12,6 +12,7 @@
 // 4-bit weights, W (K x N) in groups of `group` k of one column n:
 //     hi = max(0, max w), lo = min(0, min w)
 //     with zero points:    s = round_type((hi - lo) * (1/15)), z = rint(-lo / s)
+//                          (hi * (1/15) - lo * (1/15) where hi - lo is beyond fp32)
 //     without:             s = round_type(max |w| * (1/7)),    z = 8
 //     q = clamp(rint(w / s) + z, 0, 15), and W is read back as (q - z) * s.
 // The scale is rounded to the weights' type before it divides, so the codes fit
@@ -119,9 +120,13 @@ __global__ void __launch_bounds__(kThreads)
             lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
             bad += __shfl_xor_sync(0xffffffffu, bad, d);
         }
+        constexpr float PART = ZEROS ? 1.0f / 15.0f : 1.0f / 7.0f;
         const float range = ZEROS ? hi - lo : fmaxf(hi, -lo);
-        uint16_t sbits =
-            from_f32<F16>(__fadd_rn(__fmul_rn(range, ZEROS ? 1.0f / 15.0f : 1.0f / 7.0f), bad));
+        float part = __fmul_rn(range, PART);
+        if constexpr (ZEROS && !F16)
+            if (range > 3.402823466e38f)  // beyond fp32, though hi and lo are not
+                part = __fsub_rn(__fmul_rn(hi, PART), __fmul_rn(lo, PART));
+        uint16_t sbits = from_f32<F16>(__fadd_rn(part, bad));
         if (to_f32<F16>(sbits) < 0x1p-126f)
             sbits = 0;  // its reciprocal would leave the fp32 range
         const float s = to_f32<F16>(sbits);
