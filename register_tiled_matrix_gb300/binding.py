@@ -404,6 +404,7 @@ def _w4_check(codes, scales, zeros, K: int, group: int, device) -> int:
     N = _matrix("codes", codes)[0]
     _need("codes", codes, torch.uint8, (N, (K + W4_BLOCK - 1) // W4_BLOCK * 64), device)
     meta = ((K + group - 1) // group, N)
+    _matrix("scales", scales)
     _type_name(scales.dtype)
     _need("scales", scales, scales.dtype, meta, device)
     if zeros is not None:
@@ -444,7 +445,8 @@ def gemm_w4_dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: Optiona
                        K: int, group: int = 128, out: Optional[torch.Tensor] = None,
                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The K x N weight (q - z) * s in the scales' type."""
-    N = _w4_check(codes, scales, zeros, K, group, scales.device)
+    _matrix("codes", codes)
+    N = _w4_check(codes, scales, zeros, K, group, codes.device)
     if out is None:
         out = _empty(codes, (K, N), scales.dtype, stream)
     else:
@@ -464,8 +466,8 @@ def _workspace(workspace: Optional[torch.Tensor], operand: torch.Tensor, entry: 
         if need <= 0:
             return 0, 0, None
         workspace = _empty(operand, (need,), torch.uint8, stream)
-    elif (not workspace.is_cuda or workspace.device != operand.device
-          or not workspace.is_contiguous()):
+    elif (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda
+          or workspace.device != operand.device or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {operand.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
@@ -487,7 +489,7 @@ def _w4_product(entry: str, dtype: torch.dtype, A, codes, scales, zeros, group, 
     if not fine:
         M, K = _matrix("A", A)
         _need("A", A, dtype, (M, K))
-        _need("scales", scales, dtype, scales.shape, A.device)
+        _need("scales", scales, dtype, _matrix("scales", scales), A.device)
         N = _w4_check(codes, scales, zeros, K, group, A.device)
     if out is None:
         out = _empty(A, (M, N), torch.float32, stream)
@@ -550,7 +552,8 @@ def gemm_q8_dequantize(codes: torch.Tensor, scales: torch.Tensor, M: int, K: int
                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The saved M x K activation, codes * scales, in `dtype` (bf16 or fp16)."""
     name = _type_name(dtype)
-    _q8_check(codes, scales, M, K, scales.device)
+    _matrix("codes", codes)
+    _q8_check(codes, scales, M, K, codes.device)
     if out is None:
         out = _empty(codes, (M, K), dtype, stream)
     else:
