@@ -308,13 +308,22 @@ __device__ __forceinline__ void tile_origin(int t, int lanes, int cols, int &l0,
     c0 = in / rows * NT;
 }
 
-// Arrive on the leading CTA's barrier. Nothing this CTA wrote is read through
-// the leader: the tensor core of this SM reads the stage (made visible to it by
-// fence.proxy.async) and tensor memory, so the arrival needs no release at
-// cluster scope. With one, by a thread that forwarded each stage, the pair ran
-// at 0.9 us a stage (8192^3: 1.64 ms).
+// "This warp's part of a stage is written" to the leading CTA, whose thread issues the
+// MMAs. See mbar_arrive_cluster_stage_written for why it is no release at cluster scope: with
+// one, 4096 x 8192 x 8192 (w4) takes 802 us and an 8192^3 weight gradient 2204 us (408
+// and 860 without).
 template <bool PAIR>
-__device__ __forceinline__ void arrive_leader(uint32_t bar)
+__device__ __forceinline__ void arrive_stage(uint32_t bar)
+{
+    if constexpr (PAIR)
+        mbar_arrive_cluster_stage_written(bar);
+    else
+        arrive(bar);
+}
+
+// "This warp has read its part of an accumulation set" to the leading CTA.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_set(uint32_t bar)
 {
     if constexpr (PAIR)
         mbar_arrive_cluster_tmem_free(bar);
@@ -607,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0)
-                    arrive_leader<PAIR>(written);
+                    arrive_stage<PAIR>(written);
                 written = 0;
             }
         };
@@ -845,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            arrive_leader<PAIR>(tempty_at + set * 8);
+                            arrive_set<PAIR>(tempty_at + set * 8);
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)

@@ -370,6 +370,18 @@ __device__ __forceinline__ void mbar_arrive_cluster_tmem_free(uint32_t cluster_a
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Arrive on the leading CTA's mbarrier to say "this warp's part of a stage is in the
+// shared memory of its own CTA", after fence.proxy.async by every writer and a
+// __syncwarp. The waiting thread reads none of it: it issues the pair's MMA, and the
+// tensor core of the writer's own SM reads the stage through the async proxy, which
+// the fence has made the writes visible to. So the arrival carries no memory across
+// CTAs and CTA scope suffices; what a thread of the other CTA is to read needs
+// mbar_arrive_cluster.
+__device__ __forceinline__ void mbar_arrive_cluster_stage_written(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // 2-D tiled load into this CTA's shared memory whose completion is signalled
 // on an mbarrier in either CTA of the pair (shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap,

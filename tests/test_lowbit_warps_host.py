@@ -38,3 +38,15 @@ def test_copies_do_not_outlive_their_block():
     end = text[text.rindex("__syncthreads();"):]
     stay = re.search(r"if \(threadIdx.x == 0 && \*abort\) \{[^}]*< p\.limit_ns\)", end)
     assert stay and stay.start() < end.index("cluster_sync();")
+
+
+def test_arrivals_across_a_pair():
+    """Each arrival at the leading CTA says what its helper's contract covers."""
+    whole = re.sub(r"//[^\n]*", "", open(SOURCE).read())
+    assert whole.count("mbar_arrive_cluster_tmem_free(") == 1
+    assert whole.count("mbar_arrive_cluster_stage_written(") == 1
+    text = kernel()
+    assert len(re.findall(r"arrive_set<PAIR>\(tempty_at", text)) == 1
+    publish = text[text.index("auto publish"):text.index("arrive_stage<PAIR>(written)")]
+    assert publish.index("fence_proxy_async_shared();") < publish.index("__syncwarp();")
+    assert text.count("arrive_stage<PAIR>(") == 1
