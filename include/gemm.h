@@ -356,13 +356,19 @@ GEMM_API int gemm_f16f32_ws(int64_t M, int64_t N, int64_t K,
 /*
  * Products with an operand held in fewer bits: weights in 4 bits for serving,
  * saved activations in 8 bits for the backward pass. The codes are small
- * integers, exact in bf16 and fp16, and their scales are applied to fp32 sums,
- * so both products are those of the stored values, (q - z) * s or q * s, with
- * fp32 accumulation: only the order of the sums differs from the definition.
+ * integers, exact in bf16 and fp16, and a group's scale is applied to the group's
+ * fp32 sum, so both products are those of the stored values, (q - z) * s or q *
+ * s, with fp32 accumulation. Where the scale stands shows only at the ends of the
+ * range: sums of unscaled codes are sure to be finite for |A| <= 2^117 (w4) and
+ * |dY| <= 2^113 (q8), which holds for every fp16 value; with larger bf16 values an
+ * output may be infinite or NaN although the stored values' product is finite. An
+ * infinite scale multiplies its group's sum: a code equal to the zero point does
+ * not make NaN by itself.
  * Layout, ownership, streams, degenerate shapes, thread safety and CUDA graphs
  * are as for the products above (row-major, packed, asynchronous); one
- * dimension is at most 2^31 - 256, one matrix at most 2^40 elements, and what a call writes must not overlap what it
- * reads or, for the two-output conversions, its other outputs.
+ * dimension is at most 2^31 - 256, one matrix at most 2^40 elements, and what a
+ * call writes must not overlap what it reads or, for the two-output conversions,
+ * its other outputs.
  *
  * 4-bit weights (w4). W (K x N) in groups of `group` (32, 64 or 128)
  * consecutive k of one column; the last group may be shorter. G = ceil(K /
@@ -389,7 +395,8 @@ GEMM_API int gemm_f16f32_ws(int64_t M, int64_t N, int64_t K,
  * without). A group with a weight that is not finite gets a NaN scale.
  *
  * gemm_bf16_w4_dequantize / gemm_f16_w4_dequantize — W back, (q - z) * s in
- * fp32 rounded once to its type.
+ * fp32 rounded once to its type: within a step of the type's largest value a weight
+ * may come back infinite.
  *
  * gemm_w4_pack — codes of weights quantised elsewhere: `q` is K x N, one code a
  * byte (its low four bits); writes the layout above.
@@ -424,6 +431,9 @@ GEMM_API int gemm_f16_w4_dequantize(int64_t K, int64_t N, int group, const uint8
  * overlapping nothing; 0 for M <= 16), and where it is null or too small the
  * product runs on the FP32 pipes, many times slower. The contents of the
  * workspace on return are unspecified; two calls in flight must not share one.
+ * The tensor-core path reads scales and zeros in aligned 4-byte words: up to three
+ * bytes before and after each array are read too (never used or written), in a
+ * word that holds a byte of the array.
  */
 GEMM_API int64_t gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 GEMM_API int gemm_bf16w4f32(int64_t M, int64_t N, int64_t K, const uint16_t *A,
