@@ -143,12 +143,11 @@ __global__ void __launch_bounds__(kThreads, NB == 2 ? 1 : T == 1 && V == 8 && GS
     extern __shared__ __align__(256) uint8_t shared[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
-    const int n0 = blockIdx.x * (16 * T), m0 = blockIdx.y * (8 * NB);
+    const int n0 = blockIdx.x * (16 * T);
     const int blocks = (p.K + kW4Block - 1) / kW4Block;
     const int G = (p.K + GROUP - 1) / GROUP;
-    const int xrows = min(p.M, 8 * NB);
-    const uint32_t slot = slot_bytes(T, xrows);
-    const uint32_t mine = smem_u32(shared) + warp * warp_bytes(T, xrows);
+    const uint32_t slot = slot_bytes(T, p.M);  // M <= 8 NB
+    const uint32_t mine = smem_u32(shared) + warp * warp_bytes(T, p.M);
     const uint32_t meta = mine + r * 8;
     const uint32_t ring = mine + S::META, codes = ring + lane * 16;
     // A's values for words 0 and 2 are at xring, + 128; for words 1 and 3 at xother, + 128.
@@ -165,13 +164,13 @@ __global__ void __launch_bounds__(kThreads, NB == 2 ? 1 : T == 1 && V == 8 && GS
             col[t][h] = min(n0 + 16 * t + 8 * h + r, p.N - 1);
             row[t][h] = p.codes + col[t][h] * pitch + (int64_t)warp * kW4BlockBytes + c * 16;
         }
-    // Rows of A: lanes of rows past M (in this block of rows) copy and read nothing.
+    // Rows of A: lanes of rows past M copy and read nothing.
     const uint16_t *a[NB];
     bool in[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        const int m = m0 + 8 * j + r;
-        in[j] = 8 * j + r < xrows && m < p.M;
+        const int m = 8 * j + r;
+        in[j] = m < p.M;
         a[j] = p.A + (int64_t)m * p.K + 8 * c + (int64_t)warp * kW4Block;
     }
     // Copies this warp's block `ahead` of the round (block b) to slot `at`.
@@ -327,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, NB == 2 ? 1 : T == 1 && V == 8 && GS
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             v += red[w][nn][mm];
-        if (n0 + nn < p.N && m0 + mm < p.M)
-            p.C[(int64_t)(m0 + mm) * p.N + n0 + nn] = v;
+        if (n0 + nn < p.N && mm < p.M)
+            p.C[(int64_t)mm * p.N + n0 + nn] = v;
     }
 }
 
@@ -342,10 +341,8 @@ static cudaError_t launch_kernel(const W4Launch &L, cudaStream_t stream)
         set_smem_limit_once(kernel, kWarps * (int)warp_bytes(T, 8 * NB), done, 100);
     if (e != cudaSuccess)
         return e;
-    const dim3 grid((unsigned)((L.N + 16 * T - 1) / (16 * T)),
-                    (unsigned)((L.M + 8 * NB - 1) / (8 * NB)));
-    const int rows = L.M < 8 * NB ? L.M : 8 * NB;
-    kernel<<<grid, kThreads, kWarps * warp_bytes(T, rows), stream>>>(L);
+    const unsigned grid = (unsigned)((L.N + 16 * T - 1) / (16 * T));
+    kernel<<<grid, kThreads, kWarps * warp_bytes(T, L.M), stream>>>(L);
     return cudaGetLastError();
 }
 
