@@ -67,8 +67,8 @@ cudaError_t launch_w4_tc(const W4Launch &L, int64_t lda, const DeviceContext &d,
 cudaError_t launch_q8t_tc(const Q8tLaunch &L, int64_t ldy, const DeviceContext &d, bool mute,
                           cudaStream_t stream);
 // w4_rows.cu: few rows of A (M <= kW4RowsMax), any alignment. 16 rows x 8192 x
-// 8192 take 18.7 us, on the tensor-core kernel 29 us; more rows take another pass
-// over W (24: 37 us against 29).
+// 8192 take 17.5 to 18.1 us, 17 rows on the tensor-core kernel 30 us; a second pass over W
+// for more rows was slower than that (24 rows: 37 us).
 constexpr int kW4RowsMax = 16;
 cudaError_t launch_w4_rows(const W4Launch &L, int sms, cudaStream_t stream);
 // lowbit_simt.cu: any alignment.

@@ -4,10 +4,11 @@
 // block reads its tile once in 16-byte loads, keeps it on chip (shared memory
 // where the tile changes orientation, registers elsewhere) and writes once.
 //
-// At 8192 x 8192: w4 quantise 50 us (0.50 of the measured copy rate: some 15
+// At 8192 x 8192: w4 quantise 47 to 50 us (0.50 to 0.53 of the measured copy rate: some 15
 // instructions a weight, two bytes at a time from shared memory) and dequantise
-// 37 us (0.67), q8 quantise 47 us (0.63: three blocks of 76 registers to an SM,
-// each waiting for its tile before it converts) and dequantise 34 us (0.88).
+// 35 to 37 us (0.67 to 0.72), pack 44 us (one byte at a time; 0.33), q8 quantise 45 to
+// 47 us (0.64 to 0.67: three blocks of 80 registers to an SM, each waiting for its
+// tile before it converts) and dequantise 32 to 34 us (0.88 to 0.94).
 //
 // 4-bit weights, W (K x N) in groups of `group` k of one column n:
 //     hi = max(0, max w), lo = min(0, min w)

@@ -2,7 +2,7 @@
 // thread, both operands turned into fp32 values as their 16-deep slices are
 // stored to shared memory. Every size and alignment; no workspace: for operands
 // whose rows are off 16-byte boundaries where the caller gives none. w4 4096 x
-// 8192 x 8192 takes 33 ms, q8t 8192^3 53 ms (tensor cores 0.41 and 0.85): each
+// 8192 x 8192 takes 33 ms, q8t 8192^3 53 ms (tensor cores 0.41 and 0.86): each
 // operand is decoded anew in every 64 x 64 tile.
 //
 //     w4:  C[m][n] = sum_k A[m][k] * (q[k][n] - z[g][n]) * s[g][n],  g = k / group

@@ -35,15 +35,16 @@
 // memory, so results repeat exactly. Without a split the CTAs are persistent,
 // and the stores of one tile overlap the multiplications of the next.
 //
-// What bounds it: 4096 x 8192 x 8192 (w4) takes 0.41 ms and an 8192^3 weight
-// gradient 0.85 ms, 1330 and 1290 TFLOP/s, 0.69 and 0.67 of the measured bf16
-// rate; at 4096^3 the tensor pipe is active half of the time and no unit more. A
-// stage passes through four roles, each a chain of shared-memory round trips of
-// 130 to 190 cycles, and costs some 850 cycles where its MMAs take 512. Tried and
-// slower: one CTA of 128 x 256 (twice the L2 reads of the 2-byte operand: 0.77 and
-// 1.58 ms), a forwarding thread with cluster-scope releases in the odd CTA (1.64
-// ms), an MMA loop rolled over the steps (1.14 ms), two CTAs an SM at NT <= 64
-// (64 x 8192 x 8192 38 us against 31).
+// What bounds it: 4096 x 8192 x 8192 (w4) takes 0.41 to 0.43 ms and an 8192^3 weight
+// gradient 0.86 to 0.91 ms, 1280 to 1350 and 1210 to 1280 TFLOP/s, 0.63 to 0.71 of the
+// measured bf16 rate; groups of 64 take 0.49, of 32 0.82 ms. At 4096^3 the tensor pipe is
+// active half of the time and no unit more. A stage passes through four roles, each a
+// chain of shared-memory round trips of 130 to 190 cycles, and costs some 850 cycles
+// where its MMAs take 512. Which role sets that pace is not measured; on CTA pairs one
+// warpgroup converts every stage. Tried and slower: one CTA of 128 x 256 (twice the L2
+// reads of the 2-byte operand: 0.77 and 1.58 ms), a forwarding thread with
+// cluster-scope releases in the odd CTA (1.64 ms), an MMA loop rolled over the steps
+// (1.14 ms), two CTAs an SM at NT <= 64 (64 x 8192 x 8192 38 us against 31).
 //
 // Every wait is bounded: a thread that gives up records GEMM_ERR_TIMEOUT in the
 // device error word, and all threads still reach the barriers at the end.

@@ -22,12 +22,14 @@
 // is fp32 and is scaled when it is added to the fp32 total. The eight warps'
 // totals are added in order through shared memory.
 //
-// What bounds it: 1 x 32768 x 8192 takes 34.6 us, 0.60 of the measured copy rate
-// (1 x 8192 x 8192 12.4 us, 1 x 1024 x 1024 1.9 us in a graph). 16 columns x 128 k
-// cost 167 warp instructions (88 decode), half of the issue slots; without
-// decoding and multiplying the copies alone took 31 to 35 us, whether a lane
-// group took 64 bytes of a row or a whole line, with rings of four or eight
-// blocks. Tried and no faster: a range of k to a warp in place of every eighth
+// What bounds it: 1 x 32768 x 8192 takes 33.0 us in a graph (35 us call by call), 0.59
+// to 0.63 of the measured copy rate (1 x 8192 x 8192 12.1 to 12.6 us, 16 x 8192 x 8192
+// 17.5 to 18.1 us, 1 x 1024 x 1024 2.1 us in a graph). 16 columns x 128 k cost 167 warp
+// instructions (88 decode), half of the issue slots; without decoding and multiplying
+// the copies of this launch alone took 31 to 35 us, whether a lane group took 64 bytes
+// of a row or a whole line, with rings of four or eight blocks: at K = 8192 a warp has
+// eight blocks of k, so a block of threads spends much of its time filling and draining
+// its rings, and 1 x 8192 x 8192 ends in a second wave of a few blocks. Tried and no faster: a range of k to a warp in place of every eighth
 // block (35 to 41 us), clusters over k, shifts on the multiplier pipe (43.6 us).
 #include <cstdint>
 #include <cuda_runtime.h>
