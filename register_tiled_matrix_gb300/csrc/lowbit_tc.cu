@@ -209,7 +209,10 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
 // other waits too) the roles run through their loops on whatever is there, in
 // bounds, so no lane leaves a loop that its mates stay in, and the result is
 // unspecified. A vote of the lanes after each wait cost 3 to 8 %, a flag of its own
-// in each thread 3 to 5 %.
+// in each thread 3 to 5 %. (After a copy that never lands, a barrier that waits for
+// its bytes may so see more arrivals than its phase counts: of a product that is void
+// already. Holding those arrivals back by a flag or sending them to spare barriers cost
+// 2 to 4 % of a product that waits for nothing.)
 __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, uint64_t limit_ns, int *err,
                                         volatile int *abort)
 {
