@@ -511,6 +511,194 @@ GEMM_API int gemm_q8tbf16f32_selftest_timeout(int64_t M, int64_t N, int64_t K,
                                               int64_t wait_limit_ns, void *stream);
 
 /*
+ * 8-bit floating-point operands (f8). Codes are e4m3 bytes (4 bits of exponent, 3 of mantissa,
+ * largest 448, no infinities), rows `ld` bytes apart: ld a multiple of 16, at least the row,
+ * codes 16-byte aligned; the bytes between a row's end and the next row may be anything. Each
+ * block of 128 shares an fp32 scale, and a code stands for code * scale:
+ *     GEMM_F8_ROWS     M x K, scales M x ceil(K/128): 128 values of a row (an operand whose
+ *                      product sums along its rows)
+ *     GEMM_F8_COLUMNS  M x K, scales ceil(M/128) x K: 128 values of a column (the operands of
+ *                      a weight gradient, which sums over rows)
+ *     GEMM_F8_TILES    K x N, scales ceil(K/128) x ceil(N/128): 128 x 128 tiles (weights); E
+ *                      matrices one after another, each with tiles of its own
+ * The products take any scales.
+ *
+ * gemm_f8_pitch — bytes between the rows that the conversions below write: K rounded up to 16
+ * (the bytes past K are written as 0), or GEMM_ERR_INVALID_ARG.
+ *
+ * gemm_f32_f8_quantize, gemm_bf16_f8_quantize, gemm_f16_f8_quantize — codes and scales of X,
+ * along rows (row_codes, row_scales), along columns (col_codes, col_scales) or both from one
+ * reading; the pair that is not wanted is null. M is the number of rows written. With `rows`
+ * null they are X's (source_rows == M, fan == 1, factors null). Otherwise row i is X's row
+ * rows[i] / fan, times factors[rows[i]] in fp32 where factors (source_rows * fan of them) is
+ * given, and zeros where rows[i] is outside 0 .. source_rows * fan - 1: what gemm_*_route's
+ * rows and weights are for. A block's scale is 2^i, the least with max|x| <= 448 * 2^i, so
+ * x / scale is exact and the code its nearest e4m3 value, halves to even. A block whose largest
+ * magnitude is below 2^-100 gets codes and scale 0, one with a value that is not finite codes 0
+ * and a NaN scale (it reads back, and enters a product, as NaN).
+ *
+ * gemm_*_f8_quantize_tiles — the same for E matrices W of K x N, by tiles.
+ *
+ * gemm_*_f8_dequantize — E matrices M x K of the given kind back to values, code * scale rounded
+ * once; the next matrix starts M * ld bytes on, its scales behind the last matrix's.
+ */
+typedef enum gemm_f8_kind {
+    GEMM_F8_ROWS = 0,
+    GEMM_F8_COLUMNS = 1,
+    GEMM_F8_TILES = 2
+} gemm_f8_kind;
+
+GEMM_API int64_t gemm_f8_pitch(int64_t K);
+GEMM_API int gemm_f32_f8_quantize(int64_t M, int64_t K, const float *X, int64_t source_rows,
+                                  const int32_t *rows, int64_t fan, const float *factors,
+                                  uint8_t *row_codes, float *row_scales, uint8_t *col_codes,
+                                  float *col_scales, void *stream);
+GEMM_API int gemm_bf16_f8_quantize(int64_t M, int64_t K, const uint16_t *X, int64_t source_rows,
+                                  const int32_t *rows, int64_t fan, const float *factors,
+                                  uint8_t *row_codes, float *row_scales, uint8_t *col_codes,
+                                  float *col_scales, void *stream);
+GEMM_API int gemm_f16_f8_quantize(int64_t M, int64_t K, const uint16_t *X, int64_t source_rows,
+                                  const int32_t *rows, int64_t fan, const float *factors,
+                                  uint8_t *row_codes, float *row_scales, uint8_t *col_codes,
+                                  float *col_scales, void *stream);
+GEMM_API int gemm_f32_f8_quantize_tiles(int64_t E, int64_t K, int64_t N, const float *W,
+                                        uint8_t *codes, float *scales, void *stream);
+GEMM_API int gemm_bf16_f8_quantize_tiles(int64_t E, int64_t K, int64_t N, const uint16_t *W,
+                                        uint8_t *codes, float *scales, void *stream);
+GEMM_API int gemm_f16_f8_quantize_tiles(int64_t E, int64_t K, int64_t N, const uint16_t *W,
+                                        uint8_t *codes, float *scales, void *stream);
+GEMM_API int gemm_f32_f8_dequantize(int64_t E, int64_t M, int64_t K, int kind,
+                                    const uint8_t *codes, int64_t ld, const float *scales,
+                                    float *X, void *stream);
+GEMM_API int gemm_bf16_f8_dequantize(int64_t E, int64_t M, int64_t K, int kind,
+                                    const uint8_t *codes, int64_t ld, const float *scales,
+                                    uint16_t *X, void *stream);
+GEMM_API int gemm_f16_f8_dequantize(int64_t E, int64_t M, int64_t K, int kind,
+                                    const uint8_t *codes, int64_t ld, const float *scales,
+                                    uint16_t *X, void *stream);
+
+/*
+ * Products of 8-bit floating-point operands, fp32 results:
+ *     gemm_f8w8f32   C  (M x N) = A . W        A M x K by rows, W K x N by tiles
+ *     gemm_f8w8tf32  dX (M x K) = dY . W^T     dY M x N by rows, the same W
+ *     gemm_f8tf8f32  dW (K x N) = X^T . dY     X M x K and dY M x N by columns
+ * lda, ldw, ldy, ldx: row pitches in bytes. Any sizes (M = 1: a single token); outputs 4-byte,
+ * codes 16-byte, scales 4-byte aligned. Each block of 128's products are summed in fp32 on the
+ * tcgen05 tensor cores and scaled as they are added to the fp32 total; the summed axis is split
+ * over the CTAs of a cluster where there are few tiles, their parts added in a fixed order, so
+ * results repeat exactly. No workspace. K == 0 (gemm_f8w8tf32: N, gemm_f8tf8f32: M): zeros.
+ *
+ * gemm_f8w8f32_selftest_timeout — the failure-detection check of the kernel's bounded waits, as
+ * gemm_bf16f32_selftest_timeout; M, N, K >= 1, wait_limit_ns in [1e6, 1e10].
+ */
+GEMM_API int gemm_f8w8f32(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda,
+                          const float *a_scales, const uint8_t *W, int64_t ldw,
+                          const float *w_scales, float *C, void *stream);
+GEMM_API int gemm_f8w8tf32(int64_t M, int64_t N, int64_t K, const uint8_t *dY, int64_t ldy,
+                           const float *y_scales, const uint8_t *W, int64_t ldw,
+                           const float *w_scales, float *dX, void *stream);
+GEMM_API int gemm_f8tf8f32(int64_t M, int64_t N, int64_t K, const uint8_t *X, int64_t ldx,
+                           const float *x_scales, const uint8_t *dY, int64_t ldy,
+                           const float *y_scales, float *dW, void *stream);
+GEMM_API int gemm_f8w8f32_selftest_timeout(int64_t M, int64_t N, int64_t K, const uint8_t *A,
+                                           int64_t lda, const float *a_scales, const uint8_t *W,
+                                           int64_t ldw, const float *w_scales, float *C,
+                                           int64_t wait_limit_ns, void *stream);
+
+/*
+ * Routing of T tokens to k of E experts (1 <= k <= 32, k <= E <= 1024) by their logits (T x E).
+ *     s = softmax(logits) or, sigmoid != 0, 1 / (1 + exp(-logits)), of each token
+ *     experts[t][j]: the k largest of s + bias (bias fp32, E, null for none), best first, ties
+ *     to the lowest index, decided as in real numbers (fp32 where that is certain, else fp64)
+ *     weights[t][j] = scale * s_j, or, renormalise != 0, scale * s_j / (sum_j s_j + 1e-20);
+ *     the bias moves the choice and not the weights
+ * With groups > 1 (at most 32, dividing E) the experts are in groups of E / groups neighbours;
+ * only those of the top_groups groups whose two largest s + bias have the largest sums take
+ * part (k <= top_groups * E / groups). A NaN counts as -inf in the choice and makes its token's
+ * softmax weights NaN; a token whose logits are all -inf has softmax scores 0.
+ *
+ * And the order by expert that the experts' products work in: slot t * k + j is the token's
+ * j-th expert; its row is slots[t][j], and rows[slots[t][j]] = t * k + j. Expert e's rows are
+ * offsets[e] .. offsets[e + 1] - 1, in the order of their slots, each part's length padded to a
+ * multiple of align (1 .. 1024; 128 for gemm_f8tf8f32_experts). offsets has E + 1 entries, rows
+ * gemm_route_rows(T, E, k, align), -1 where there is no slot: at the parts' ends and behind
+ * offsets[E]. `workspace`: gemm_route_workspace_bytes(T, E) bytes (0 for few tokens).
+ *
+ * gemm_*_route_backward — dlogits (T x E, fp32) from dweights (T x k) and the chosen experts;
+ * entries outside 0 .. E - 1 are passed over.
+ */
+GEMM_API int64_t gemm_route_rows(int64_t T, int64_t E, int64_t k, int64_t align);
+GEMM_API int64_t gemm_route_workspace_bytes(int64_t T, int64_t E);
+GEMM_API int gemm_f32_route(int64_t T, int64_t E, int64_t k, const float *logits,
+                            const float *bias, int64_t groups, int64_t top_groups, int sigmoid,
+                            int renormalise, float scale, int64_t align, int32_t *experts,
+                            float *weights, int32_t *slots, int32_t *rows, int32_t *offsets,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+GEMM_API int gemm_bf16_route(int64_t T, int64_t E, int64_t k, const uint16_t *logits,
+                            const float *bias, int64_t groups, int64_t top_groups, int sigmoid,
+                            int renormalise, float scale, int64_t align, int32_t *experts,
+                            float *weights, int32_t *slots, int32_t *rows, int32_t *offsets,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+GEMM_API int gemm_f16_route(int64_t T, int64_t E, int64_t k, const uint16_t *logits,
+                            const float *bias, int64_t groups, int64_t top_groups, int sigmoid,
+                            int renormalise, float scale, int64_t align, int32_t *experts,
+                            float *weights, int32_t *slots, int32_t *rows, int32_t *offsets,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+GEMM_API int gemm_f32_route_backward(int64_t T, int64_t E, int64_t k, const float *logits,
+                                     int sigmoid, int renormalise, float scale,
+                                     const int32_t *experts, const float *dweights,
+                                     float *dlogits, void *stream);
+GEMM_API int gemm_bf16_route_backward(int64_t T, int64_t E, int64_t k, const uint16_t *logits,
+                                     int sigmoid, int renormalise, float scale,
+                                     const int32_t *experts, const float *dweights,
+                                     float *dlogits, void *stream);
+GEMM_API int gemm_f16_route_backward(int64_t T, int64_t E, int64_t k, const uint16_t *logits,
+                                     int sigmoid, int renormalise, float scale,
+                                     const int32_t *experts, const float *dweights,
+                                     float *dlogits, void *stream);
+
+/*
+ * The experts' products: gemm_f8w8f32 and its gradients over R rows in the order by expert.
+ * Rows offsets[e] .. offsets[e + 1] - 1 of A, C, dY and dX belong to expert e and its matrix of
+ * W (E matrices of K x N, one after another, E <= 1024); gemm_f8tf8f32_experts sums over them
+ * and writes E matrices dW, zeros for an expert without rows; its offsets are multiples of 128.
+ * `offsets` (E + 1, on the device) is read by the kernel and taken as ascending within 0 .. R:
+ * each entry counts as at least the one before it and at most R. Rows of C (dX) outside
+ * offsets[0] .. offsets[E] - 1 are left as they were (but with an empty sum, K == 0 or N == 0,
+ * all R rows are zeros). Otherwise as the products above.
+ *
+ * gemm_experts_join — Y (T x N) = sum_j weights[t][j] * C[slots[t][j]], weights null: ones (the
+ * sum of the parts of a token's gradient). Added in fp32 in the order of j. Slots outside
+ * 0 .. R - 1 add nothing.
+ * gemm_*_experts_join_backward — dweights[t][j] = sum_n dY[t][n] * C[slots[t][j]][n]. (dC is
+ * gemm_*_f8_quantize of dY with rows and factors = weights.)
+ */
+GEMM_API int gemm_f8w8f32_experts(int64_t R, int64_t N, int64_t K, int64_t E,
+                                  const int32_t *offsets, const uint8_t *A, int64_t lda,
+                                  const float *a_scales, const uint8_t *W, int64_t ldw,
+                                  const float *w_scales, float *C, void *stream);
+GEMM_API int gemm_f8w8tf32_experts(int64_t R, int64_t N, int64_t K, int64_t E,
+                                   const int32_t *offsets, const uint8_t *dY, int64_t ldy,
+                                   const float *y_scales, const uint8_t *W, int64_t ldw,
+                                   const float *w_scales, float *dX, void *stream);
+GEMM_API int gemm_f8tf8f32_experts(int64_t R, int64_t N, int64_t K, int64_t E,
+                                   const int32_t *offsets, const uint8_t *X, int64_t ldx,
+                                   const float *x_scales, const uint8_t *dY, int64_t ldy,
+                                   const float *y_scales, float *dW, void *stream);
+GEMM_API int gemm_experts_join(int64_t T, int64_t N, int64_t k, int64_t R, const float *C,
+                               const int32_t *slots, const float *weights, float *Y,
+                               void *stream);
+GEMM_API int gemm_f32_experts_join_backward(int64_t T, int64_t N, int64_t k, int64_t R,
+                                            const float *dY, const float *C,
+                                            const int32_t *slots, float *dweights, void *stream);
+GEMM_API int gemm_bf16_experts_join_backward(int64_t T, int64_t N, int64_t k, int64_t R,
+                                            const uint16_t *dY, const float *C,
+                                            const int32_t *slots, float *dweights, void *stream);
+GEMM_API int gemm_f16_experts_join_backward(int64_t T, int64_t N, int64_t k, int64_t R,
+                                            const uint16_t *dY, const float *C,
+                                            const int32_t *slots, float *dweights, void *stream);
+
+/*
  * gemm_get_device_error — synchronises `stream`, then returns and clears the
  * current device's error word: GEMM_OK, or GEMM_ERR_TIMEOUT if a bounded wait
  * in any kernel of this library on this device gave up since the last call.

@@ -11,6 +11,13 @@ Two CUDA paths behind a C ABI (include/gemm.h, libgemm_gb300.so):
                 products with an operand held in fewer bits: 4-bit weights
                 with group scales, activations saved in 8 bits.
 
+  gemm_f8w8f32, gemm_f8w8tf32, gemm_f8tf8f32
+                products of 8-bit floating-point operands with a scale for each
+                block of 128, forward and backward.
+  gemm_route, gemm_f8w8f32_experts, gemm_experts_join
+                a layer of experts on them: routing, the experts' products and
+                their sum, each with its backward pass.
+
 This package is the thin Python binding (torch is used only for device
 memory and streams) plus the in-tree build step.
 """
@@ -55,4 +62,23 @@ from .binding import (  # noqa: F401
     library_path,
     load_library,
     status_string,
+)
+from .f8 import (  # noqa: F401
+    F8_BLOCK,
+    F8_KINDS,
+    gemm_experts_join,
+    gemm_experts_join_backward,
+    gemm_f8_dequantize,
+    gemm_f8_quantize,
+    gemm_f8_quantize_tiles,
+    gemm_f8tf8f32,
+    gemm_f8tf8f32_experts,
+    gemm_f8w8f32,
+    gemm_f8w8f32_experts,
+    gemm_f8w8f32_selftest_timeout,
+    gemm_f8w8tf32,
+    gemm_f8w8tf32_experts,
+    gemm_route,
+    gemm_route_backward,
+    gemm_route_rows,
 )

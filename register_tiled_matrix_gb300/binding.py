@@ -95,6 +95,33 @@ def load_library() -> ctypes.CDLL:
         lib.gemm_bf16w4f32_selftest_timeout.restype = c_int
         lib.gemm_q8tbf16f32_selftest_timeout.argtypes = [i64] * 3 + [p] * 4 + [i64, p]
         lib.gemm_q8tbf16f32_selftest_timeout.restype = c_int
+        f32 = ctypes.c_float
+        lib.gemm_f8_pitch.argtypes = [i64]
+        lib.gemm_route_rows.argtypes = [i64] * 4
+        lib.gemm_route_workspace_bytes.argtypes = [i64, i64]
+        for name in ("gemm_f8_pitch", "gemm_route_rows", "gemm_route_workspace_bytes"):
+            getattr(lib, name).restype = i64
+        operands = [p, i64, p, p, i64, p, p]  # two of (codes, pitch, scales), the result
+        for name, args in [("gemm_f8w8f32_selftest_timeout", [i64] * 3 + operands + [i64, p]),
+                           ("gemm_experts_join", [i64] * 4 + [p] * 5)]:
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, c_int
+        for name in ("gemm_f8w8f32", "gemm_f8w8tf32", "gemm_f8tf8f32"):
+            for entry, args in ((name, [i64] * 3 + operands + [p]),
+                                (f"{name}_experts", [i64] * 4 + [p] + operands + [p])):
+                f = getattr(lib, entry)
+                f.argtypes, f.restype = args, c_int
+        for t in ("f32", "bf16", "f16"):
+            for name, args in ((f"gemm_{t}_f8_quantize", [i64, i64, p, i64, p, i64] + [p] * 6),
+                               (f"gemm_{t}_f8_quantize_tiles", [i64] * 3 + [p] * 4),
+                               (f"gemm_{t}_f8_dequantize", [i64] * 3 + [c_int, p, i64, p, p, p]),
+                               (f"gemm_{t}_route", [i64] * 3 + [p, p, i64, i64, c_int, c_int, f32,
+                                                                i64] + [p] * 6 + [i64, p]),
+                               (f"gemm_{t}_route_backward", [i64] * 3 + [p, c_int, c_int, f32] +
+                                [p] * 4),
+                               (f"gemm_{t}_experts_join_backward", [i64] * 4 + [p] * 5)):
+                f = getattr(lib, name)
+                f.argtypes, f.restype = args, c_int
         lib.gemm_fp32_pipe_peak.argtypes = [i64, ctypes.c_int, p, ctypes.POINTER(ctypes.c_double),
                                             p]
         lib.gemm_fp32_pipe_peak.restype = ctypes.c_int

@@ -1,0 +1,808 @@
+// Products of e4m3 operands with an fp32 scale for each block of 128, on the sm_103a tensor
+// cores (tcgen05, kind::f8f6f4):
+//
+//     forward  Y[m][n]  = sum_b a[m][b] w[b][n/128] * sum_{k in b} A[m][k] W[k][n]
+//     input    dX[m][k] = sum_b y[m][b] w[k/128][b] * sum_{n in b} dY[m][n] W[k][n]
+//     weight   dW[k][n] = sum_b x[b][k] y[b][n]     * sum_{m in b} X[m][k] dY[m][n]
+//
+// The scales are constant over a block b of 128 of the summed axis (the depth), so the tensor
+// core sums one block's products of codes in fp32 (a product of two codes is exact) and the
+// scales multiply that sum as it is added to the running fp32 total.
+//
+// One CTA computes 128 lanes x NT columns, a pair of CTAs 256 x 256. Its roles are
+//  * a producer thread: TMA of both operands' next 128 of depth into a ring of stages. A code is
+//    a byte, so a stage's row is one 128-byte swizzle row, along the depth or across it: the
+//    tensor core reads both, and no operand is ever transposed;
+//  * an MMA warp: a stage is four steps of 32 into one accumulation set in tensor memory, SETS
+//    sets in turn, so the next block is multiplied while the last one is read;
+//  * PW promoting warpgroups: read a set (a lane a thread), scale it into fp32 totals in
+//    registers, and store them at the end of the tile.
+// Rows of A are the lanes: a thread's scale is its row's times the tile's of W. With few rows
+// W's columns take the lanes instead (SWAP) and 16 to 128 rows of A the accumulator's columns,
+// so that no lane idles and W is read once; the rows' scales then come through shared memory,
+// as the columns' of a weight gradient do.
+//
+// Experts: rows offsets[e] .. offsets[e+1]-1 belong to expert e. The offsets stay on the device;
+// every CTA turns them into a running count of tiles in shared memory and finds a tile's expert
+// by bisection. Offsets are taken as ascending within 0 .. rows, whatever they hold, so no
+// access leaves the arrays.
+//
+// With few tiles the depth is split over S CTAs (pairs) of a cluster; their totals meet in
+// shared memory and are added in rank order, so results repeat exactly. Without a split the
+// CTAs are persistent.
+//
+// Every wait is bounded: a thread that gives up records GEMM_ERR_TIMEOUT in the device error
+// word, and all threads still reach the barriers at the end.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "f8.h"
+#include "kernels.h"
+#include "lowbit_types.cuh"
+#include "ptx.cuh"
+#include "tc_roles.cuh"
+
+namespace rtm {
+namespace f8t {
+
+using namespace roles;
+
+constexpr int LANES = 128;
+constexpr int BK = kF8Block;   // depth of a stage: 128 codes = a 128-byte swizzle row
+constexpr int UMMA_K = 32;
+constexpr uint32_t A_BYTES = LANES * BK;  // 16 KB
+constexpr int kMaxGroups = kRouteMaxExperts;
+
+template <int NT, bool SWAP>
+struct Cfg {
+    static constexpr bool PAIR = NT == 256;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int TILE_LANES = PAIR ? 2 * LANES : LANES;
+    static constexpr int ROWS = SWAP ? NT : TILE_LANES;  // of C in a tile
+    static constexpr int COLS = SWAP ? TILE_LANES : NT;
+    static constexpr int BN = PAIR ? NT / 2 : NT;  // columns staged by a CTA
+    static constexpr int PW = PAIR ? 2 : 1;        // promoting warpgroups
+    static constexpr int THREADS = 128 * (1 + PW);
+    // Registers a thread of a pair's warpgroups after the split of 3 x 168.
+    static constexpr int R_ISSUE = 40, R_PROMOTE = 232;
+    static constexpr int CPT = NT / PW;  // columns of a promoting thread
+    static constexpr int CH = CPT >= 128 || CPT < 32 ? 16 : 32;  // read from tensor memory at once
+    static constexpr int SETS = PAIR ? 2 : 4;
+    static constexpr uint32_t TMEM_COLS = SETS * NT;
+    static constexpr uint32_t B_BYTES = BN * BK;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = NT >= 128 ? 6 : NT == 64 ? 8 : 10;
+    static constexpr int PITCH = NT + 4;  // floats per lane of a partial tile
+    // Partial tiles have room of their own where the stages are too small.
+    static constexpr uint32_t OFF_GROUPS = STAGES * STAGE_BYTES;
+    static constexpr uint32_t OFF_SCALE = OFF_GROUPS + 2 * (kMaxGroups + 4) * 4;
+    static constexpr uint32_t OFF_BARS = OFF_SCALE + PW * 2 * 128 * 4;
+    static constexpr size_t SMEM_BYTES = OFF_BARS + 256 + 1024 /*align*/;
+    static_assert(LANES * PITCH * 4 <= OFF_GROUPS, "a partial tile fits the stages");
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+// "This warp has read its part of an accumulation set" to the leading CTA.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_set(uint32_t bar)
+{
+    if constexpr (PAIR)
+        mbar_arrive_cluster_tmem_free(bar);
+    else
+        arrive(bar);
+}
+
+struct Params {
+    int rows, cols;     // of C; weight: of one matrix C
+    int depth;          // forward, input; weight without offsets
+    int total;          // weight: rows of X and dY
+    int groups;         // experts
+    const int32_t *offsets;
+    const float *a_scales, *b_scales;
+    float *C;
+    int *err;
+    unsigned long long limit_ns;
+    int splits;
+    int mute;
+    int c_vec;  // rows of C on 16-byte boundaries
+};
+
+// kind::f8f6f4, D fp32, both operands e4m3, M = 128 (256 for a pair), N = NT.
+template <int NT, bool SWAP>
+__host__ __device__ constexpr uint32_t idesc(bool lanes_mn, bool cols_mn)
+{
+    return (1u << 4) | ((lanes_mn ? 1u : 0u) << 15) | ((cols_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(Cfg<NT, SWAP>::TILE_LANES >> 4) << 24);
+}
+
+// acc += v * (s0, s1), two at a time.
+__device__ __forceinline__ void fma2_each(float &a0, float &a1, float v0, float v1, float s0, float s1)
+{
+    asm("{\n\t.reg .b64 a, v, s;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 v, {%2, %3};\n\t"
+        "mov.b64 s, {%4, %5};\n\t"
+        "fma.rn.f32x2 a, v, s, a;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}\n"
+        : "+f"(a0), "+f"(a1)
+        : "f"(v0), "f"(v1), "f"(s0), "f"(s1));
+}
+
+// v * s, two at a time.
+__device__ __forceinline__ void mul2(float &v0, float &v1, float s)
+{
+    asm("{\n\t.reg .b64 v, s;\n\t"
+        "mov.b64 v, {%0, %1};\n\t"
+        "mov.b64 s, {%2, %2};\n\t"
+        "mul.rn.f32x2 v, v, s;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}\n"
+        : "+f"(v0), "+f"(v1)
+        : "f"(s));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[N])
+{
+    if constexpr (N == 32)
+        tmem_ld_32x32b_x32(taddr, v);
+    else
+        tmem_ld_32x32b_x16(taddr, v);
+}
+
+// Waits for the loads so far; what uses v comes after.
+template <int N>
+__device__ __forceinline__ void tmem_arrived(uint32_t (&v)[N])
+{
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+r"(v[i]));
+}
+
+__device__ __forceinline__ void warpgroup_barrier(int pw)
+{
+    if (pw == 0)
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    else
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// What a tile is: its expert, first row and column of C, the rows' end, and the depth it sums.
+struct Tile {
+    int group, r0, c0, row_end;
+    int d0, depth;  // weight: first row of X and dY, and how many
+};
+
+template <int MODE, int NT, bool SWAP>
+struct Schedule {
+    using Cf = Cfg<NT, SWAP>;
+    const int32_t *start;  // groups + 1 row offsets
+    const int32_t *tiles;  // groups + 1 running counts
+    const Params *p;
+
+    __device__ __forceinline__ int total() const { return tiles[p->groups]; }
+
+    __device__ __forceinline__ Tile at(int t) const
+    {
+        int lo = 0, hi = p->groups - 1;  // the last group with tiles[g] <= t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tiles[mid] <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        Tile x;
+        x.group = lo;
+        const int begin = start[lo], end = start[lo + 1], local = t - tiles[lo];
+        const int first = MODE == kF8Weight ? 0 : begin;
+        x.row_end = MODE == kF8Weight ? p->rows : end;
+        x.d0 = MODE == kF8Weight ? begin : 0;
+        x.depth = MODE == kF8Weight ? end - begin : p->depth;
+        // In bands of 2048 rows, so that the tiles in flight share both operands in L2.
+        constexpr int BAND = 2048 / Cf::ROWS;
+        const int tr = (x.row_end - first + Cf::ROWS - 1) / Cf::ROWS;
+        const int tc = (p->cols + Cf::COLS - 1) / Cf::COLS;
+        const int band = local / (BAND * tc), row0 = band * BAND;
+        const int rows = min(tr - row0, BAND), in = local - band * BAND * tc;
+        x.r0 = first + (row0 + in % rows) * Cf::ROWS;
+        x.c0 = in / rows * Cf::COLS;
+        return x;
+    }
+};
+
+// This CTA's blocks of a tile's depth.
+struct Blocks {
+    int first, count;
+};
+__device__ __forceinline__ Blocks blocks_of(const Tile &x, int splits, int rank)
+{
+    const int all = (x.depth + BK - 1) / BK, per = (all + splits - 1) / splits;
+    const int first = min(all, rank * per);
+    return {first, min(all, first + per) - first};
+}
+
+// Row offsets and running tile counts of the groups, by one warp.
+template <int MODE, int NT, bool SWAP>
+__device__ __forceinline__ void count_tiles(const Params &p, int32_t *start, int32_t *tiles, int lane)
+{
+    using Cf = Cfg<NT, SWAP>;
+    const int most = MODE == kF8Weight ? p.total : p.rows;
+    const int tc = (p.cols + Cf::COLS - 1) / Cf::COLS;
+    const int each = (p.rows + Cf::ROWS - 1) / Cf::ROWS * tc;  // weight: the same for every group
+    int low = 0, sum = 0;
+    if (p.offsets)
+        low = min(max(p.offsets[0], 0), most);
+    if (lane == 0) {
+        start[0] = low;
+        tiles[0] = 0;
+    }
+    for (int b = 0; b < p.groups; b += 32) {
+        const int g = b + lane;
+        int hi = 0;
+        if (g < p.groups)
+            hi = p.offsets ? min(max(p.offsets[g + 1], 0), most) : most;
+        hi = max(hi, low);
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, hi, o);
+            if (lane >= o)
+                hi = max(hi, y);
+        }
+        int before = __shfl_up_sync(0xffffffffu, hi, 1);
+        if (lane == 0)
+            before = low;
+        int n = 0;
+        if (g < p.groups)
+            n = MODE == kF8Weight ? each : (hi - before + Cf::ROWS - 1) / Cf::ROWS * tc;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o)
+                n += y;
+        }
+        if (g < p.groups) {
+            start[g + 1] = hi;
+            tiles[g + 1] = sum + n;
+        }
+        sum += __shfl_sync(0xffffffffu, n, 31);
+        low = __shfl_sync(0xffffffffu, hi, 31);
+    }
+}
+
+template <int MODE, int NT, bool SWAP>
+__global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
+    f8_tc_kernel(const __grid_constant__ CUtensorMap tm_lanes,
+                 const __grid_constant__ CUtensorMap tm_cols, const Params p)
+{
+    using Cf = Cfg<NT, SWAP>;
+    constexpr bool PAIR = Cf::PAIR;
+    constexpr int CTAS = Cf::CTAS;
+    // Which operand is W (batched by expert), and which lie with the depth along their rows.
+    constexpr bool LANES_MN = SWAP ? MODE == kF8Forward : MODE == kF8Weight;
+    constexpr bool COLS_MN = SWAP ? false : MODE != kF8Input;
+    constexpr bool COLUMN_SCALES = SWAP || MODE == kF8Weight;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+    int32_t *start = reinterpret_cast<int32_t *>(smem + Cf::OFF_GROUPS);
+    int32_t *tile_count = start + kMaxGroups + 4;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::OFF_BARS);
+    uint64_t *empty = full + Cf::STAGES;
+    uint64_t *tfull = empty + Cf::STAGES;
+    uint64_t *tempty = tfull + Cf::SETS;
+    uint64_t *drain = tempty + Cf::SETS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    static_assert((2 * Cf::STAGES + 2 * Cf::SETS + 1) * 8 + 8 <= 256, "barriers");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wg = warp >> 2;
+    const int S = p.splits;
+    const uint32_t cta = PAIR || S > 1 ? cluster_ctarank() : 0u;
+    const int rank = cta / CTAS;                   // of the depth split
+    const uint32_t leader = cta - cta % CTAS;      // the pair's even CTA, which issues the MMAs
+    const bool even = cta == leader;
+    const int half = even ? 0 : LANES;             // this CTA's lanes of a pair's tile
+    const uint32_t pair_mask = 3u << leader;
+    const int unit = blockIdx.x / (S * CTAS), units = gridDim.x / (S * CTAS);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Cf::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < Cf::SETS; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4 * Cf::PW * CTAS);
+        }
+        mbar_init(drain, 1);
+        *abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tm_lanes);
+        tma_prefetch_desc(&tm_cols);
+    }
+    __syncwarp();
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(tmem_slot, Cf::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, Cf::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    if (warp == 2)
+        count_tiles<MODE, NT, SWAP>(p, start, tile_count, lane);
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR)
+        cluster_sync();  // the peer's barriers are initialised before any remote signal
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Schedule<MODE, NT, SWAP> plan{start, tile_count, &p};
+    const int tiles = plan.total();
+
+    if (wg == 0) {
+        if constexpr (PAIR)
+            regs_dec<Cf::R_ISSUE>();
+        if (warp == 0 && lane == 0 && !p.mute) {
+            // ------------------------------------------------ producer
+            Place<Cf::STAGES> stage;
+            bool gave_up = false;
+#pragma unroll 1
+            for (int t = unit; t < tiles && !gave_up; t += units) {
+                const Tile x = plan.at(t);
+                const Blocks b = blocks_of(x, S, rank);
+                const int l0 = (SWAP ? x.c0 : x.r0) + half;
+                const int c0 = (SWAP ? x.r0 : x.c0) + (even ? 0 : Cf::BN);
+                const int lane_batch = SWAP ? x.group : 0;
+                const int col_batch = !SWAP && MODE != kF8Weight ? x.group : 0;
+                int d = x.d0 + b.first * BK;
+#pragma unroll 1
+                for (int i = 0; i < b.count; ++i, d += BK) {
+                    if (!wait_bounded(smem_u32(&empty[stage.at]), stage.phase ^ 1, p.limit_ns, abort)) {
+                        give_up(p.err, abort);
+                        gave_up = true;
+                        break;
+                    }
+                    const uint32_t dst = smem_u32(smem + stage.at * Cf::STAGE_BYTES);
+                    const int lx = LANES_MN ? l0 : d, ly = LANES_MN ? d : l0;
+                    const int cx = COLS_MN ? c0 : d, cy = COLS_MN ? d : c0;
+                    if constexpr (PAIR) {  // both CTAs' bytes on the even one's barrier
+                        if (even)
+                            mbar_arrive_expect_tx(&full[stage.at], 2 * Cf::STAGE_BYTES);
+                        const uint32_t bar = mapa_shared(smem_u32(&full[stage.at]), leader);
+                        tma_load_3d_pair(dst, &tm_lanes, bar, lx, ly, lane_batch);
+                        tma_load_3d_pair(dst + A_BYTES, &tm_cols, bar, cx, cy, col_batch);
+                    } else {
+                        mbar_arrive_expect_tx(&full[stage.at], Cf::STAGE_BYTES);
+                        tma_load_3d(dst, &tm_lanes, &full[stage.at], lx, ly, lane_batch);
+                        tma_load_3d(dst + A_BYTES, &tm_cols, &full[stage.at], cx, cy, col_batch);
+                    }
+                    stage.advance();
+                }
+            }
+        } else if (warp == 1 && even) {
+            // ------------------------------------------------ MMA
+            // Along the depth: rows of 128 B, 8-row groups 1024 B apart, 32 B a step. Across
+            // it: a row of 128 B for each of the depth, 32 rows a step.
+            constexpr uint32_t LSTEP = (LANES_MN ? UMMA_K * 128 : UMMA_K) >> 4;
+            constexpr uint32_t CSTEP = (COLS_MN ? UMMA_K * 128 : UMMA_K) >> 4;
+            constexpr uint32_t ID = idesc<NT, SWAP>(LANES_MN, COLS_MN);
+            const uint64_t ldesc0 = sdesc_sw128(smem_u32(smem), LANES_MN ? A_BYTES : 16, 1024);
+            const uint64_t cdesc0 = sdesc_sw128(smem_u32(smem) + A_BYTES, COLS_MN ? A_BYTES : 16, 1024);
+            const bool elected = elect_one();
+            Place<Cf::STAGES> stage;
+            Place<Cf::SETS> set;
+            const uint32_t full_at = smem_u32(full), tempty_at = smem_u32(tempty);
+            bool any = false;
+#pragma unroll 1
+            for (int t = unit; t < tiles; t += units) {
+                const Blocks b = blocks_of(plan.at(t), S, rank);
+#pragma unroll 1
+                for (int i = 0; i < b.count; ++i) {
+                    wait_on(tempty_at + set.at * 8, set.phase ^ 1, p.limit_ns, p.err, abort);
+                    wait_on(full_at + stage.at * 8, stage.phase, p.limit_ns, p.err, abort);
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + set.at * NT;
+                    const uint64_t ldesc = ldesc0 + stage.at * (Cf::STAGE_BYTES >> 4);
+                    const uint64_t cdesc = cdesc0 + stage.at * (Cf::STAGE_BYTES >> 4);
+                    if (elected) {
+#pragma unroll
+                        for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+                            if constexpr (PAIR)
+                                umma_f8_pair(d, ldesc + kk * LSTEP, cdesc + kk * CSTEP, ID, kk > 0);
+                            else
+                                umma_f8(d, ldesc + kk * LSTEP, cdesc + kk * CSTEP, ID, kk > 0);
+                        }
+                        commit<PAIR>(tfull + set.at, pair_mask);
+                        commit<PAIR>(empty + stage.at, pair_mask);
+                    }
+                    __syncwarp();
+                    any = true;
+                    set.advance();
+                    stage.advance();
+                }
+            }
+            if (any) {
+                if (elected)
+                    commit<PAIR>(drain, pair_mask & (~pair_mask + 1));  // the even CTA
+                volatile int no_abort = 0;
+                wait_bounded(smem_u32(drain), 0, p.limit_ns, &no_abort);  // before TMEM is freed
+            }
+        }
+    } else {
+        // ------------------------------------------------ promote and store
+        if constexpr (PAIR)
+            regs_inc<Cf::R_PROMOTE>();
+        const int pw = wg - 1, quarter = warp & 3;
+        const int row = quarter * 32 + lane;  // TMEM lane
+        const uint32_t ring = smem_u32(smem + Cf::OFF_SCALE) + (uint32_t)pw * (2 * 128 * 4);
+        const uint32_t tfull_at = smem_u32(tfull);
+        const uint32_t tempty_at = PAIR ? mapa_shared(smem_u32(tempty), leader) : smem_u32(tempty);
+        Place<Cf::SETS> set;
+        const int depth_blocks = (p.depth + BK - 1) / BK, col_blocks = (p.cols + BK - 1) / BK;
+        float acc[Cf::CPT];
+#pragma unroll 1
+        for (int t = unit; t < tiles; t += units) {
+            const Tile x = plan.at(t);
+            const Blocks b = blocks_of(x, S, rank);
+            const int lane0 = (SWAP ? x.c0 : x.r0) + half;
+            const int col0 = (SWAP ? x.r0 : x.c0) + pw * Cf::CPT;
+            // This thread's scales of block i: its lane's, the tile's, and (through the ring)
+            // one column's.
+            const float *lane_scale, *tile_scale = nullptr, *column_scale = nullptr;
+            int lane_step, tile_step = 0, column_step = 0;
+            if constexpr (MODE == kF8Weight) {
+                const int64_t block = x.d0 / BK + b.first;
+                lane_scale = p.a_scales + block * p.rows + min(lane0 + row, p.rows - 1);
+                lane_step = p.rows;
+                column_scale = p.b_scales + block * p.cols + min(col0 + (int)(threadIdx.x & 127), p.cols - 1);
+                column_step = p.cols;
+            } else {
+                // W's tiles: forward depth x columns, input columns x depth.
+                const int cb = min((SWAP ? lane0 : col0) / BK, col_blocks - 1);
+                const int64_t matrix = (int64_t)x.group * depth_blocks * col_blocks;
+                tile_scale = p.b_scales + matrix +
+                             (MODE == kF8Forward ? (int64_t)b.first * col_blocks + cb
+                                                 : (int64_t)cb * depth_blocks + b.first);
+                tile_step = MODE == kF8Forward ? col_blocks : 1;
+                const int r = SWAP ? min(col0 + (int)(threadIdx.x & 127), x.row_end - 1)
+                                   : min(lane0 + row, x.row_end - 1);
+                const float *s = p.a_scales + (int64_t)r * depth_blocks + b.first;
+                if constexpr (SWAP) {
+                    column_scale = s;
+                    column_step = 1;
+                    lane_scale = nullptr;
+                    lane_step = 0;
+                } else {
+                    lane_scale = s;
+                    lane_step = 1;
+                }
+            }
+            // The next block's, two blocks ahead of use.
+            int unread = b.count;
+            auto fetch = [&](float &ls, float &cs) {
+                if (--unread < 0)
+                    return;
+                float ts = 1.f;
+                if constexpr (MODE != kF8Weight) {
+                    ts = __ldg(tile_scale);
+                    tile_scale += tile_step;
+                }
+                if constexpr (!SWAP) {
+                    ls = __ldg(lane_scale) * ts;
+                    lane_scale += lane_step;
+                }
+                if constexpr (COLUMN_SCALES) {
+                    cs = __ldg(column_scale) * (SWAP ? ts : 1.f);
+                    column_scale += column_step;
+                }
+            };
+            float ls0 = 0.f, ls1 = 0.f, cs0 = 0.f, cs1 = 0.f;
+            fetch(ls0, cs0);
+            fetch(ls1, cs1);
+#pragma unroll
+            for (int j = 0; j < Cf::CPT; ++j)
+                acc[j] = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < b.count; ++i) {
+                const float ls = ls0;
+                const uint32_t scales = ring + (uint32_t)(i & 1) * (128 * 4);
+                if constexpr (COLUMN_SCALES) {
+                    // Block i - 1's readers have passed this barrier before block i + 1's write.
+                    sts32(scales + (threadIdx.x & 127) * 4, cs0);
+                    warpgroup_barrier(pw);
+                }
+                ls0 = ls1;
+                cs0 = cs1;
+                fetch(ls1, cs1);
+                wait_on(tfull_at + set.at * 8, set.phase, p.limit_ns, p.err, abort);
+                __syncwarp();  // the lanes left the wait each for itself; the load is the warp's
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + set.at * NT +
+                                       (uint32_t)(pw * Cf::CPT);
+                constexpr int CH = Cf::CH, N = Cf::CPT / CH;
+                uint32_t v[2][CH];
+                tmem_load<CH>(taddr, v[0]);
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    uint32_t(&w)[CH] = v[c & 1];
+                    tmem_arrived<CH>(w);
+                    if (c + 1 < N) {
+                        tmem_load<CH>(taddr + (c + 1) * CH, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            arrive_set<PAIR>(tempty_at + set.at * 8);
+                    }
+#pragma unroll
+                    for (int j = 0; j < CH; j += 4) {
+                        float f[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            f[e] = __uint_as_float(w[j + e]);
+                        float *a = acc + c * CH + j;
+                        if constexpr (COLUMN_SCALES) {
+                            const uint4 s = lds128(scales + (c * CH + j) * 4);
+                            if constexpr (!SWAP) {
+                                mul2(f[0], f[1], ls);
+                                mul2(f[2], f[3], ls);
+                            }
+                            fma2_each(a[0], a[1], f[0], f[1], __uint_as_float(s.x), __uint_as_float(s.y));
+                            fma2_each(a[2], a[3], f[2], f[3], __uint_as_float(s.z), __uint_as_float(s.w));
+                        } else {
+                            fma2(a[0], a[1], ls, f[0], f[1]);
+                            fma2(a[2], a[3], ls, f[2], f[3]);
+                        }
+                    }
+                }
+                set.advance();
+            }
+            if constexpr (COLUMN_SCALES)
+                warpgroup_barrier(pw);  // the ring's readers, before the next tile's writes
+            if (S > 1) {
+                const uint32_t part =
+                    smem_u32(smem) + (uint32_t)(row * Cf::PITCH + pw * Cf::CPT) * 4u;
+#pragma unroll
+                for (int j = 0; j < Cf::CPT; j += 4)
+                    sts128(part + 4 * j,
+                           make_uint4(__float_as_uint(acc[j]), __float_as_uint(acc[j + 1]),
+                                      __float_as_uint(acc[j + 2]), __float_as_uint(acc[j + 3])));
+                break;
+            }
+            float *C = p.C + (MODE == kF8Weight ? (int64_t)x.group * p.rows * p.cols : 0);
+            const int gl = lane0 + row;
+            if constexpr (SWAP) {  // a warp's lanes: 32 consecutive floats of a row of C
+                if (gl < p.cols) {
+                    float *c = C + (int64_t)col0 * p.cols + gl;
+                    const int n = x.row_end - col0;
+#pragma unroll
+                    for (int j = 0; j < Cf::CPT; ++j, c += p.cols)
+                        if (j < n)
+                            *c = acc[j];
+                }
+            } else if (gl < x.row_end) {
+                float *c = C + (int64_t)gl * p.cols + col0;
+                const int n = p.cols - col0;
+#pragma unroll
+                for (int j = 0; j < Cf::CPT; j += 4) {
+                    if (p.c_vec && j + 3 < n) {
+                        *reinterpret_cast<float4 *>(c + j) =
+                            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (j + e < n)
+                                c[j + e] = acc[j + e];
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();  // the barriers below are the whole warp's
+
+    if (S > 1) {
+        cluster_sync();  // every partial tile of the cluster is in shared memory
+        if (wg > 0 && unit < tiles) {
+            const Tile x = plan.at(unit);
+            const int row = threadIdx.x & 127, pw = wg - 1;
+            const int cols = NT / S, first = rank * cols;
+            const int gl = (SWAP ? x.c0 : x.r0) + half + row, col0 = SWAP ? x.r0 : x.c0;
+            const uint32_t mine = smem_u32(smem) + (uint32_t)(row * Cf::PITCH) * 4u;
+            float *C = p.C + (MODE == kF8Weight ? (int64_t)x.group * p.rows * p.cols : 0);
+            for (int cc = pw * 2; cc < cols; cc += 2 * Cf::PW) {
+                const uint32_t off = (uint32_t)(first + cc) * 4u;
+                float2 sum = ld_shared_cluster_v2(mapa_shared(mine + off, cta % CTAS));
+                for (int q = 1; q < S; ++q) {
+                    const float2 v = ld_shared_cluster_v2(
+                        mapa_shared(mine + off, (uint32_t)q * CTAS + cta % CTAS));
+                    sum.x += v.x;
+                    sum.y += v.y;
+                }
+                const float a[2] = {sum.x, sum.y};
+                const int gc = col0 + first + cc;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (SWAP) {
+                        if (gl < p.cols && gc + e < x.row_end)
+                            C[(int64_t)(gc + e) * p.cols + gl] = a[e];
+                    } else {
+                        if (gl < x.row_end && gc + e < p.cols)
+                            C[(int64_t)gl * p.cols + gc + e] = a[e];
+                    }
+                }
+            }
+        }
+        cluster_sync();  // no CTA leaves while a peer may still read its partial
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // No copy into this CTA's shared memory may outlive it. The MMAs waited for every
+    // stage's bytes, unless a role gave up: then copies that nobody waited for get
+    // the time of a wait to land. (A pair's CTAs leave together, below.)
+    if (threadIdx.x == 0 && *abort) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < p.limit_ns) {
+        }
+    }
+    __syncwarp();
+    if constexpr (PAIR)
+        cluster_sync();  // no CTA leaves while its peer may still signal or read it
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem_base, Cf::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, Cf::TMEM_COLS);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// batch x rows x cols codes, rows ld and matrices rows * ld bytes apart; boxes of box_rows x 128.
+static bool encode_codes(EncodeTiledFn fn, CUtensorMap *map, const void *base, uint64_t batch,
+                         uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows)
+{
+    cuuint64_t dims[3] = {cols, rows, batch};
+    cuuint64_t strides[2] = {ld, batch > 1 ? rows * ld : ld};
+    cuuint32_t box[3] = {128, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Most tiles that any offsets can make.
+static int64_t most_tiles(const F8Launch &L, int rows, int cols)
+{
+    const int64_t tc = (L.cols + cols - 1) / cols, tr = (L.rows + rows - 1) / rows;
+    if (L.mode == kF8Weight)
+        return tr * tc * L.experts;
+    if (!L.offsets)
+        return tr * tc;
+    return (L.rows / rows + (L.experts < L.rows ? L.experts : L.rows)) * tc;
+}
+
+template <int MODE, int NT, bool SWAP>
+static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mute, cudaStream_t stream)
+{
+    using Cf = Cfg<NT, SWAP>;
+    auto fn = reinterpret_cast<EncodeTiledFn>(d.encode_tiled);
+    if (!fn)
+        return cudaErrorNotSupported;
+    const uint64_t E = (uint64_t)L.experts;
+    CUtensorMap lanes, cols;
+    bool ok;
+    if constexpr (MODE == kF8Weight) {
+        ok = encode_codes(fn, &lanes, L.a, 1, L.depth, L.rows, L.lda, BK) &&
+             encode_codes(fn, &cols, L.b, 1, L.depth, L.cols, L.ldb, BK);
+    } else {
+        CUtensorMap &am = SWAP ? cols : lanes, &wm = SWAP ? lanes : cols;
+        ok = encode_codes(fn, &am, L.a, 1, L.rows, L.depth, L.lda, SWAP ? NT : LANES);
+        if constexpr (MODE == kF8Forward)
+            ok = ok && encode_codes(fn, &wm, L.b, E, L.depth, L.cols, L.ldb, BK);
+        else
+            ok = ok && encode_codes(fn, &wm, L.b, E, L.cols, L.depth, L.ldb, SWAP ? LANES : Cf::BN);
+    }
+    if (!ok)
+        return cudaErrorInvalidValue;
+    auto kernel = f8_tc_kernel<MODE, NT, SWAP>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = set_smem_limit_once(kernel, (int)Cf::SMEM_BYTES, done);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = most_tiles(L, Cf::ROWS, Cf::COLS);
+    if (tiles > 0x1fffffff)
+        return cudaErrorInvalidValue;
+    Params p = {};
+    p.rows = (int)L.rows;
+    p.cols = (int)L.cols;
+    p.depth = (int)L.depth;
+    p.total = (int)L.depth;
+    p.groups = L.experts;
+    p.offsets = L.offsets;
+    p.a_scales = L.a_scales;
+    p.b_scales = L.b_scales;
+    p.C = L.C;
+    p.err = d.err;
+    p.limit_ns = d.wait_limit_ns;
+    p.mute = mute ? 1 : 0;
+    p.c_vec = L.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 15) == 0;
+    // Few tiles: split the depth while every CTA keeps at least two blocks (a pair four) and
+    // all clusters (of at most 8 CTAs) are resident at once.
+    constexpr int CTAS = Cf::CTAS, LEAST = Cf::PAIR ? 4 : 2;
+    const int64_t blocks = f8_blocks(L.depth) / (MODE == kF8Weight && L.offsets ? L.experts : 1);
+    int splits = 1;
+    while (splits * CTAS < 8 && tiles * splits * CTAS * 2 <= d.sms && blocks >= splits * 2 * LEAST)
+        splits *= 2;
+    static std::atomic<int> resident[4][64] = {};  // clusters of 1, 2, 4, 8
+    int fit = d.sms;
+    for (; splits * CTAS > 1; splits /= 2) {
+        const int size = splits * CTAS;
+        fit = resident_clusters(kernel, size, Cf::THREADS, Cf::SMEM_BYTES,
+                                resident[size == 2 ? 1 : size == 4 ? 2 : 3]);
+        if (fit <= 0)
+            fit = d.sms / size;
+        if (tiles <= fit || splits == 1)
+            break;
+    }
+    if (splits * CTAS == 1)
+        fit = d.sms;
+    p.splits = splits;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((tiles < fit ? tiles : fit) * splits * CTAS), 1, 1);
+    cfg.blockDim = dim3(Cf::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)(splits * CTAS);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, lanes, cols, p);
+}
+
+template <int MODE>
+static cudaError_t launch_mode(const F8Launch &L, const DeviceContext &d, bool mute, cudaStream_t stream)
+{
+    if constexpr (MODE != kF8Weight) {
+        const int64_t rows = L.offsets ? (L.rows + L.experts - 1) / L.experts : L.rows;
+        if (rows <= 16)
+            return launch_cfg<MODE, 16, true>(L, d, mute, stream);
+        if (rows <= 32)
+            return launch_cfg<MODE, 32, true>(L, d, mute, stream);
+        if (rows <= 64)
+            return launch_cfg<MODE, 64, true>(L, d, mute, stream);
+        if (rows <= 128)
+            return launch_cfg<MODE, 128, true>(L, d, mute, stream);
+    }
+    if (most_tiles(L, 256, 256) * 4 >= d.sms)
+        return launch_cfg<MODE, 256, false>(L, d, mute, stream);
+    return launch_cfg<MODE, 128, false>(L, d, mute, stream);
+}
+
+} // namespace f8t
+
+cudaError_t launch_f8_tc(const F8Launch &L, const DeviceContext &d, bool mute, cudaStream_t stream)
+{
+    return L.mode == kF8Forward ? f8t::launch_mode<kF8Forward>(L, d, mute, stream)
+           : L.mode == kF8Input ? f8t::launch_mode<kF8Input>(L, d, mute, stream)
+                                : f8t::launch_mode<kF8Weight>(L, d, mute, stream);
+}
+
+} // namespace rtm
