@@ -54,12 +54,11 @@ int quantize(int64_t M, int64_t K, int type, const void *X, int64_t source, cons
              uint8_t *col_codes, float *col_scales, void *stream)
 {
     if (!size_ok(M, f8_pitch(K)) || !size_ok(source, K) || fan < 1 || fan > kMaxDim ||
-        (rows && source > kMaxDim / fan) || (!rows && (source != M || fan != 1 || factors)) ||
-        !row_codes != !row_scales || !col_codes != !col_scales)
+        source > kMaxDim / fan || !row_codes != !row_scales || !col_codes != !col_scales)
         return GEMM_ERR_INVALID_ARG;
     if (M == 0 || K == 0)
         return GEMM_OK;
-    if ((source > 0 && !X) || (!row_codes && !col_codes))
+    if ((!rows && (source != M || fan != 1 || factors)) || (source > 0 && !X) || (!row_codes && !col_codes))
         return GEMM_ERR_INVALID_ARG;
     const Range out[4] = {{row_codes, M * f8_pitch(K)},
                           {row_scales, M * f8_blocks(K) * 4},

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
         if (KIND != kTiles && p.factors) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[i][j] *= factor;
+                v[i][j] = fmaf(v[i][j], factor, 0.f);  // one rounding; no -0 past the row's end
         }
     }
 

@@ -219,30 +219,34 @@ template <int V>
 __device__ __forceinline__ int select_exactly(const RouteLaunch &L, int64_t t, int lane, double *v)
 {
     double top = -INFINITY, sum = 0;
+    bool nan = false;
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
         const double z = e < L.E ? (double)load(L.logits, L.type, t * L.E + e) : -INFINITY;
         v[e] = z;
+        nan = nan || z != z;
         top = fmax(top, z);
     }
+    nan = __any_sync(kAll, nan);
     if (!L.sigmoid) {
 #pragma unroll
         for (int o = 16; o > 0; o /= 2)
             top = fmax(top, __shfl_xor_sync(kAll, top, o));
     }
+    const bool nothing = top == -INFINITY && !nan;
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
         const double z = v[i * 32 + lane];
         const double x = exp(L.sigmoid ? -z : z - top);
-        const double s = L.sigmoid ? 1.0 / (1.0 + x) : top == -INFINITY ? 0.0 : x;
+        const double s = L.sigmoid ? 1.0 / (1.0 + x) : nothing ? 0.0 : x;
         v[i * 32 + lane] = s;
         sum += s;
     }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2)
         sum += __shfl_xor_sync(kAll, sum, o);
-    if (L.sigmoid || top == -INFINITY)
+    if (L.sigmoid || nothing)
         sum = 1.0;
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
