@@ -53,6 +53,11 @@ constexpr int BK = kF8Block;   // depth of a stage: 128 codes = a 128-byte swizz
 constexpr int UMMA_K = 32;
 constexpr uint32_t A_BYTES = LANES * BK;  // 16 KB
 constexpr int kMaxGroups = kRouteMaxExperts;
+// The scales' ring. A slot is written SCALE_AHEAD blocks ahead of use, when the accumulation set
+// of SETS blocks ago is full, so the promoting warps are through with all but the last
+// 2 * SETS + 2 blocks.
+constexpr int SCALE_SLOTS = 16, SCALE_AHEAD = 6;
+constexpr int SCALERS = 2;  // warps
 
 template <int NT, bool SWAP>
 struct Cfg {
@@ -65,19 +70,23 @@ struct Cfg {
     static constexpr int PW = PAIR ? 2 : 1;        // promoting warpgroups
     static constexpr int THREADS = 128 * (1 + PW);
     // Registers a thread of a pair's warpgroups after the split of 3 x 168.
-    static constexpr int R_ISSUE = 40, R_PROMOTE = 232;
+    static constexpr int R_ISSUE = 56, R_PROMOTE = 224;
     static constexpr int CPT = NT / PW;  // columns of a promoting thread
-    static constexpr int CH = CPT >= 128 || CPT < 32 ? 16 : 32;  // read from tensor memory at once
+    static constexpr int CH = CPT < 32 ? CPT : 32;  // read from tensor memory at once
     static constexpr int SETS = PAIR ? 2 : 4;
     static constexpr uint32_t TMEM_COLS = SETS * NT;
     static constexpr uint32_t B_BYTES = BN * BK;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+    // Floats of a slot: the lanes' scales or none, the columns' or none, the tiles'.
+    static constexpr int SCALE_COLUMNS = SWAP ? 0 : LANES, SCALE_TILE = SCALE_COLUMNS + NT;
+    static constexpr int SCALE_PITCH = SCALE_TILE + 4;
+    static_assert(SCALE_AHEAD + 2 * SETS + 2 <= SCALE_SLOTS, "scales are read before their slot is written");
     static constexpr int STAGES = NT >= 128 ? 6 : NT == 64 ? 8 : 10;
     static constexpr int PITCH = NT + 4;  // floats per lane of a partial tile
     // Partial tiles have room of their own where the stages are too small.
     static constexpr uint32_t OFF_GROUPS = STAGES * STAGE_BYTES;
     static constexpr uint32_t OFF_SCALE = OFF_GROUPS + 2 * (kMaxGroups + 4) * 4;
-    static constexpr uint32_t OFF_BARS = OFF_SCALE + PW * 2 * 128 * 4;
+    static constexpr uint32_t OFF_BARS = OFF_SCALE + SCALE_SLOTS * SCALE_PITCH * 4;
     static constexpr size_t SMEM_BYTES = OFF_BARS + 256 + 1024 /*align*/;
     static_assert(LANES * PITCH * 4 <= OFF_GROUPS, "a partial tile fits the stages");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -105,7 +114,7 @@ struct Params {
     unsigned long long limit_ns;
     int splits;
     int mute;
-    int c_vec;  // rows of C on 16-byte boundaries
+    int c_vec;  // rows of C on 32-byte boundaries
 };
 
 // kind::f8f6f4, D fp32, both operands e4m3, M = 128 (256 for a pair), N = NT.
@@ -144,10 +153,12 @@ __device__ __forceinline__ void mul2(float &v0, float &v1, float s)
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[N])
 {
-    if constexpr (N == 32)
-        tmem_ld_32x32b_x32(taddr, v);
-    else
+    if constexpr (N == 16)
         tmem_ld_32x32b_x16(taddr, v);
+    else
+#pragma unroll
+        for (int i = 0; i < N; i += 32)
+            tmem_ld_32x32b_x32(taddr + i, *reinterpret_cast<uint32_t(*)[32]>(v + i));
 }
 
 // Waits for the loads so far; what uses v comes after.
@@ -160,17 +171,14 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&v)[N])
         asm volatile("" : "+r"(v[i]));
 }
 
-__device__ __forceinline__ void warpgroup_barrier(int pw)
-{
-    if (pw == 0)
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-    else
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-}
+__device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds32(addr)); }
 
-__device__ __forceinline__ void sts32(uint32_t addr, float v)
+// Eight neighbouring floats, 32-byte aligned: a whole sector in one store.
+__device__ __forceinline__ void store8(float *p, const float *v)
 {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
 
 // What a tile is: its expert, first row and column of C, the rows' end, and the depth it sums.
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < Cf::SETS; ++i) {
-            mbar_init(&tfull[i], 1);
+            mbar_init(&tfull[i], 1 + SCALERS);  // the MMAs, the block's scales
             mbar_init(&tempty[i], 4 * Cf::PW * CTAS);
         }
         mbar_init(drain, 1);
@@ -354,7 +362,9 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
         if (warp == 0 && lane == 0 && !p.mute) {
             // ------------------------------------------------ producer
             Place<Cf::STAGES> stage;
-            bool gave_up = false;
+            const uint32_t empty_at = smem_u32(empty), base = smem_u32(smem);
+            const uint32_t full_at = PAIR ? mapa_shared(smem_u32(full), leader) : smem_u32(full);
+            bool gave_up = false, seen = false;  // what the look ahead said
 #pragma unroll 1
             for (int t = unit; t < tiles && !gave_up; t += units) {
                 const Tile x = plan.at(t);
@@ -366,18 +376,22 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                 int d = x.d0 + b.first * BK;
 #pragma unroll 1
                 for (int i = 0; i < b.count; ++i, d += BK) {
-                    if (!wait_bounded(smem_u32(&empty[stage.at]), stage.phase ^ 1, p.limit_ns, abort)) {
+                    if (!seen &&
+                        !wait_bounded(empty_at + stage.at * 8, stage.phase ^ 1, p.limit_ns, abort)) {
                         give_up(p.err, abort);
                         gave_up = true;
                         break;
                     }
-                    const uint32_t dst = smem_u32(smem + stage.at * Cf::STAGE_BYTES);
+                    Place<Cf::STAGES> next = stage;
+                    next.advance();
+                    seen = peek(empty_at + next.at * 8, next.phase ^ 1);
+                    const uint32_t dst = base + stage.at * Cf::STAGE_BYTES;
+                    const uint32_t bar = full_at + stage.at * 8;
                     const int lx = LANES_MN ? l0 : d, ly = LANES_MN ? d : l0;
                     const int cx = COLS_MN ? c0 : d, cy = COLS_MN ? d : c0;
                     if constexpr (PAIR) {  // both CTAs' bytes on the even one's barrier
                         if (even)
                             mbar_arrive_expect_tx(&full[stage.at], 2 * Cf::STAGE_BYTES);
-                        const uint32_t bar = mapa_shared(smem_u32(&full[stage.at]), leader);
                         tma_load_3d_pair(dst, &tm_lanes, bar, lx, ly, lane_batch);
                         tma_load_3d_pair(dst + A_BYTES, &tm_cols, bar, cx, cy, col_batch);
                     } else {
@@ -385,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         tma_load_3d(dst, &tm_lanes, &full[stage.at], lx, ly, lane_batch);
                         tma_load_3d(dst + A_BYTES, &tm_cols, &full[stage.at], cx, cy, col_batch);
                     }
-                    stage.advance();
+                    stage = next;
                 }
             }
         } else if (warp == 1 && even) {
@@ -402,15 +416,23 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
             Place<Cf::SETS> set;
             const uint32_t full_at = smem_u32(full), tempty_at = smem_u32(tempty);
             bool any = false;
+            bool full_seen = false, empty_seen = false;  // what the look ahead said
 #pragma unroll 1
             for (int t = unit; t < tiles; t += units) {
                 const Blocks b = blocks_of(plan.at(t), S, rank);
 #pragma unroll 1
                 for (int i = 0; i < b.count; ++i) {
-                    wait_on(tempty_at + set.at * 8, set.phase ^ 1, p.limit_ns, p.err, abort);
-                    wait_on(full_at + stage.at * 8, stage.phase, p.limit_ns, p.err, abort);
-                    __syncwarp();
+                    if (!empty_seen)
+                        wait_on(tempty_at + set.at * 8, set.phase ^ 1, p.limit_ns, p.err, abort);
+                    if (!full_seen)
+                        wait_on(full_at + stage.at * 8, stage.phase, p.limit_ns, p.err, abort);
                     tc_fence_after();
+                    Place<Cf::STAGES> next_stage = stage;
+                    next_stage.advance();
+                    Place<Cf::SETS> next_set = set;
+                    next_set.advance();
+                    full_seen = peek(full_at + next_stage.at * 8, next_stage.phase);
+                    empty_seen = peek(tempty_at + next_set.at * 8, next_set.phase ^ 1);
                     const uint32_t d = tmem_base + set.at * NT;
                     const uint64_t ldesc = ldesc0 + stage.at * (Cf::STAGE_BYTES >> 4);
                     const uint64_t cdesc = cdesc0 + stage.at * (Cf::STAGE_BYTES >> 4);
@@ -425,10 +447,9 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         commit<PAIR>(tfull + set.at, pair_mask);
                         commit<PAIR>(empty + stage.at, pair_mask);
                     }
-                    __syncwarp();
                     any = true;
-                    set.advance();
-                    stage.advance();
+                    set = next_set;
+                    stage = next_stage;
                 }
             }
             if (any) {
@@ -437,6 +458,93 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                 volatile int no_abort = 0;
                 wait_bounded(smem_u32(drain), 0, p.limit_ns, &no_abort);  // before TMEM is freed
             }
+        } else if (warp >= 2) {
+            // ------------------------------------------------ scales
+            // A thread copies the scales of lanes (columns) id, id + 64, ...
+            const int id = threadIdx.x & 63;
+            const uint32_t ring = smem_u32(smem + Cf::OFF_SCALE), tfull_at = smem_u32(tfull);
+            const int depth_blocks = (p.depth + BK - 1) / BK, col_blocks = (p.cols + BK - 1) / BK;
+            constexpr int NL = SWAP ? 0 : LANES / 64;
+            constexpr int NC = !COLUMN_SCALES ? 0 : NT < 64 ? 1 : NT / 64;
+            const float *lanes[NL > 0 ? NL : 1], *columns[NC > 0 ? NC : 1], *tile = nullptr;
+            int tile_step = 0;
+            int ft = unit, left = -1;  // the tile whose scales are asked for, its blocks left
+            uint32_t fslot = 0;
+            auto fetch = [&]() {
+                while (left <= 0 && ft < tiles) {  // the next tile that has blocks
+                    if (left == 0)
+                        ft += units;
+                    if (ft >= tiles)
+                        break;
+                    const Tile x = plan.at(ft);
+                    const Blocks b = blocks_of(x, S, rank);
+                    left = b.count;
+                    const int lane0 = (SWAP ? x.c0 : x.r0) + half, col0 = SWAP ? x.r0 : x.c0;
+                    if constexpr (MODE == kF8Weight) {
+                        const int64_t block = x.d0 / BK + b.first;
+#pragma unroll
+                        for (int j = 0; j < NL; ++j)
+                            lanes[j] = p.a_scales + block * p.rows + min(lane0 + id + 64 * j, p.rows - 1);
+#pragma unroll
+                        for (int j = 0; j < NC; ++j)
+                            columns[j] = p.b_scales + block * p.cols + min(col0 + id + 64 * j, p.cols - 1);
+                    } else {
+                        // W's tiles: forward depth x columns, input columns x depth.
+                        const int cb = min((SWAP ? lane0 : col0 + (warp - 2) * BK) / BK, col_blocks - 1);
+                        tile = p.b_scales + (int64_t)x.group * depth_blocks * col_blocks +
+                               (MODE == kF8Forward ? (int64_t)b.first * col_blocks + cb
+                                                   : (int64_t)cb * depth_blocks + b.first);
+                        tile_step = MODE == kF8Forward ? col_blocks : 1;
+#pragma unroll
+                        for (int j = 0; j < (SWAP ? NC : NL); ++j)
+                            (SWAP ? columns : lanes)[j] =
+                                p.a_scales + b.first +
+                                (int64_t)min((SWAP ? col0 : lane0) + id + 64 * j, x.row_end - 1) * depth_blocks;
+                    }
+                }
+                if (left > 0) {
+                    const uint32_t slot = ring + fslot * (Cf::SCALE_PITCH * 4);
+#pragma unroll
+                    for (int j = 0; j < NL; ++j) {
+                        cp_async_4_full(slot + (id + 64 * j) * 4, lanes[j]);
+                        lanes[j] += MODE == kF8Weight ? p.rows : 1;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NC; ++j) {
+                        if (NT >= 64 || id < NT)
+                            cp_async_4_full(slot + (Cf::SCALE_COLUMNS + id + 64 * j) * 4, columns[j]);
+                        columns[j] += MODE == kF8Weight ? p.cols : 1;
+                    }
+                    if constexpr (MODE != kF8Weight) {
+                        if (lane == 0 && warp - 2 < Cf::PW)
+                            cp_async_4_full(slot + (Cf::SCALE_TILE + warp - 2) * 4, tile);
+                        tile += tile_step;
+                    }
+                    fslot = (fslot + 1) % SCALE_SLOTS;
+                    --left;
+                }
+                cp_async_commit();
+            };
+#pragma unroll 1
+            for (int i = 0; i < SCALE_AHEAD; ++i)
+                fetch();
+            Place<Cf::SETS> set;
+#pragma unroll 1
+            for (int t = unit; t < tiles; t += units) {
+                const int blocks = blocks_of(plan.at(t), S, rank).count;
+#pragma unroll 1
+                for (int i = 0; i < blocks; ++i) {
+                    // In step with the sets: an arrival counts for the set's present phase.
+                    wait_on(tfull_at + set.at * 8, set.phase ^ 1, p.limit_ns, p.err, abort);
+                    fetch();
+                    cp_async_wait<SCALE_AHEAD>();
+                    __syncwarp();
+                    if (lane == 0)
+                        arrive(tfull_at + set.at * 8);
+                    set.advance();
+                }
+            }
+            cp_async_wait<0>();
         }
     } else {
         // ------------------------------------------------ promote and store
@@ -444,101 +552,49 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
             regs_inc<Cf::R_PROMOTE>();
         const int pw = wg - 1, quarter = warp & 3;
         const int row = quarter * 32 + lane;  // TMEM lane
-        const uint32_t ring = smem_u32(smem + Cf::OFF_SCALE) + (uint32_t)pw * (2 * 128 * 4);
+        const uint32_t ring = smem_u32(smem + Cf::OFF_SCALE);
+        uint32_t slot = 0;
         const uint32_t tfull_at = smem_u32(tfull);
         const uint32_t tempty_at = PAIR ? mapa_shared(smem_u32(tempty), leader) : smem_u32(tempty);
         Place<Cf::SETS> set;
-        const int depth_blocks = (p.depth + BK - 1) / BK, col_blocks = (p.cols + BK - 1) / BK;
         float acc[Cf::CPT];
+        bool seen = false;  // what the look ahead said
 #pragma unroll 1
         for (int t = unit; t < tiles; t += units) {
             const Tile x = plan.at(t);
             const Blocks b = blocks_of(x, S, rank);
             const int lane0 = (SWAP ? x.c0 : x.r0) + half;
             const int col0 = (SWAP ? x.r0 : x.c0) + pw * Cf::CPT;
-            // This thread's scales of block i: its lane's, the tile's, and (through the ring)
-            // one column's.
-            const float *lane_scale, *tile_scale = nullptr, *column_scale = nullptr;
-            int lane_step, tile_step = 0, column_step = 0;
-            if constexpr (MODE == kF8Weight) {
-                const int64_t block = x.d0 / BK + b.first;
-                lane_scale = p.a_scales + block * p.rows + min(lane0 + row, p.rows - 1);
-                lane_step = p.rows;
-                column_scale = p.b_scales + block * p.cols + min(col0 + (int)(threadIdx.x & 127), p.cols - 1);
-                column_step = p.cols;
-            } else {
-                // W's tiles: forward depth x columns, input columns x depth.
-                const int cb = min((SWAP ? lane0 : col0) / BK, col_blocks - 1);
-                const int64_t matrix = (int64_t)x.group * depth_blocks * col_blocks;
-                tile_scale = p.b_scales + matrix +
-                             (MODE == kF8Forward ? (int64_t)b.first * col_blocks + cb
-                                                 : (int64_t)cb * depth_blocks + b.first);
-                tile_step = MODE == kF8Forward ? col_blocks : 1;
-                const int r = SWAP ? min(col0 + (int)(threadIdx.x & 127), x.row_end - 1)
-                                   : min(lane0 + row, x.row_end - 1);
-                const float *s = p.a_scales + (int64_t)r * depth_blocks + b.first;
-                if constexpr (SWAP) {
-                    column_scale = s;
-                    column_step = 1;
-                    lane_scale = nullptr;
-                    lane_step = 0;
-                } else {
-                    lane_scale = s;
-                    lane_step = 1;
-                }
-            }
-            // The next block's, two blocks ahead of use.
-            int unread = b.count;
-            auto fetch = [&](float &ls, float &cs) {
-                if (--unread < 0)
-                    return;
-                float ts = 1.f;
-                if constexpr (MODE != kF8Weight) {
-                    ts = __ldg(tile_scale);
-                    tile_scale += tile_step;
-                }
-                if constexpr (!SWAP) {
-                    ls = __ldg(lane_scale) * ts;
-                    lane_scale += lane_step;
-                }
-                if constexpr (COLUMN_SCALES) {
-                    cs = __ldg(column_scale) * (SWAP ? ts : 1.f);
-                    column_scale += column_step;
-                }
-            };
-            float ls0 = 0.f, ls1 = 0.f, cs0 = 0.f, cs1 = 0.f;
-            fetch(ls0, cs0);
-            fetch(ls1, cs1);
 #pragma unroll
             for (int j = 0; j < Cf::CPT; ++j)
                 acc[j] = 0.f;
 #pragma unroll 1
             for (int i = 0; i < b.count; ++i) {
-                const float ls = ls0;
-                const uint32_t scales = ring + (uint32_t)(i & 1) * (128 * 4);
-                if constexpr (COLUMN_SCALES) {
-                    // Block i - 1's readers have passed this barrier before block i + 1's write.
-                    sts32(scales + (threadIdx.x & 127) * 4, cs0);
-                    warpgroup_barrier(pw);
-                }
-                ls0 = ls1;
-                cs0 = cs1;
-                fetch(ls1, cs1);
-                wait_on(tfull_at + set.at * 8, set.phase, p.limit_ns, p.err, abort);
+                if (!seen)
+                    wait_on(tfull_at + set.at * 8, set.phase, p.limit_ns, p.err, abort);
                 __syncwarp();  // the lanes left the wait each for itself; the load is the warp's
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + set.at * NT +
                                        (uint32_t)(pw * Cf::CPT);
-                constexpr int CH = Cf::CH, N = Cf::CPT / CH;
-                uint32_t v[2][CH];
-                tmem_load<CH>(taddr, v[0]);
+                const uint32_t scales = ring + slot * (Cf::SCALE_PITCH * 4);
+                slot = (slot + 1) % SCALE_SLOTS;
+                Place<Cf::SETS> next = set;
+                next.advance();
+                float ls = 1.f;
+                constexpr int CH = Cf::CH;
 #pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    uint32_t(&w)[CH] = v[c & 1];
-                    tmem_arrived<CH>(w);
-                    if (c + 1 < N) {
-                        tmem_load<CH>(taddr + (c + 1) * CH, v[(c + 1) & 1]);
-                    } else {
+                for (int c = 0; c < Cf::CPT; c += CH) {
+                    uint32_t v[CH];
+                    tmem_load<CH>(taddr + c, v);
+                    if (c == 0) {  // while the first load is under way
+                        seen = peek(tfull_at + next.at * 8, next.phase);
+                        if constexpr (!SWAP)
+                            ls = lds_f32(scales + row * 4);
+                        if constexpr (MODE != kF8Weight)
+                            ls *= lds_f32(scales + (Cf::SCALE_TILE + pw) * 4);
+                    }
+                    tmem_arrived<CH>(v);
+                    if (c + CH == Cf::CPT) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
@@ -549,14 +605,12 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         float f[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            f[e] = __uint_as_float(w[j + e]);
-                        float *a = acc + c * CH + j;
+                            f[e] = __uint_as_float(v[j + e]);
+                        float *a = acc + c + j;
                         if constexpr (COLUMN_SCALES) {
-                            const uint4 s = lds128(scales + (c * CH + j) * 4);
-                            if constexpr (!SWAP) {
-                                mul2(f[0], f[1], ls);
-                                mul2(f[2], f[3], ls);
-                            }
+                            const uint4 s = lds128(scales + (Cf::SCALE_COLUMNS + pw * Cf::CPT + c + j) * 4);
+                            mul2(f[0], f[1], ls);
+                            mul2(f[2], f[3], ls);
                             fma2_each(a[0], a[1], f[0], f[1], __uint_as_float(s.x), __uint_as_float(s.y));
                             fma2_each(a[2], a[3], f[2], f[3], __uint_as_float(s.z), __uint_as_float(s.w));
                         } else {
@@ -565,10 +619,8 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         }
                     }
                 }
-                set.advance();
+                set = next;
             }
-            if constexpr (COLUMN_SCALES)
-                warpgroup_barrier(pw);  // the ring's readers, before the next tile's writes
             if (S > 1) {
                 const uint32_t part =
                     smem_u32(smem) + (uint32_t)(row * Cf::PITCH + pw * Cf::CPT) * 4u;
@@ -594,13 +646,12 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                 float *c = C + (int64_t)gl * p.cols + col0;
                 const int n = p.cols - col0;
 #pragma unroll
-                for (int j = 0; j < Cf::CPT; j += 4) {
-                    if (p.c_vec && j + 3 < n) {
-                        *reinterpret_cast<float4 *>(c + j) =
-                            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                for (int j = 0; j < Cf::CPT; j += 8) {
+                    if (p.c_vec && j + 7 < n) {
+                        store8(c + j, acc + j);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 8; ++e)
                             if (j + e < n)
                                 c[j + e] = acc[j + e];
                     }
@@ -740,7 +791,7 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
     p.err = d.err;
     p.limit_ns = d.wait_limit_ns;
     p.mute = mute ? 1 : 0;
-    p.c_vec = L.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 15) == 0;
+    p.c_vec = L.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 31) == 0;
     // Few tiles: split the depth while every CTA keeps at least two blocks (a pair four) and
     // all clusters (of at most 8 CTAs) are resident at once.
     constexpr int CTAS = Cf::CTAS, LEAST = Cf::PAIR ? 4 : 2;
