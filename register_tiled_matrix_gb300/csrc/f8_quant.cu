@@ -9,9 +9,10 @@
 // sums over rows), or 128 x 128 (weights).
 //
 // A block of 256 threads owns 128 columns of 16 P rows: thread (tid & 15, tid >> 4) holds eight
-// neighbouring columns of P rows 16 apart in registers, so X is read once whatever is made of
-// it. A row's maximum meets in 16 lanes, a column's in registers, two lanes and shared memory.
-// Maxima are of the magnitudes' bits: their order is the values', and a NaN exceeds all.
+// neighbouring columns of P rows 16 apart in registers, as they came, so X is read once whatever
+// is made of it and several blocks fit an SM to cover each other's loads. A row's maximum meets
+// in 16 lanes, a column's in registers, two lanes and shared memory. Maxima are of the
+// magnitudes' bits, two 16-bit values at a time: their order is the values', and a NaN exceeds all.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,22 +71,48 @@ __device__ __forceinline__ float load1(const void *X, int64_t i)
         return __half2float(static_cast<const __half *>(X)[i]);
 }
 
-// Eight values from i on; i's address on 16 bytes.
+// Eight values as they lie in memory.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void *X, int64_t i, float (&v)[8])
-{
-    if constexpr (TYPE == kF32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(X) + i);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 a =
-            __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(X) + i));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw {
+    static constexpr int WORDS = TYPE == kF32 ? 8 : 4;
+    uint32_t w[WORDS];
+
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (TYPE == kBf16) {
+        for (int j = 0; j < WORDS; ++j)
+            w[j] = 0;
+    }
+    // From i on; i's address on 16 bytes.
+    __device__ __forceinline__ void load(const void *X, int64_t i)
+    {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(X) +
+                                                         i * (TYPE == kF32 ? 4 : 2));
+#pragma unroll
+        for (int j = 0; j < WORDS; j += 4) {
+            const uint4 a = __ldg(p + j / 4);
+            w[j] = a.x, w[j + 1] = a.y, w[j + 2] = a.z, w[j + 3] = a.w;
+        }
+    }
+    // The first n of them.
+    __device__ __forceinline__ void load_some(const void *X, int64_t i, int64_t n)
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) {
+                if constexpr (TYPE == kF32)
+                    w[j] = __ldg(static_cast<const uint32_t *>(X) + i + j);
+                else
+                    w[j / 2] |= (uint32_t)__ldg(static_cast<const uint16_t *>(X) + i + j) << (16 * (j & 1));
+            }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) {
+            if constexpr (TYPE == kF32) {
+                v[j] = __uint_as_float(w[j]);
+            } else if constexpr (TYPE == kBf16) {
                 v[2 * j] = __uint_as_float(w[j] << 16);
                 v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
             } else {
@@ -95,86 +122,139 @@ __device__ __forceinline__ void load8(const void *X, int64_t i, float (&v)[8])
             }
         }
     }
+};
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)  // of two 16-bit halves
+{
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The fp32 bits of a 16-bit magnitude.
+template <int TYPE>
+__device__ __forceinline__ uint32_t widen(uint32_t half)
+{
+    if constexpr (TYPE == kBf16)
+        return half << 16;
+    else
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)half)));
 }
 
 struct Params {
-    int64_t M, K, source, fan;  // M: rows of one matrix
+    int64_t M, K, source;  // M: rows of one matrix
+    uint32_t fan;
     const void *X;
     const int32_t *rows;
     const float *factors;
     uint8_t *row_codes, *col_codes;  // kTiles: row_codes, row_scales
     float *row_scales, *col_scales;
     int64_t col_blocks, row_blocks;  // of one matrix
+    int64_t blocks;  // of rows, of all matrices
     int vec;  // X's rows on 16-byte boundaries
 };
 
 enum Kind { kRows = 1, kColumns = 2, kBoth = 3, kTiles = 4 };
 
-template <int TYPE, int KIND, int P>
+template <int TYPE, int KIND, int P, bool FACTORS>
 __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
 {
     constexpr bool DOWN = KIND != kRows;  // a scale spans rows
+    constexpr bool HALVES = TYPE != kF32 && !FACTORS;  // maxima of 16-bit magnitudes
+    constexpr int TOPS = HALVES ? 4 : 8;
     static_assert(!DOWN || P == 8, "128 rows");
     __shared__ uint32_t top_of[DOWN ? 8 : 1][DOWN ? 128 : 1];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
-    const int64_t cb = blockIdx.x % p.col_blocks, all = blockIdx.x / p.col_blocks;
-    const int64_t rb = KIND == kTiles ? all % p.row_blocks : all;
+    const int64_t cb = blockIdx.x, all = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+    if (all >= p.blocks)
+        return;
     const int64_t e = KIND == kTiles ? all / p.row_blocks : 0;
+    const int64_t rb = KIND == kTiles ? all - e * p.row_blocks : all;
     const int64_t c0 = cb * kF8Block + tx * 8;
     const int64_t r0 = rb * (16 * P) + ty;
     const int64_t base = e * p.M;  // first row of this matrix
     const int64_t pitch = f8_pitch(p.K);
 
-    float v[P][8];
+    Raw<TYPE> raw[P];
+    float factor[FACTORS ? P : 1];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int64_t r = r0 + 16 * i;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[i][j] = 0.f;
+        raw[i].clear();
+        if constexpr (FACTORS)
+            factor[i] = 0.f;
         if (r >= p.M)
             continue;
         int64_t from = base + r;
-        float factor = 1.f;
         if (KIND != kTiles && p.rows) {
-            const int64_t slot = __ldg(p.rows + r);
-            from = slot / p.fan;
+            const int slot = __ldg(p.rows + r);
+            from = (uint32_t)slot / p.fan;
             if (slot < 0 || from >= p.source)
                 continue;
-            if (p.factors)
-                factor = __ldg(p.factors + slot);
+            if constexpr (FACTORS)
+                factor[i] = __ldg(p.factors + slot);
         }
-        if (p.vec && c0 + 8 <= p.K) {
-            load8<TYPE>(p.X, from * p.K + c0, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j < p.K)
-                    v[i][j] = load1<TYPE>(p.X, from * p.K + c0 + j);
-        }
-        if (KIND != kTiles && p.factors) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] = fmaf(v[i][j], factor, 0.f);  // one rounding; no -0 past the row's end
-        }
+        if (p.vec && c0 + 8 <= p.K)
+            raw[i].load(p.X, from * p.K + c0);
+        else
+            raw[i].load_some(p.X, from * p.K + c0, p.K - c0);
     }
-
-    if constexpr (KIND & kRows) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            uint32_t top = 0;
+    auto values = [&](int i, float (&v)[8]) {
+        raw[i].values(v);
+        if constexpr (FACTORS) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                top = max(top, magnitude(v[i][j]));
+                v[j] = fmaf(v[j], factor[i], 0.f);  // one rounding; no -0 past the row's end
+        }
+    };
+    // Magnitudes of row i: fp32 bits, or two 16-bit ones a word.
+    auto magnitudes = [&](int i, uint32_t (&m)[TOPS]) {
+        if constexpr (HALVES) {
 #pragma unroll
-            for (int m = 1; m < 16; m *= 2)
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+            for (int j = 0; j < 4; ++j)
+                m[j] = raw[i].w[j] & 0x7fff7fffu;
+        } else {
+            float v[8];
+            values(i, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                m[j] = __float_as_uint(v[j]) & 0x7fffffffu;
+        }
+    };
+    auto larger = [](uint32_t a, uint32_t b) { return HALVES ? max2(a, b) : max(a, b); };
+
+    uint32_t tops[DOWN ? TOPS : 1];
+    if constexpr (DOWN) {
+#pragma unroll
+        for (int j = 0; j < TOPS; ++j)
+            tops[j] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        uint32_t m[TOPS];
+        magnitudes(i, m);
+        if constexpr (DOWN) {
+#pragma unroll
+            for (int j = 0; j < TOPS; ++j)
+                tops[j] = larger(tops[j], m[j]);
+        }
+        if constexpr (KIND & kRows) {
+            uint32_t top = m[0];
+#pragma unroll
+            for (int j = 1; j < TOPS; ++j)
+                top = larger(top, m[j]);
+#pragma unroll
+            for (int o = 1; o < 16; o *= 2)
+                top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if constexpr (HALVES)
+                top = widen<TYPE>(max(top & 0xffffu, top >> 16));
             const Scale s = scale_of(top);
             const int64_t r = r0 + 16 * i;
             if (r < p.M) {
+                float v[8];
+                values(i, v);
                 if (c0 < pitch)
-                    *reinterpret_cast<uint2 *>(p.row_codes + r * pitch + c0) =
-                        codes8(v[i], s.inv, s.nil);
+                    *reinterpret_cast<uint2 *>(p.row_codes + r * pitch + c0) = codes8(v, s.inv, s.nil);
                 if (tx == 0)
                     p.row_scales[r * p.col_blocks + cb] = s.s;
             }
@@ -182,19 +262,16 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
     }
 
     if constexpr (DOWN) {
-        uint32_t top[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            top[j] = 0;
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                top[j] = max(top[j], magnitude(v[i][j]));
-            top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-        }
+        for (int j = 0; j < TOPS; ++j)
+            tops[j] = larger(tops[j], __shfl_xor_sync(0xffffffffu, tops[j], 16));
         if ((threadIdx.x & 16) == 0) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                top_of[warp][tx * 8 + j] = top[j];
+                top_of[warp][tx * 8 + j] =
+                    HALVES ? widen<TYPE == kF32 ? kBf16 : TYPE>(j & 1 ? tops[j / 2] >> 16
+                                                                     : tops[j / 2] & 0xffffu)
+                           : tops[j % TOPS];
         }
         __syncthreads();
         if (threadIdx.x < 128) {
@@ -218,50 +295,67 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int64_t r = r0 + 16 * i;
+                float v[8];
+                values(i, v);
                 if (r < p.M && c0 < pitch)
                     *reinterpret_cast<uint2 *>(p.row_codes + (base + r) * pitch + c0) =
-                        codes8(v[i], s.inv, s.nil);
+                        codes8(v, s.inv, s.nil);
             }
         } else {
             float inv[8];
+            uint32_t keep[2] = {0, 0};  // 0 for the codes of a column that are 0
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const Scale s = scale_of(top_of[0][tx * 8 + j]);
                 inv[j] = s.inv;
-                if (s.nil) {
-#pragma unroll
-                    for (int i = 0; i < P; ++i)
-                        v[i][j] = 0.f;
-                }
+                keep[j / 4] |= s.nil ? 0u : 0xffu << (8 * (j & 3));
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int64_t r = r0 + 16 * i;
-                if (r >= p.M || c0 >= pitch)
-                    continue;
+                float v[8];
+                values(i, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[i][j] *= inv[j];
-                *reinterpret_cast<uint2 *>(p.col_codes + r * pitch + c0) =
-                    codes8(v[i], 1.f, false);
+                    v[j] *= inv[j];
+                const uint2 q = codes8(v, 1.f, false);
+                if (r < p.M && c0 < pitch)
+                    *reinterpret_cast<uint2 *>(p.col_codes + r * pitch + c0) =
+                        make_uint2(q.x & keep[0], q.y & keep[1]);
             }
         }
     }
 }
 
-template <int KIND, int P>
-static cudaError_t launch_kind(int type, const Params &p, int64_t blocks, cudaStream_t stream)
+template <int KIND, int P, bool FACTORS>
+static cudaError_t launch_kind(int type, Params p, int64_t blocks, cudaStream_t stream)
 {
-    if (blocks > 0x7fffffff)
+    const int64_t y = blocks < 65535 ? blocks : 65535, z = (blocks + y - 1) / y;
+    if (z > 65535 || p.col_blocks > 0x7fffffff)
         return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)blocks;
+    p.blocks = blocks;
+    const dim3 grid((unsigned)p.col_blocks, (unsigned)y, (unsigned)z);
     if (type == kF32)
-        f8_quantize_kernel<kF32, KIND, P><<<grid, kThreads, 0, stream>>>(p);
+        f8_quantize_kernel<kF32, KIND, P, FACTORS><<<grid, kThreads, 0, stream>>>(p);
     else if (type == kBf16)
-        f8_quantize_kernel<kBf16, KIND, P><<<grid, kThreads, 0, stream>>>(p);
+        f8_quantize_kernel<kBf16, KIND, P, FACTORS><<<grid, kThreads, 0, stream>>>(p);
     else
-        f8_quantize_kernel<kF16, KIND, P><<<grid, kThreads, 0, stream>>>(p);
+        f8_quantize_kernel<kF16, KIND, P, FACTORS><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <bool FACTORS>
+static cudaError_t launch_rows_and_columns(int type, const Params &p, cudaStream_t stream)
+{
+    const int64_t down = f8_blocks(p.M);
+    if (p.row_codes && p.col_codes)
+        return launch_kind<kBoth, 8, FACTORS>(type, p, down, stream);
+    if (p.col_codes)
+        return launch_kind<kColumns, 8, FACTORS>(type, p, down, stream);
+    // Four rows a thread where that still makes many blocks.
+    if (p.M * p.col_blocks >= 64 * 2048)
+        return launch_kind<kRows, 4, FACTORS>(type, p, (p.M + 63) / 64, stream);
+    return launch_kind<kRows, 1, FACTORS>(type, p, (p.M + 15) / 16, stream);
 }
 
 static bool rows_on_16(int type, const void *X, int64_t K)
@@ -269,9 +363,10 @@ static bool rows_on_16(int type, const void *X, int64_t K)
     return K * (type == kF32 ? 4 : 2) % 16 == 0 && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
 }
 
-// Sixteen codes a thread.
+// A warp takes 512 codes of a row, a thread four at a time 128 apart, so that loads and stores
+// of a warp are whole lines whatever the result's type.
 struct BackParams {
-    int64_t rows, M, K, ld, chunks;  // rows: of all matrices; chunks of 16 codes a row
+    int64_t rows, M, K, ld, chunks;  // rows: of all matrices; chunks of 512 codes a row
     const uint8_t *codes;
     const float *scales;
     void *X;
@@ -283,73 +378,86 @@ struct BackParams {
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) f8_dequantize_kernel(const BackParams p)
 {
-    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int64_t at = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (at >= p.rows * p.chunks)
         return;
-    const int64_t r = at / p.chunks, c0 = (at - r * p.chunks) * 16;
-    const int64_t e = r / p.M, m = r - e * p.M;
+    const int64_t r = at / p.chunks, e = r / p.M, m = r - e * p.M;
+    const int64_t c0 = (at - r * p.chunks) * 512 + lane * 4;
     const float *s = p.scales + (e * p.row_blocks + (m >> p.bm_shift)) * p.col_blocks;
-    const uint8_t *q = p.codes + r * p.ld + c0;
-    uint32_t word[4] = {0, 0, 0, 0};
-    if (c0 + 16 <= p.K) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(q));  // rows lie on 16 bytes
-        word[0] = w.x, word[1] = w.y, word[2] = w.z, word[3] = w.w;
-    } else {
+    const uint8_t *q = p.codes + r * p.ld;
+    uint32_t word[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c0 + j < p.K)
-                word[j / 4] |= (uint32_t)__ldg(q + j) << (8 * (j & 3));
-    }
-    float v[16];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint32_t h;
-        const uint16_t two = (uint16_t)(word[j / 2] >> (16 * (j & 1)));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-    }
-    const int64_t left = p.K - c0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        if (j < left)
-            v[j] *= __ldg(s + ((c0 + j) >> p.bk_shift));
-    const int64_t to = r * p.K + c0;
-    if (p.vec && left >= 16) {
-        if constexpr (TYPE == kF32) {
-            float4 *x = reinterpret_cast<float4 *>(static_cast<float *>(p.X) + to);
+    for (int i = 0; i < 4; ++i) {
+        const int64_t c = c0 + 128 * i;
+        word[i] = 0;
+        if (c + 4 <= p.K) {
+            word[i] = __ldg(reinterpret_cast<const uint32_t *>(q + c));  // rows lie on 16 bytes
+        } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                x[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else {
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (TYPE == kBf16) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                    o[j] = *reinterpret_cast<const uint32_t *>(&b);
-                } else {
-                    const __half2 b = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-                    o[j] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-            }
-            uint4 *x = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.X) + to);
-            x[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            x[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                if (c + j < p.K)
+                    word[i] |= (uint32_t)__ldg(q + c + j) << (8 * j);
         }
-        return;
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        if (j < left) {
-            if constexpr (TYPE == kF32)
-                static_cast<float *>(p.X)[to + j] = v[j];
-            else if constexpr (TYPE == kBf16)
-                static_cast<__nv_bfloat16 *>(p.X)[to + j] = __float2bfloat16_rn(v[j]);
-            else
-                static_cast<__half *>(p.X)[to + j] = __float2half_rn(v[j]);
+    for (int i = 0; i < 4; ++i) {
+        const int64_t c = c0 + 128 * i, left = p.K - c;
+        if (left <= 0)
+            return;
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t h;
+            const uint16_t two = (uint16_t)(word[i] >> (16 * j));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
         }
+        if (p.bk_shift) {
+            const float one = __ldg(s + (c >> p.bk_shift));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] *= one;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left)
+                    v[j] *= __ldg(s + c + j);
+        }
+        const int64_t to = r * p.K + c;
+        if (p.vec && left >= 4) {
+            if constexpr (TYPE == kF32) {
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.X) + to) =
+                    make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+                uint32_t o[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (TYPE == kBf16) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                        o[j] = *reinterpret_cast<const uint32_t *>(&b);
+                    } else {
+                        const __half2 b = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+                        o[j] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                }
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.X) + to) = make_uint2(o[0], o[1]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) {
+                    if constexpr (TYPE == kF32)
+                        static_cast<float *>(p.X)[to + j] = v[j];
+                    else if constexpr (TYPE == kBf16)
+                        static_cast<__nv_bfloat16 *>(p.X)[to + j] = __float2bfloat16_rn(v[j]);
+                    else
+                        static_cast<__half *>(p.X)[to + j] = __float2half_rn(v[j]);
+                }
+        }
+    }
 }
 
 } // namespace f8q
@@ -361,7 +469,7 @@ cudaError_t launch_f8_quantize(const F8QuantLaunch &L, cudaStream_t stream)
     p.M = L.M;
     p.K = L.K;
     p.source = L.source;
-    p.fan = L.fan;
+    p.fan = (uint32_t)L.fan;
     p.X = L.X;
     p.rows = L.rows;
     p.factors = L.factors;
@@ -371,12 +479,8 @@ cudaError_t launch_f8_quantize(const F8QuantLaunch &L, cudaStream_t stream)
     p.col_scales = L.col_scales;
     p.col_blocks = f8_blocks(L.K);
     p.vec = rows_on_16(L.type, L.X, L.K);
-    const int64_t down = f8_blocks(L.M) * p.col_blocks;
-    if (L.row_codes && L.col_codes)
-        return launch_kind<kBoth, 8>(L.type, p, down, stream);
-    if (L.col_codes)
-        return launch_kind<kColumns, 8>(L.type, p, down, stream);
-    return launch_kind<kRows, 1>(L.type, p, (L.M + 15) / 16 * p.col_blocks, stream);
+    return L.factors ? launch_rows_and_columns<true>(L.type, p, stream)
+                     : launch_rows_and_columns<false>(L.type, p, stream);
 }
 
 cudaError_t launch_f8_quantize_tiles(int64_t E, int64_t K, int64_t N, int type, const void *W,
@@ -392,7 +496,7 @@ cudaError_t launch_f8_quantize_tiles(int64_t E, int64_t K, int64_t N, int type, 
     p.row_blocks = f8_blocks(K);
     p.col_blocks = f8_blocks(N);
     p.vec = rows_on_16(type, W, N);
-    return launch_kind<kTiles, 8>(type, p, E * p.row_blocks * p.col_blocks, stream);
+    return launch_kind<kTiles, 8, false>(type, p, E * p.row_blocks, stream);
 }
 
 cudaError_t launch_f8_dequantize(int64_t E, int64_t M, int64_t K, int bm, int bk, int type,
@@ -405,7 +509,7 @@ cudaError_t launch_f8_dequantize(int64_t E, int64_t M, int64_t K, int bm, int bk
     p.M = M;
     p.K = K;
     p.ld = ld;
-    p.chunks = (K + 15) / 16;
+    p.chunks = (K + 511) / 512;
     p.codes = codes;
     p.scales = scales;
     p.X = X;
@@ -414,7 +518,7 @@ cudaError_t launch_f8_dequantize(int64_t E, int64_t M, int64_t K, int bm, int bk
     p.row_blocks = bm == 1 ? M : f8_blocks(M);
     p.col_blocks = bk == 1 ? K : f8_blocks(K);
     p.vec = rows_on_16(type, X, K);
-    const int64_t blocks = (p.rows * p.chunks + kThreads - 1) / kThreads;
+    const int64_t blocks = (p.rows * p.chunks + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7fffffff)
         return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)blocks;

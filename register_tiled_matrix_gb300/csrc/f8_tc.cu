@@ -171,6 +171,18 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&v)[N])
         asm volatile("" : "+r"(v[i]));
 }
 
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b)
+{
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+
 __device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds32(addr)); }
 
 // Eight neighbouring floats, 32-byte aligned: a whole sector in one store.
@@ -296,6 +308,9 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
     constexpr bool LANES_MN = SWAP ? MODE == kF8Forward : MODE == kF8Weight;
     constexpr bool COLS_MN = SWAP ? false : MODE != kF8Input;
     constexpr bool COLUMN_SCALES = SWAP || MODE == kF8Weight;
+    // Read from tensor memory as matrix fragments: a thread then has 4 lanes of a quarter of the
+    // columns, and half as many of the columns' scales to load.
+    constexpr bool FRAGMENTS = MODE == kF8Weight;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     int32_t *start = reinterpret_cast<int32_t *>(smem + Cf::OFF_GROUPS);
@@ -581,47 +596,98 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                 Place<Cf::SETS> next = set;
                 next.advance();
                 float ls = 1.f;
-                constexpr int CH = Cf::CH;
+                if constexpr (FRAGMENTS) {
+                    // acc: 64 columns c, lanes of half q, 8 columns k, lane t / 4 (+ 8).
+                    float rs[4];
 #pragma unroll
-                for (int c = 0; c < Cf::CPT; c += CH) {
-                    uint32_t v[CH];
-                    tmem_load<CH>(taddr + c, v);
-                    if (c == 0) {  // while the first load is under way
-                        seen = peek(tfull_at + next.at * 8, next.phase);
-                        if constexpr (!SWAP)
-                            ls = lds_f32(scales + row * 4);
-                        if constexpr (MODE != kF8Weight)
+                    for (int q = 0; q < 4; ++q)
+                        rs[q] = lds_f32(scales + (quarter * 32 + q * 8 + (lane >> 2)) * 4);
+                    seen = peek(tfull_at + next.at * 8, next.phase);
+#pragma unroll
+                    for (int c = 0; c < Cf::CPT; c += 64) {
+                        float2 cs[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            cs[k] = lds_f32x2(scales + (Cf::SCALE_COLUMNS + pw * Cf::CPT + c + 8 * k +
+                                                        2 * (lane & 3)) * 4);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t v[32];
+                            tmem_ld_16x256b_x8(taddr + ((uint32_t)(q * 16) << 16) + c, v);
+                            tmem_arrived<32>(v);
+                            if (c + 64 == Cf::CPT && q == 1) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0)
+                                    arrive_set<PAIR>(tempty_at + set.at * 8);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    float f0 = __uint_as_float(v[4 * k + 2 * e]);
+                                    float f1 = __uint_as_float(v[4 * k + 2 * e + 1]);
+                                    mul2(f0, f1, rs[2 * q + e]);
+                                    float *t = acc + ((c / 64 * 2 + q) * 8 + k) * 4 + 2 * e;
+                                    fma2_each(t[0], t[1], f0, f1, cs[k].x, cs[k].y);
+                                }
+                        }
+                    }
+                } else {
+                    constexpr int CH = Cf::CH;
+#pragma unroll
+                    for (int c = 0; c < Cf::CPT; c += CH) {
+                        uint32_t v[CH];
+                        tmem_load<CH>(taddr + c, v);
+                        if (c == 0) {  // while the first load is under way
+                            seen = peek(tfull_at + next.at * 8, next.phase);
+                            if constexpr (!SWAP)
+                                ls = lds_f32(scales + row * 4);
                             ls *= lds_f32(scales + (Cf::SCALE_TILE + pw) * 4);
-                    }
-                    tmem_arrived<CH>(v);
-                    if (c + CH == Cf::CPT) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            arrive_set<PAIR>(tempty_at + set.at * 8);
-                    }
+                        }
+                        tmem_arrived<CH>(v);
+                        if (c + CH == Cf::CPT) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                arrive_set<PAIR>(tempty_at + set.at * 8);
+                        }
 #pragma unroll
-                    for (int j = 0; j < CH; j += 4) {
-                        float f[4];
+                        for (int j = 0; j < CH; j += 4) {
+                            float f[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            f[e] = __uint_as_float(v[j + e]);
-                        float *a = acc + c + j;
-                        if constexpr (COLUMN_SCALES) {
-                            const uint4 s = lds128(scales + (Cf::SCALE_COLUMNS + pw * Cf::CPT + c + j) * 4);
-                            mul2(f[0], f[1], ls);
-                            mul2(f[2], f[3], ls);
-                            fma2_each(a[0], a[1], f[0], f[1], __uint_as_float(s.x), __uint_as_float(s.y));
-                            fma2_each(a[2], a[3], f[2], f[3], __uint_as_float(s.z), __uint_as_float(s.w));
-                        } else {
-                            fma2(a[0], a[1], ls, f[0], f[1]);
-                            fma2(a[2], a[3], ls, f[2], f[3]);
+                            for (int e = 0; e < 4; ++e)
+                                f[e] = __uint_as_float(v[j + e]);
+                            float *a = acc + c + j;
+                            if constexpr (SWAP) {
+                                const uint4 s = lds128(scales + (Cf::SCALE_COLUMNS + pw * Cf::CPT + c + j) * 4);
+                                mul2(f[0], f[1], ls);
+                                mul2(f[2], f[3], ls);
+                                fma2_each(a[0], a[1], f[0], f[1], __uint_as_float(s.x), __uint_as_float(s.y));
+                                fma2_each(a[2], a[3], f[2], f[3], __uint_as_float(s.z), __uint_as_float(s.w));
+                            } else {
+                                fma2(a[0], a[1], ls, f[0], f[1]);
+                                fma2(a[2], a[3], ls, f[2], f[3]);
+                            }
                         }
                     }
                 }
                 set = next;
             }
+            // Of fragments: f(lane of the tile's half, column, the two values from it).
+            auto each_fragment = [&](auto f) {
+#pragma unroll
+                for (int i = 0; i < Cf::CPT / 2; ++i)  // c / 64, q, k, e as above
+                    f(quarter * 32 + (i / 16 % 2) * 16 + (i % 2) * 8 + (lane >> 2),
+                      pw * Cf::CPT + (i / 32) * 64 + (i / 2 % 8) * 8 + 2 * (lane & 3), acc + 2 * i);
+            };
             if (S > 1) {
+                if constexpr (FRAGMENTS) {
+                    each_fragment([&](int l, int c, const float *v) {
+                        sts_f32x2(smem_u32(smem) + (uint32_t)(l * Cf::PITCH + c) * 4u, v[0], v[1]);
+                    });
+                    break;
+                }
                 const uint32_t part =
                     smem_u32(smem) + (uint32_t)(row * Cf::PITCH + pw * Cf::CPT) * 4u;
 #pragma unroll
@@ -633,7 +699,22 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
             }
             float *C = p.C + (MODE == kF8Weight ? (int64_t)x.group * p.rows * p.cols : 0);
             const int gl = lane0 + row;
-            if constexpr (SWAP) {  // a warp's lanes: 32 consecutive floats of a row of C
+            if constexpr (FRAGMENTS) {
+                each_fragment([&](int l, int c, const float *v) {
+                    const int r = lane0 + l, at = x.c0 + c;
+                    float *to = C + (int64_t)r * p.cols + at;
+                    if (r >= x.row_end)
+                        return;
+                    if (p.c_vec && at + 1 < p.cols) {
+                        *reinterpret_cast<float2 *>(to) = make_float2(v[0], v[1]);
+                    } else {
+                        if (at < p.cols)
+                            to[0] = v[0];
+                        if (at + 1 < p.cols)
+                            to[1] = v[1];
+                    }
+                });
+            } else if constexpr (SWAP) {  // a warp's lanes: 32 consecutive floats of a row of C
                 if (gl < p.cols) {
                     float *c = C + (int64_t)col0 * p.cols + gl;
                     const int n = x.row_end - col0;

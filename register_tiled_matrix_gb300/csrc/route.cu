@@ -52,82 +52,82 @@ __device__ __forceinline__ float of_key(uint32_t k)
     return __uint_as_float((int32_t)k < 0 ? k & 0x7fffffffu : ~k);
 }
 
-// The values that a selection runs on, a lane's i-th: fp32 as ordered bits in registers, fp64
-// in the warp's shared memory.
+// The values that a selection runs on, a lane's i-th, as ordered bits: of fp32 in registers, of
+// fp64 in the warp's shared memory (the GPU has few fp64 units; comparing bits needs none).
 template <int V>
 struct Keys {
     using Type = uint32_t;
+    using Value = float;
     uint32_t v[V];
     __device__ __forceinline__ Type at(int i, int) const { return v[i]; }
-    static __device__ __forceinline__ double value(Type k) { return of_key(k); }
+    static __device__ __forceinline__ Value value(Type k) { return of_key(k); }
+    static __device__ __forceinline__ Type key(Value f) { return key_of(f); }
 };
-struct Doubles {
-    using Type = double;
-    const double *v;
+struct DoubleKeys {
+    using Type = uint64_t;
+    using Value = double;
+    const uint64_t *v;
     __device__ __forceinline__ Type at(int i, int lane) const { return v[i * 32 + lane]; }
-    static __device__ __forceinline__ double value(Type k) { return k; }
+    static __device__ __forceinline__ Value value(Type k)
+    {
+        return __longlong_as_double((int64_t)k < 0 ? k & 0x7fffffffffffffffull : ~k);
+    }
+    static __device__ __forceinline__ Type key(Value f)
+    {
+        const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
+        return f != f ? 0x000fffffffffffffull : (int64_t)u < 0 ? ~u : u | 0x8000000000000000ull;
+    }
 };
 
+constexpr int kNone = 0x7fffffff;
+
+// The largest of the lanes' keys and the index that came with it, the lowest on a tie; kNone
+// where no lane has one. Keys are never 0.
+__device__ __forceinline__ int best_of(uint32_t mine, int at, uint32_t &top)
+{
+    const uint32_t m = __reduce_max_sync(kAll, mine);
+    top = m;
+    return (int)__reduce_min_sync(kAll, mine == m ? (uint32_t)at : (uint32_t)kNone);
+}
+__device__ __forceinline__ int best_of(uint64_t mine, int at, uint64_t &top)
+{
+    const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(mine >> 32));
+    const bool in = (uint32_t)(mine >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(kAll, in ? (uint32_t)mine : 0u);
+    top = (uint64_t)hi << 32 | lo;
+    return (int)__reduce_min_sync(kAll, mine == top ? (uint32_t)at : (uint32_t)kNone);
+}
+
 // The largest of the lanes' open values (bit i of `open`: the i-th takes part) and its index
-// i * 32 + lane, the lowest on a tie; -1 where nothing is open.
+// i * 32 + lane.
 template <int V, class S>
 __device__ __forceinline__ int best(const S &v, uint32_t open, int lane, typename S::Type &top)
 {
-    constexpr bool SINGLE = sizeof(typename S::Type) == 4;
-    constexpr int NONE = 0x7fffffff;
     typename S::Type mine = 0;
-    int at = NONE;
-#pragma unroll(SINGLE ? V : 1)
+    int at = kNone;
+#pragma unroll
     for (int i = 0; i < V; ++i) {
-        const typename S::Type x = v.at(i, lane);
-        if ((open >> i & 1) && (at == NONE || x > mine)) {
+        const typename S::Type x = (open >> i & 1) ? v.at(i, lane) : 0;
+        if (x > mine) {
             mine = x;
             at = i * 32 + lane;
         }
     }
-    if constexpr (SINGLE) {
-        const uint32_t m = __reduce_max_sync(kAll, mine);  // open keys are never 0
-        at = (int)__reduce_min_sync(kAll, mine == m ? (uint32_t)at : (uint32_t)NONE);
-        top = m;
-    } else {
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) {
-            const double other = __shfl_xor_sync(kAll, mine, o);
-            const int oat = __shfl_xor_sync(kAll, at, o);
-            if (oat != NONE && (at == NONE || other > mine || (other == mine && oat < at))) {
-                mine = other;
-                at = oat;
-            }
-        }
-        top = mine;
-    }
-    return at == NONE ? -1 : at;
+    return best_of(mine, at, top);
 }
 
-// The same over one value a lane.
-__device__ __forceinline__ int best_lane(double mine, bool in, int lane, double &top)
+// Whether a's lead over b is beyond what fp32 can have moved. A sigmoid is within 2e-7 of the
+// real one and 1e-6 of itself, a softmax score within 1e-6, and 6e-6 of itself while it is above
+// 1e-30 (the exponent's rounding, 2^-24 of at most 70, and the sum's); adding the bias or two
+// scores rounds once more, 2^-24 of the sum.
+__device__ __forceinline__ bool leads(float a, float b, const RouteLaunch &L)
 {
-    int at = in ? lane : 32;
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        const double other = __shfl_xor_sync(kAll, mine, o);
-        const int oat = __shfl_xor_sync(kAll, at, o);
-        if (oat < 32 && (at == 32 || other > mine || (other == mine && oat < at))) {
-            mine = other;
-            at = oat;
-        }
-    }
-    top = mine;
-    return at;
+    const float size = fabsf(a) + fabsf(b);
+    if (L.bias)
+        return a - b > (L.sigmoid ? 1e-6f : 4e-6f) + 2.5e-7f * size;
+    return a - b > (L.sigmoid ? 2.5e-6f : 1.3e-5f) * size + 1e-30f;
 }
-
-// Whether a's lead over b is beyond what fp32 can have moved: scores are within 5e-7 of the
-// real ones, and, relative to themselves, within 6e-6 while they are above 1e-30 (the exponent's
-// rounding, 2^-24 of at most 70, and a few steps).
-__device__ __forceinline__ bool leads(double a, double b, bool biased)
-{
-    return a - b > (biased ? 4e-6 + 1e-6 * (fabs(a) + fabs(b)) : 1.2e-5 * (fabs(a) + fabs(b)) + 1e-30);
-}
+__device__ __forceinline__ bool leads(double, double, const RouteLaunch &) { return true; }
 
 struct Args {
     RouteLaunch L;
@@ -141,16 +141,17 @@ template <int V, class S>
 __device__ __forceinline__ bool select(const S &v, const RouteLaunch &L, int lane, bool scored,
                                        int &mine)
 {
+    using Key = typename S::Type;
+    using Value = typename S::Value;
     uint32_t open = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
         if (i * 32 + lane < L.E)
             open |= 1u << i;
-    const bool biased = L.bias != nullptr;
     bool sure = true;
     if (L.groups > 1) {
         const int size = L.E / L.groups;
-        double sum = 0;  // lane g: group g's
+        Key sum = 0;  // lane g: group g's
 #pragma unroll 1
         for (int g = 0; g < L.groups; ++g) {
             uint32_t in = 0;
@@ -160,9 +161,9 @@ __device__ __forceinline__ bool select(const S &v, const RouteLaunch &L, int lan
                 if (e >= g * size && e < (g + 1) * size)
                     in |= 1u << i;
             }
-            typename S::Type top;
+            Key top;
             const int at = best<V>(v, in, lane, top);
-            double s = S::value(top);
+            Value s = S::value(top);
             if (size > 1) {
                 if ((at & 31) == lane)
                     in &= ~(1u << (at >> 5));
@@ -170,38 +171,39 @@ __device__ __forceinline__ bool select(const S &v, const RouteLaunch &L, int lan
                 s += S::value(top);
             }
             if (lane == g)
-                sum = s;
+                sum = S::key(s);
         }
-        bool left = lane < L.groups;
         uint32_t chosen = 0;
-        double last = 0, top;
-        const int rounds = min(L.top_groups + 1, L.groups);
+        Value last = 0;
+        const int rounds = scored ? min(L.top_groups + 1, L.groups) : L.top_groups;
 #pragma unroll 1
         for (int j = 0; j < rounds; ++j) {
-            const int g = best_lane(sum, left, lane, top);
-            if (j < L.top_groups) {
+            Key top;
+            const int g = best_of(sum, lane, top);
+            if (j == L.top_groups) {
+                sure = leads(last, S::value(top), L);
+            } else {
                 chosen |= 1u << g;
-                left = left && g != lane;
-            } else if (scored && !leads(last, top, biased)) {
-                sure = false;
+                if (g == lane)
+                    sum = 0;
             }
-            last = top;
+            last = S::value(top);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (!(chosen >> min((i * 32 + lane) / size, 31) & 1))
                 open &= ~(1u << i);
     }
-    double last = 0;
+    Value last = 0;
 #pragma unroll 1
     for (int j = 0; j <= L.k; ++j) {
         if (j == L.k && !scored)
             break;
-        typename S::Type top;
+        Key top;
         const int at = best<V>(v, open, lane, top);
-        if (at < 0)
+        if (at == kNone)
             break;
-        if (scored && j > 0 && !leads(last, S::value(top), biased))
+        if (scored && j > 0 && !leads(last, S::value(top), L))
             sure = false;
         last = S::value(top);
         if (j < L.k) {
@@ -216,31 +218,30 @@ __device__ __forceinline__ bool select(const S &v, const RouteLaunch &L, int lan
 
 // The same from scores in fp64. v: V * 32 of the warp's own in shared memory.
 template <int V>
-__device__ __forceinline__ int select_exactly(const RouteLaunch &L, int64_t t, int lane, double *v)
+__device__ __forceinline__ int select_exactly(const RouteLaunch &L, int64_t t, int lane, uint64_t *v)
 {
-    double top = -INFINITY, sum = 0;
+    float top = -INFINITY;
     bool nan = false;
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
-        const double z = e < L.E ? (double)load(L.logits, L.type, t * L.E + e) : -INFINITY;
-        v[e] = z;
+        const float z = e < L.E ? load(L.logits, L.type, t * L.E + e) : -INFINITY;
         nan = nan || z != z;
-        top = fmax(top, z);
+        top = fmaxf(top, z);
     }
     nan = __any_sync(kAll, nan);
-    if (!L.sigmoid) {
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2)
-            top = fmax(top, __shfl_xor_sync(kAll, top, o));
-    }
+    for (int o = 16; o > 0; o /= 2)
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
     const bool nothing = top == -INFINITY && !nan;
+    double sum = 0;
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
-        const double z = v[i * 32 + lane];
-        const double x = exp(L.sigmoid ? -z : z - top);
+        const int e = i * 32 + lane;
+        const double z = e < L.E ? (double)load(L.logits, L.type, t * L.E + e) : -INFINITY;
+        const double x = exp(L.sigmoid ? -z : z - (double)top);
         const double s = L.sigmoid ? 1.0 / (1.0 + x) : nothing ? 0.0 : x;
-        v[i * 32 + lane] = s;
+        v[e] = (uint64_t)__double_as_longlong(s);
         sum += s;
     }
 #pragma unroll
@@ -251,12 +252,12 @@ __device__ __forceinline__ int select_exactly(const RouteLaunch &L, int64_t t, i
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
-        const double s = v[e] / sum + (L.bias && e < L.E ? (double)__ldg(L.bias + e) : 0.0);
-        v[e] = s == s ? s : -INFINITY;
+        const double s = __longlong_as_double((int64_t)v[e]);
+        v[e] = DoubleKeys::key(s / sum + (L.bias && e < L.E ? (double)__ldg(L.bias + e) : 0.0));
     }
     __syncwarp();
     int mine = 0;
-    select<V>(Doubles{v}, L, lane, false, mine);
+    select<V>(DoubleKeys{v}, L, lane, false, mine);
     __syncwarp();
     return mine;
 }
@@ -312,7 +313,7 @@ __device__ __forceinline__ Shift read_token(const RouteLaunch &L, int64_t t, int
 }
 
 template <int V>
-__device__ __forceinline__ void choose_token(const RouteLaunch &L, int64_t t, int lane, double *exact)
+__device__ __forceinline__ void choose_token(const RouteLaunch &L, int64_t t, int lane, uint64_t *exact)
 {
     float z[V];
     const Shift f = read_token<V>(L, t, lane, z);
@@ -370,26 +371,41 @@ __device__ __forceinline__ void place_block(const Args &a, int32_t *counts, int3
     __syncthreads();
     count_slots(L.experts, first, last, counts + warp * L.E, lane);
     __syncthreads();
-    // Every expert's slots in all runs and in those before; its part's length into sums.
+    // Every expert's slots in all runs (sums) and in those before (scan). Whole numbers: the
+    // order of these additions changes nothing.
     for (int e = threadIdx.x; e < L.E; e += threads) {
-        int32_t before = 0, total = 0;
-        if (a.runs > 1) {
-            for (int r = 0; r < a.runs; ++r) {
-                const int32_t c = L.counts[(int64_t)r * L.E + e];
+        int32_t total = 0;
+        if (a.runs == 1)
+            for (int w = 0; w < kWarps; ++w)
+                total += counts[w * L.E + e];
+        sums[e] = total;
+        scan[e] = 0;
+    }
+    if (a.runs > 1) {
+        __syncthreads();
+        const int parts = max(1, threads / L.E), each_run = (a.runs + parts - 1) / parts;
+        for (int i = threadIdx.x; i < parts * L.E; i += threads) {
+            const int part = i / L.E, e = i - part * L.E;
+            const int r0 = part * each_run, r1 = min(a.runs, r0 + each_run);
+            int32_t before = 0, total = 0;
+#pragma unroll 8
+            for (int r = r0; r < r1; ++r) {
+                const int32_t c = __ldg(L.counts + r * L.E + e);
                 before += r < run ? c : 0;
                 total += c;
             }
-        } else {
-            for (int w = 0; w < kWarps; ++w)
-                total += counts[w * L.E + e];
+            atomicAdd(sums + e, total);
+            atomicAdd(scan + e, before);
         }
-        int32_t at = before;
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < L.E; e += threads) {
+        int32_t at = scan[e];
         for (int w = 0; w < kWarps; ++w) {
             const int32_t c = counts[w * L.E + e];
             counts[w * L.E + e] = at;
             at += c;
         }
-        sums[e] = total;
     }
     __syncthreads();
     // Starts of the experts' parts: an exclusive scan of the padded lengths by one warp.
@@ -453,7 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 2 : 1) choose_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t from = min(L.T, blockIdx.x * a.per), to = min(L.T, from + a.per);
     for (int64_t t = from + warp; t < to; t += kWarps)
-        choose_token<V>(L, t, lane, reinterpret_cast<double *>(shared) + warp * V * 32);
+        choose_token<V>(L, t, lane, reinterpret_cast<uint64_t *>(shared) + warp * V * 32);
     __syncthreads();
     if (a.runs == 1) {
         place_block(a, shared, shared + kWarps * L.E, shared + (kWarps + 1) * L.E + 1, from * L.k,
@@ -530,93 +546,118 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- joining
 
-// Four columns a thread, a row in chunks of 1024; bound by the bytes of C.
+// Four columns a thread, a row in chunks of 1024 (or 256 of few tokens, whose call is bound by
+// latency); four rows of C are asked for at once. Bound by the bytes of C.
 template <bool VEC>
 __global__ void __launch_bounds__(256)
     join_kernel(int64_t T, int64_t N, int k, int64_t R, const float *C, const int32_t *slots,
                 const float *weights, float *Y, int64_t chunks)
 {
-    const int64_t t = blockIdx.x / chunks;
-    const int64_t n = (blockIdx.x - t * chunks) * 1024 + (VEC ? threadIdx.x * 4 : threadIdx.x);
+    const int64_t t = blockIdx.x / chunks, width = blockDim.x * 4;
+    const int64_t n = (blockIdx.x - t * chunks) * width + (VEC ? threadIdx.x * 4 : threadIdx.x);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < k; ++j) {
-        const int64_t r = __ldg(slots + t * k + j);
-        if (r < 0 || r >= R)
-            continue;
-        const float w = weights ? __ldg(weights + t * k + j) : 1.f;
-        const float *c = C + r * N + n;
-        if constexpr (VEC) {
-            if (n < N) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(c));
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-                acc[2] = fmaf(w, v.z, acc[2]);
-                acc[3] = fmaf(w, v.w, acc[3]);
-            }
-        } else {
+    if (n >= N)
+        return;
+    for (int j0 = 0; j0 < k; j0 += 4) {
+        float v[4][4], w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (n + 256 * i < N)
-                    acc[i] = fmaf(w, __ldg(c + 256 * i), acc[i]);
+                v[j][i] = 0.f;
+            if (j0 + j >= k)
+                continue;
+            const int64_t r = __ldg(slots + t * k + j0 + j);
+            if (r < 0 || r >= R)
+                continue;
+            w[j] = weights ? __ldg(weights + t * k + j0 + j) : 1.f;
+            const float *c = C + r * N + n;
+            if constexpr (VEC) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(c));
+                v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + blockDim.x * i < N)
+                        v[j][i] = __ldg(c + blockDim.x * i);
+            }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (j0 + j < k)
+                    acc[i] = fmaf(w[j], v[j][i], acc[i]);
     }
     float *y = Y + t * N + n;
     if constexpr (VEC) {
-        if (n < N)
-            *reinterpret_cast<float4 *>(y) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4 *>(y) = make_float4(acc[0], acc[1], acc[2], acc[3]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (n + 256 * i < N)
-                y[256 * i] = acc[i];
+            if (n + blockDim.x * i < N)
+                y[blockDim.x * i] = acc[i];
     }
 }
 
-// A warp a slot.
-template <bool VEC>
-__global__ void __launch_bounds__(256)
+// Four values of dY from i on, their address on 8 (fp32: 16) bytes.
+__device__ __forceinline__ float4 load4(const void *p, int type, int64_t i)
+{
+    if (type == kF32)
+        return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
+    const uint2 b = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i));
+    if (type == kBf16)
+        return make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                           __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&b.x));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&b.y));
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+
+// A slot's product is summed by the threads of a block of 128 (many slots: by a warp each), four
+// columns at a time and four of those loads under way; then warps are added in order.
+template <bool VEC, int WARPS>
+__global__ void __launch_bounds__(128)
     join_backward_kernel(int64_t count, int64_t N, int k, int64_t R, int type, const void *dY,
                          const float *C, const int32_t *slots, float *dweights)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= count)
-        return;
-    const int64_t r = slots[i], t = i / k;
+    __shared__ float part[4];
+    constexpr int THREADS = WARPS * 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t i = (int64_t)blockIdx.x * (4 / WARPS) + (WARPS == 4 ? 0 : warp);
+    const int id = WARPS == 4 ? threadIdx.x : lane;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const int64_t r = i < count ? slots[i] : -1, t = i / k;
     if (r >= 0 && r < R) {
         const float *c = C + r * N;
         if constexpr (VEC) {
-            for (int64_t n = lane * 4; n < N; n += 128) {
+#pragma unroll 4
+            for (int64_t n = id * 4; n < N; n += THREADS * 4) {
                 const float4 v = __ldg(reinterpret_cast<const float4 *>(c + n));
-                float4 d;
-                if (type == kF32) {
-                    d = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(dY) + t * N + n));
-                } else {
-                    const uint2 b = __ldg(reinterpret_cast<const uint2 *>(
-                        static_cast<const uint16_t *>(dY) + t * N + n));
-                    if (type == kBf16) {
-                        d = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
-                                        __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
-                    } else {
-                        const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&b.x));
-                        const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&b.y));
-                        d = make_float4(lo.x, lo.y, hi.x, hi.y);
-                    }
-                }
+                const float4 d = load4(dY, type, t * N + n);
                 sum[0] = fmaf(d.x, v.x, sum[0]);
                 sum[1] = fmaf(d.y, v.y, sum[1]);
                 sum[2] = fmaf(d.z, v.z, sum[2]);
                 sum[3] = fmaf(d.w, v.w, sum[3]);
             }
         } else {
-            for (int64_t n = lane; n < N; n += 32)
+#pragma unroll 4
+            for (int64_t n = id; n < N; n += THREADS)
                 sum[0] = fmaf(load(dY, type, t * N + n), __ldg(c + n), sum[0]);
         }
     }
-    const float all = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-    if (lane == 0)
+    float all = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if constexpr (WARPS == 4) {
+        if (lane == 0)
+            part[warp] = all;
+        __syncthreads();
+        all = (part[0] + part[1]) + (part[2] + part[3]);
+        if (threadIdx.x == 0)
+            dweights[i] = all;
+    } else if (lane == 0 && i < count) {
         dweights[i] = all;
+    }
 }
 
 static int runs_of(int64_t T) { return T <= kOneBlock ? 1 : (int)(T < kMaxRuns * 2 ? (T + 1) / 2 : kMaxRuns); }
@@ -702,14 +743,35 @@ cudaError_t launch_experts_join(int64_t T, int64_t N, int k, int64_t R, const fl
                                 const int32_t *slots, const float *weights, float *Y,
                                 cudaStream_t stream)
 {
-    const int64_t chunks = (N + 1023) / 1024;
+    const int threads = T * N < 152 * 4096 ? 64 : 256;
+    const int64_t chunks = (N + threads * 4 - 1) / (threads * 4);
     if (T * chunks > 0x7fffffff)
         return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(T * chunks);
     if (N % 4 == 0 && ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(Y)) & 15) == 0)
-        route::join_kernel<true><<<grid, 256, 0, stream>>>(T, N, k, R, C, slots, weights, Y, chunks);
+        route::join_kernel<true><<<grid, threads, 0, stream>>>(T, N, k, R, C, slots, weights, Y, chunks);
     else
-        route::join_kernel<false><<<grid, 256, 0, stream>>>(T, N, k, R, C, slots, weights, Y, chunks);
+        route::join_kernel<false><<<grid, threads, 0, stream>>>(T, N, k, R, C, slots, weights, Y, chunks);
+    return cudaGetLastError();
+}
+
+template <bool VEC>
+static cudaError_t launch_join_backward(int64_t T, int64_t N, int k, int64_t R, int type,
+                                        const void *dY, const float *C, const int32_t *slots,
+                                        float *dweights, cudaStream_t stream)
+{
+    // A block a slot while that leaves SMs idle.
+    const int64_t count = T * k;
+    const bool few = count < 152 * 16;
+    const int64_t blocks = few ? count : (count + 3) / 4;
+    if (blocks > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    if (few)
+        route::join_backward_kernel<VEC, 4><<<(unsigned)blocks, 128, 0, stream>>>(
+            count, N, k, R, type, dY, C, slots, dweights);
+    else
+        route::join_backward_kernel<VEC, 1><<<(unsigned)blocks, 128, 0, stream>>>(
+            count, N, k, R, type, dY, C, slots, dweights);
     return cudaGetLastError();
 }
 
@@ -717,16 +779,10 @@ cudaError_t launch_experts_join_backward(int64_t T, int64_t N, int k, int64_t R,
                                          const void *dY, const float *C, const int32_t *slots,
                                          float *dweights, cudaStream_t stream)
 {
-    const int64_t count = T * k, blocks = (count + 7) / 8;
-    if (blocks > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    if (N % 4 == 0 && ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(dY)) & 15) == 0)
-        route::join_backward_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(
-            count, N, k, R, type, dY, C, slots, dweights);
-    else
-        route::join_backward_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(
-            count, N, k, R, type, dY, C, slots, dweights);
-    return cudaGetLastError();
+    const bool vec =
+        N % 4 == 0 && ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(dY)) & 15) == 0;
+    return vec ? launch_join_backward<true>(T, N, k, R, type, dY, C, slots, dweights, stream)
+               : launch_join_backward<false>(T, N, k, R, type, dY, C, slots, dweights, stream);
 }
 
 } // namespace rtm
