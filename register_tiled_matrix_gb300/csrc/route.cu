@@ -52,27 +52,22 @@ __device__ __forceinline__ float of_key(uint32_t k)
     return __uint_as_float((int32_t)k < 0 ? k & 0x7fffffffu : ~k);
 }
 
-// The values that a selection runs on, a lane's i-th, as ordered bits: of fp32 in registers, of
-// fp64 in the warp's shared memory (the GPU has few fp64 units; comparing bits needs none).
-template <int V>
-struct Keys {
-    using Type = uint32_t;
+// What a selection compares: ordered bits, of fp32 or of fp64 (the GPU has few fp64 units;
+// comparing bits needs none). A key is never 0.
+struct Single {
+    using Key = uint32_t;
     using Value = float;
-    uint32_t v[V];
-    __device__ __forceinline__ Type at(int i, int) const { return v[i]; }
-    static __device__ __forceinline__ Value value(Type k) { return of_key(k); }
-    static __device__ __forceinline__ Type key(Value f) { return key_of(f); }
+    static __device__ __forceinline__ Value value(Key k) { return of_key(k); }
+    static __device__ __forceinline__ Key key(Value f) { return key_of(f); }
 };
-struct DoubleKeys {
-    using Type = uint64_t;
+struct Double {
+    using Key = uint64_t;
     using Value = double;
-    const uint64_t *v;
-    __device__ __forceinline__ Type at(int i, int lane) const { return v[i * 32 + lane]; }
-    static __device__ __forceinline__ Value value(Type k)
+    static __device__ __forceinline__ Value value(Key k)
     {
         return __longlong_as_double((int64_t)k < 0 ? k & 0x7fffffffffffffffull : ~k);
     }
-    static __device__ __forceinline__ Type key(Value f)
+    static __device__ __forceinline__ Key key(Value f)
     {
         const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
         return f != f ? 0x000fffffffffffffull : (int64_t)u < 0 ? ~u : u | 0x8000000000000000ull;
@@ -81,39 +76,38 @@ struct DoubleKeys {
 
 constexpr int kNone = 0x7fffffff;
 
-// The largest of the lanes' keys and the index that came with it, the lowest on a tie; kNone
-// where no lane has one. Keys are never 0.
-__device__ __forceinline__ int best_of(uint32_t mine, int at, uint32_t &top)
-{
-    const uint32_t m = __reduce_max_sync(kAll, mine);
-    top = m;
-    return (int)__reduce_min_sync(kAll, mine == m ? (uint32_t)at : (uint32_t)kNone);
-}
-__device__ __forceinline__ int best_of(uint64_t mine, int at, uint64_t &top)
+// The largest of the lanes' keys.
+__device__ __forceinline__ uint32_t warp_max(uint32_t mine) { return __reduce_max_sync(kAll, mine); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t mine)
 {
     const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(mine >> 32));
-    const bool in = (uint32_t)(mine >> 32) == hi;
-    const uint32_t lo = __reduce_max_sync(kAll, in ? (uint32_t)mine : 0u);
-    top = (uint64_t)hi << 32 | lo;
-    return (int)__reduce_min_sync(kAll, mine == top ? (uint32_t)at : (uint32_t)kNone);
+    const uint32_t lo =
+        __reduce_max_sync(kAll, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+    return (uint64_t)hi << 32 | lo;
 }
 
-// The largest of the lanes' open values (bit i of `open`: the i-th takes part) and its index
-// i * 32 + lane.
-template <int V, class S>
-__device__ __forceinline__ int best(const S &v, uint32_t open, int lane, typename S::Type &top)
+// The largest key v[i] of expert i * 32 + lane and its expert, the lowest on a tie, whose key
+// becomes 0. kNone where all are.
+template <int V, class Key>
+__device__ __forceinline__ int take_best(Key (&v)[V], int lane, Key &top)
 {
-    typename S::Type mine = 0;
-    int at = kNone;
+    Key mine = v[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const typename S::Type x = (open >> i & 1) ? v.at(i, lane) : 0;
-        if (x > mine) {
-            mine = x;
-            at = i * 32 + lane;
-        }
-    }
-    return best_of(mine, at, top);
+    for (int i = 1; i < V; ++i)
+        mine = v[i] > mine ? v[i] : mine;
+    top = warp_max(mine);
+    uint32_t at = kNone;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+        at = v[i] == top ? i * 32 + lane : at;
+    at = __reduce_min_sync(kAll, at);
+    if (top == 0)
+        return kNone;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (at == i * 32 + lane)
+            v[i] = 0;
+    return (int)at;
 }
 
 // Whether a's lead over b is beyond what fp32 can have moved. A sigmoid is within 2e-7 of the
@@ -136,98 +130,86 @@ struct Args {
 };
 
 // The k chosen experts, lane j the j-th. `scored`: v are scores whose gaps count; returns
-// whether all of them were wide enough.
-template <int V, class S>
-__device__ __forceinline__ bool select(const S &v, const RouteLaunch &L, int lane, bool scored,
-                                       int &mine)
+// whether all of them were wide enough. scratch: V * 32 keys of the warp's own.
+template <class S, int V>
+__device__ __forceinline__ bool select(typename S::Key (&v)[V], const RouteLaunch &L, int lane,
+                                       bool scored, typename S::Key *scratch, int &mine)
 {
-    using Key = typename S::Type;
+    using Key = typename S::Key;
     using Value = typename S::Value;
-    uint32_t open = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i * 32 + lane < L.E)
-            open |= 1u << i;
     bool sure = true;
     if (L.groups > 1) {
-        const int size = L.E / L.groups;
-        Key sum = 0;  // lane g: group g's
-#pragma unroll 1
-        for (int g = 0; g < L.groups; ++g) {
-            uint32_t in = 0;
+        // 32 / groups lanes (a power of two) find the two largest of a group.
+        const int size = L.E / L.groups, share = 1 << (31 - __clz(32 / L.groups));
+        const int group = lane / share;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = i * 32 + lane;
-                if (e >= g * size && e < (g + 1) * size)
-                    in |= 1u << i;
+        for (int i = 0; i < V; ++i)
+            scratch[i * 32 + lane] = v[i];
+        __syncwarp();
+        Key one = 0, two = 0;
+        if (group < L.groups)
+            for (int i = lane % share; i < size; i += share) {
+                const Key x = scratch[group * size + i];
+                two = x > one ? one : x > two ? x : two;
+                one = x > one ? x : one;
             }
-            Key top;
-            const int at = best<V>(v, in, lane, top);
-            Value s = S::value(top);
-            if (size > 1) {
-                if ((at & 31) == lane)
-                    in &= ~(1u << (at >> 5));
-                best<V>(v, in, lane, top);
-                s += S::value(top);
-            }
-            if (lane == g)
-                sum = S::key(s);
+        for (int o = 1; o < share; o *= 2) {
+            const Key x = __shfl_xor_sync(kAll, one, o), y = __shfl_xor_sync(kAll, two, o);
+            const Key low = one < x ? one : x, high = two > y ? two : y;
+            one = one > x ? one : x;
+            two = low > high ? low : high;
         }
+        __syncwarp();
+        Key sum[1] = {S::key(size > 1 ? S::value(one) + S::value(two) : S::value(one))};
+        sum[0] = __shfl_sync(kAll, sum[0], min(lane, L.groups - 1) * share);  // lane g: group g's
+        if (lane >= L.groups)
+            sum[0] = 0;
         uint32_t chosen = 0;
         Value last = 0;
         const int rounds = scored ? min(L.top_groups + 1, L.groups) : L.top_groups;
 #pragma unroll 1
         for (int j = 0; j < rounds; ++j) {
             Key top;
-            const int g = best_of(sum, lane, top);
-            if (j == L.top_groups) {
+            const int g = take_best<1>(sum, lane, top);
+            if (j == L.top_groups)
                 sure = leads(last, S::value(top), L);
-            } else {
+            else
                 chosen |= 1u << g;
-                if (g == lane)
-                    sum = 0;
-            }
             last = S::value(top);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (!(chosen >> min((i * 32 + lane) / size, 31) & 1))
-                open &= ~(1u << i);
+                v[i] = 0;
     }
     Value last = 0;
+    const int rounds = scored ? L.k + 1 : L.k;
 #pragma unroll 1
-    for (int j = 0; j <= L.k; ++j) {
-        if (j == L.k && !scored)
-            break;
+    for (int j = 0; j < rounds; ++j) {
         Key top;
-        const int at = best<V>(v, open, lane, top);
+        const int at = take_best<V>(v, lane, top);
         if (at == kNone)
             break;
         if (scored && j > 0 && !leads(last, S::value(top), L))
             sure = false;
         last = S::value(top);
-        if (j < L.k) {
-            if (lane == j)
-                mine = at;
-            if ((at & 31) == lane)
-                open &= ~(1u << (at >> 5));
-        }
+        if (lane == j && j < L.k)
+            mine = at;
     }
     return sure;
 }
 
-// The same from scores in fp64. v: V * 32 of the warp's own in shared memory.
+// The same from scores in fp64; z: the token's logits in the warp's shared memory.
 template <int V>
-__device__ __forceinline__ int select_exactly(const RouteLaunch &L, int64_t t, int lane, uint64_t *v)
+__device__ __forceinline__ int select_exactly(const RouteLaunch &L, const float *z, int lane,
+                                              uint64_t *scratch)
 {
     float top = -INFINITY;
     bool nan = false;
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        const float z = e < L.E ? load(L.logits, L.type, t * L.E + e) : -INFINITY;
-        nan = nan || z != z;
-        top = fmaxf(top, z);
+        nan = nan || z[i * 32 + lane] != z[i * 32 + lane];
+        top = fmaxf(top, z[i * 32 + lane]);
     }
     nan = __any_sync(kAll, nan);
 #pragma unroll
@@ -237,11 +219,10 @@ __device__ __forceinline__ int select_exactly(const RouteLaunch &L, int64_t t, i
     double sum = 0;
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        const double z = e < L.E ? (double)load(L.logits, L.type, t * L.E + e) : -INFINITY;
-        const double x = exp(L.sigmoid ? -z : z - (double)top);
-        const double s = L.sigmoid ? 1.0 / (1.0 + x) : nothing ? 0.0 : x;
-        v[e] = (uint64_t)__double_as_longlong(s);
+        const double x = (double)z[i * 32 + lane];
+        const double w = exp(L.sigmoid ? -x : x - (double)top);
+        const double s = L.sigmoid ? 1.0 / (1.0 + w) : nothing ? 0.0 : w;
+        scratch[i * 32 + lane] = (uint64_t)__double_as_longlong(s);
         sum += s;
     }
 #pragma unroll
@@ -252,13 +233,17 @@ __device__ __forceinline__ int select_exactly(const RouteLaunch &L, int64_t t, i
 #pragma unroll 1
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
-        const double s = __longlong_as_double((int64_t)v[e]);
-        v[e] = DoubleKeys::key(s / sum + (L.bias && e < L.E ? (double)__ldg(L.bias + e) : 0.0));
+        const double s = __longlong_as_double((int64_t)scratch[e]);
+        scratch[e] =
+            e < L.E ? Double::key(s / sum + (L.bias ? (double)__ldg(L.bias + e) : 0.0)) : 0;
     }
+    uint64_t v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = scratch[i * 32 + lane];
     __syncwarp();
     int mine = 0;
-    select<V>(DoubleKeys{v}, L, lane, false, mine);
-    __syncwarp();
+    select<Double, V>(v, L, lane, false, scratch, mine);
     return mine;
 }
 
@@ -284,60 +269,75 @@ __device__ __forceinline__ float score_of(const RouteLaunch &L, const Shift &f, 
 
 // z[i]: the logit of expert i * 32 + lane, -inf behind the last.
 template <int V>
-__device__ __forceinline__ Shift read_token(const RouteLaunch &L, int64_t t, int lane, float (&z)[V])
+__device__ __forceinline__ void read_token(const RouteLaunch &L, int64_t t, int lane, float (&z)[V])
 {
-    float top = -INFINITY;
-    bool nan = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
         z[i] = e < L.E ? load(L.logits, L.type, t * L.E + e) : -INFINITY;
-        nan = nan || z[i] != z[i];
-        top = fmaxf(top, z[i]);
     }
+}
+
+template <int V>
+__device__ __forceinline__ Shift shift_of(const RouteLaunch &L, const float (&z)[V])
+{
     Shift f = {0.f, 1.f, false};
     if (L.sigmoid)
         return f;
+    float top = -INFINITY;
+    bool nan = false;
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2)
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    f.top = top;
+    for (int i = 0; i < V; ++i) {
+        nan = nan || z[i] != z[i];
+        top = fmaxf(top, z[i]);
+    }
+    f.top = of_key(warp_max(key_of(top)));
     nan = __any_sync(kAll, nan);
-    f.nothing = top == -INFINITY && !nan;
+    f.nothing = f.top == -INFINITY && !nan;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        sum += f.nothing ? 0.f : expf(z[i] - top);
+        sum += f.nothing ? 0.f : expf(z[i] - f.top);
     f.whole = warp_sum(sum);  // NaN where a logit is
     return f;
 }
 
+// The experts and weights of the token with logits z; bias: the experts' (0 without one). At
+// `chosen` (shared memory; may be null) too. In shared memory of the warp's own: scratch, V * 32
+// keys of 64 bits, and held, V * 32 logits.
 template <int V>
-__device__ __forceinline__ void choose_token(const RouteLaunch &L, int64_t t, int lane, uint64_t *exact)
+__device__ __forceinline__ void choose_token(const RouteLaunch &L, int64_t t, int lane,
+                                             const float (&z)[V], const float (&bias)[V],
+                                             uint64_t *scratch, float *held, int32_t *chosen)
 {
-    float z[V];
-    const Shift f = read_token<V>(L, t, lane, z);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        held[i * 32 + lane] = z[i];
+    const Shift f = shift_of<V>(L, z);
     const bool by_logit = !L.bias && L.groups == 1;
-    Keys<V> keys;
+    uint32_t keys[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
         float x = z[i];
         if (!by_logit)
-            x = score_of(L, f, x) + (L.bias && e < L.E ? __ldg(L.bias + e) : 0.f);
-        keys.v[i] = key_of(x);
+            x = score_of(L, f, x) + bias[i];
+        keys[i] = i * 32 + lane < L.E ? key_of(x) : 0;
     }
     int mine = 0;
-    if (!select<V>(keys, L, lane, !by_logit, mine))
-        mine = select_exactly<V>(L, t, lane, exact);
+    if (!select<Single, V>(keys, L, lane, !by_logit, reinterpret_cast<uint32_t *>(scratch), mine))
+        mine = select_exactly<V>(L, held, lane, scratch);
+    __syncwarp();
     float p = 0.f;
     if (lane < L.k)
-        p = score_of(L, f, load(L.logits, L.type, t * L.E + mine));
+        p = score_of(L, f, held[mine]);
     const float total = warp_sum(p) + kNil;
     if (lane < L.k) {
         L.experts[t * L.k + lane] = mine;
         L.weights[t * L.k + lane] = L.scale * (L.renormalise ? p / total : p);
+        if (chosen)
+            chosen[lane] = mine;
     }
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- order by expert
@@ -356,39 +356,35 @@ __device__ __forceinline__ void count_slots(const int32_t *experts, int64_t from
     }
 }
 
-// Places the block's slots. counts: kWarps x E in shared memory, each warp's own; `sums`: E
-// and one more. With more than one run the other runs' counts are in L.counts.
-__device__ __forceinline__ void place_block(const Args &a, int32_t *counts, int32_t *sums,
-                                            int32_t *scan, int64_t from, int64_t to)
+// Places the block's slots [from, to) with the experts that `experts` holds from `from` on. In
+// shared memory: counts (kWarps x E, each warp's own), sums (E), scan (E + 1), warps (kWarps).
+// With more than one run the other runs' counts are in L.counts.
+__device__ __forceinline__ void place_block(const Args &a, const int32_t *experts, int32_t *counts,
+                                            int32_t *sums, int32_t *scan, int32_t *warps,
+                                            int64_t from, int64_t to)
 {
     const RouteLaunch &L = a.L;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = kWarps * 32;
     const int run = blockIdx.x;
     const int64_t n = to - from, each = (n + kWarps - 1) / kWarps;
-    const int64_t first = min(to, from + warp * each), last = min(to, first + each);
+    const int64_t first = min(n, warp * each), last = min(n, first + each);
     for (int i = threadIdx.x; i < kWarps * L.E; i += threads)
         counts[i] = 0;
-    __syncthreads();
-    count_slots(L.experts, first, last, counts + warp * L.E, lane);
-    __syncthreads();
-    // Every expert's slots in all runs (sums) and in those before (scan). Whole numbers: the
-    // order of these additions changes nothing.
     for (int e = threadIdx.x; e < L.E; e += threads) {
-        int32_t total = 0;
-        if (a.runs == 1)
-            for (int w = 0; w < kWarps; ++w)
-                total += counts[w * L.E + e];
-        sums[e] = total;
+        sums[e] = 0;
         scan[e] = 0;
     }
+    __syncthreads();
+    count_slots(experts, first, last, counts + warp * L.E, lane);
+    // Every expert's slots in all runs (sums) and in those before (scan). Whole numbers: the
+    // order of these additions changes nothing.
     if (a.runs > 1) {
-        __syncthreads();
         const int parts = max(1, threads / L.E), each_run = (a.runs + parts - 1) / parts;
         for (int i = threadIdx.x; i < parts * L.E; i += threads) {
             const int part = i / L.E, e = i - part * L.E;
             const int r0 = part * each_run, r1 = min(a.runs, r0 + each_run);
             int32_t before = 0, total = 0;
-#pragma unroll 8
+#pragma unroll 16
             for (int r = r0; r < r1; ++r) {
                 const int32_t c = __ldg(L.counts + r * L.E + e);
                 before += r < run ? c : 0;
@@ -397,36 +393,51 @@ __device__ __forceinline__ void place_block(const Args &a, int32_t *counts, int3
             atomicAdd(sums + e, total);
             atomicAdd(scan + e, before);
         }
-        __syncthreads();
-    }
-    for (int e = threadIdx.x; e < L.E; e += threads) {
-        int32_t at = scan[e];
-        for (int w = 0; w < kWarps; ++w) {
-            const int32_t c = counts[w * L.E + e];
-            counts[w * L.E + e] = at;
-            at += c;
-        }
     }
     __syncthreads();
-    // Starts of the experts' parts: an exclusive scan of the padded lengths by one warp.
-    if (warp == 0) {
-        int32_t carry = 0;
-        for (int b = 0; b < L.E; b += 32) {
-            const int e = b + lane;
-            const int32_t c = e < L.E ? (sums[e] + L.align - 1) / L.align * L.align : 0;
-            int32_t x = c;
+    // A thread has one or two neighbouring experts: its warps' first places among the expert's
+    // slots, and the padded length of its part, whose exclusive sum is the part's start.
+    const int own = L.E > threads ? 2 : 1;
+    int32_t length[2] = {0, 0};
 #pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int32_t y = __shfl_up_sync(kAll, x, o);
-                if (lane >= o)
-                    x += y;
+    for (int i = 0; i < 2; ++i) {
+        const int e = threadIdx.x * own + i;
+        if (i < own && e < L.E) {
+            int32_t at = scan[e];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const int32_t c = counts[w * L.E + e];
+                counts[w * L.E + e] = at;
+                at += c;
             }
-            if (e < L.E)
-                scan[e] = carry + x - c;
-            carry += __shfl_sync(kAll, x, 31);
+            if (a.runs == 1)
+                sums[e] = at;
+            length[i] = (sums[e] + L.align - 1) / L.align * L.align;
         }
-        if (lane == 0)
-            scan[L.E] = carry;
+    }
+    int32_t x = length[0] + length[1];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int32_t y = __shfl_up_sync(kAll, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    if (lane == 31)
+        warps[warp] = x;
+    __syncthreads();  // and every read of scan as the counts before
+    int32_t start = x - length[0] - length[1];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        start += w < warp ? warps[w] : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = threadIdx.x * own + i;
+        if (i < own && e < L.E) {
+            scan[e] = start;
+            start += length[i];
+            if (e == L.E - 1)
+                scan[L.E] = start;
+        }
     }
     __syncthreads();
     if (run == 0)
@@ -435,7 +446,7 @@ __device__ __forceinline__ void place_block(const Args &a, int32_t *counts, int3
     // Slots in order: this warp's run of them.
     for (int64_t i = first; i < last; i += 32) {
         const bool in = i + lane < last;
-        const int e = in ? L.experts[i + lane] : -1;
+        const int e = in ? experts[i + lane] : -1;
         const uint32_t same = __match_any_sync(kAll, e);
         const int rank = __popc(same & ((1u << lane) - 1));
         int32_t at = 0;
@@ -446,34 +457,72 @@ __device__ __forceinline__ void place_block(const Args &a, int32_t *counts, int3
             if (rank == 0)
                 counts[warp * L.E + e] += __popc(same);
             const int32_t to_row = scan[e] + at;
-            L.rows[to_row] = (int32_t)(i + lane);
-            L.slots[i + lane] = to_row;
+            L.rows[to_row] = (int32_t)(from + i + lane);
+            L.slots[from + i + lane] = to_row;
         }
         __syncwarp();
     }
     // Rows that no slot takes: the ends of the parts, and what lies behind the last.
-    for (int e = run * kWarps + warp; e < L.E; e += a.runs * kWarps)
-        for (int32_t i = scan[e] + sums[e] + lane; i < scan[e + 1]; i += 32)
-            L.rows[i] = -1;
+    if (L.align > 1)
+        for (int e = run * kWarps + warp; e < L.E; e += a.runs * kWarps)
+            for (int32_t i = scan[e] + sums[e] + lane; i < scan[e + 1]; i += 32)
+                L.rows[i] = -1;
     for (int64_t i = scan[L.E] + (int64_t)run * threads + threadIdx.x; i < L.R;
          i += (int64_t)a.runs * threads)
         L.rows[i] = -1;
 }
 
-// Experts and weights of a run of tokens, and the run's slots counted by expert.
+// Words of shared memory of place_block.
+__host__ __device__ constexpr int place_words(int E) { return (kWarps + 2) * E + 1 + kWarps; }
+
+__device__ __forceinline__ void place_in(const Args &a, const int32_t *experts, int32_t *words,
+                                         int64_t from, int64_t to)
+{
+    const int E = a.L.E;
+    place_block(a, experts, words, words + kWarps * E, words + (kWarps + 1) * E,
+                words + (kWarps + 2) * E + 1, from, to);
+}
+
+// Experts and weights of a run of tokens, and the run's slots counted by expert; a single run
+// places them, too.
 template <int V>
-__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 2 : 1) choose_kernel(const Args a)
+__global__ void __launch_bounds__(kWarps * 32, 1) choose_kernel(const Args a)
 {
     extern __shared__ __align__(8) int32_t shared[];
+    __shared__ int32_t chosen[kOneBlock * kRouteMaxChosen];
     const RouteLaunch &L = a.L;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t from = min(L.T, blockIdx.x * a.per), to = min(L.T, from + a.per);
-    for (int64_t t = from + warp; t < to; t += kWarps)
-        choose_token<V>(L, t, lane, reinterpret_cast<uint64_t *>(shared) + warp * V * 32);
+    uint64_t *scratch = reinterpret_cast<uint64_t *>(shared) + warp * V * 32;
+    float *held = reinterpret_cast<float *>(shared) + (kWarps * 2 + warp) * V * 32;
+    constexpr bool AHEAD = V <= 8;  // the next token's logits are read while this one is chosen for
+    float bias[V], z[V], next[V];
+    auto read_bias = [&]() {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            bias[i] = L.bias && i * 32 + lane < L.E ? __ldg(L.bias + i * 32 + lane) : 0.f;
+    };
+    if constexpr (AHEAD) {
+        read_bias();
+        if (from + warp < to)
+            read_token<V>(L, from + warp, lane, next);
+    }
+    for (int64_t t = from + warp; t < to; t += kWarps) {
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                z[i] = next[i];
+            if (t + kWarps < to)
+                read_token<V>(L, t + kWarps, lane, next);
+        } else {
+            read_token<V>(L, t, lane, z);
+            read_bias();
+        }
+        choose_token<V>(L, t, lane, z, bias, scratch, held, a.runs == 1 ? chosen + t * L.k : nullptr);
+    }
     __syncthreads();
     if (a.runs == 1) {
-        place_block(a, shared, shared + kWarps * L.E, shared + (kWarps + 1) * L.E + 1, from * L.k,
-                    to * L.k);
+        place_in(a, chosen, shared, from * L.k, to * L.k);
         return;
     }
     for (int e = threadIdx.x; e < L.E; e += kWarps * 32)
@@ -492,8 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32) place_kernel(const Args a)
     extern __shared__ int32_t shared[];
     const RouteLaunch &L = a.L;
     const int64_t from = min(L.T, blockIdx.x * a.per), to = min(L.T, from + a.per);
-    place_block(a, shared, shared + kWarps * L.E, shared + (kWarps + 1) * L.E + 1, from * L.k,
-                to * L.k);
+    place_in(a, L.experts + from * L.k, shared, from * L.k, to * L.k);
 }
 
 // dz from dw, a warp a token: with g_j = ds of the chosen (through the renormalisation where
@@ -508,7 +556,8 @@ __global__ void __launch_bounds__(256)
     if (t >= L.T)
         return;
     float z[V];
-    const Shift f = read_token<V>(L, t, lane, z);
+    read_token<V>(L, t, lane, z);
+    const Shift f = shift_of<V>(L, z);
     int mine = -1;
     float dw = 0.f, p = 0.f;
     if (lane < L.k) {
@@ -662,12 +711,12 @@ __global__ void __launch_bounds__(128)
 
 static int runs_of(int64_t T) { return T <= kOneBlock ? 1 : (int)(T < kMaxRuns * 2 ? (T + 1) / 2 : kMaxRuns); }
 
-constexpr size_t place_bytes(int E) { return ((size_t)(kWarps + 2) * E + 2) * 4; }
+constexpr size_t place_bytes(int E) { return (size_t)place_words(E) * 4; }
 
 template <int V>
 static cudaError_t launch_choose(const Args &a, cudaStream_t stream)
 {
-    constexpr size_t exact = (size_t)kWarps * V * 32 * 8;  // select_exactly's scores
+    constexpr size_t exact = (size_t)kWarps * V * 32 * 12;  // the warps' scratch and logits
     constexpr size_t most = place_bytes(V * 32);
     static std::atomic<uint64_t> done{0};
     const cudaError_t e =
