@@ -28,9 +28,11 @@ namespace rtm {
 namespace route {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kOneBlock = 128;   // tokens
+constexpr int kOneBlock = 32;    // tokens
 constexpr int kMaxRuns = 152;    // blocks of the two-launch form: one an SM
-constexpr int kWarps = 16;       // of a block
+// Warps of a block: as many as its registers and shared memory allow; eight for at most as many
+// tokens (one token of 256 experts: 13.4 us with 32, where most only take part in the order).
+__host__ __device__ constexpr int warps_of(int V, bool few) { return few ? 8 : V <= 8 ? 32 : 16; }
 constexpr float kNil = 1e-20f;
 constexpr uint32_t kNegInfKey = 0x007fffffu;
 
@@ -217,7 +219,8 @@ __device__ __forceinline__ int select_exactly(const RouteLaunch &L, const float 
         top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
     const bool nothing = top == -INFINITY && !nan;
     double sum = 0;
-#pragma unroll 1
+    constexpr int TOGETHER = V < 4 ? V : 4;  // fp64 instructions are slow to answer
+#pragma unroll TOGETHER
     for (int i = 0; i < V; ++i) {
         const double x = (double)z[i * 32 + lane];
         const double w = exp(L.sigmoid ? -x : x - (double)top);
@@ -230,17 +233,14 @@ __device__ __forceinline__ int select_exactly(const RouteLaunch &L, const float 
         sum += __shfl_xor_sync(kAll, sum, o);
     if (L.sigmoid || nothing)
         sum = 1.0;
-#pragma unroll 1
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        const double s = __longlong_as_double((int64_t)scratch[e]);
-        scratch[e] =
-            e < L.E ? Double::key(s / sum + (L.bias ? (double)__ldg(L.bias + e) : 0.0)) : 0;
-    }
+    const double part = 1.0 / sum;
     uint64_t v[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        v[i] = scratch[i * 32 + lane];
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        const double s = __longlong_as_double((int64_t)scratch[e]) * part;
+        v[i] = e < L.E ? Double::key(s + (L.bias ? (double)__ldg(L.bias + e) : 0.0)) : 0;
+    }
     __syncwarp();
     int mine = 0;
     select<Double, V>(v, L, lane, false, scratch, mine);
@@ -255,16 +255,16 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// What a token's scores are made with: s = exp(z - top) / whole, or the sigmoid.
+// What a token's scores are made with: s = exp(z - top) * part, or the sigmoid.
 struct Shift {
-    float top, whole;
+    float top, part;
     bool nothing;  // every logit is -inf: softmax scores are 0
 };
 __device__ __forceinline__ float score_of(const RouteLaunch &L, const Shift &f, float z)
 {
     if (L.sigmoid)
-        return 1.f / (1.f + expf(-z));
-    return f.nothing ? 0.f : expf(z - f.top) / f.whole;
+        return __fdividef(1.f, 1.f + expf(-z));  // 0 where the score is below 2^-126
+    return f.nothing ? 0.f : expf(z - f.top) * f.part;
 }
 
 // z[i]: the logit of expert i * 32 + lane, -inf behind the last.
@@ -298,7 +298,7 @@ __device__ __forceinline__ Shift shift_of(const RouteLaunch &L, const float (&z)
 #pragma unroll
     for (int i = 0; i < V; ++i)
         sum += f.nothing ? 0.f : expf(z[i] - f.top);
-    f.whole = warp_sum(sum);  // NaN where a logit is
+    f.part = f.nothing ? 0.f : 1.f / warp_sum(sum);  // NaN where a logit is
     return f;
 }
 
@@ -359,13 +359,14 @@ __device__ __forceinline__ void count_slots(const int32_t *experts, int64_t from
 // Places the block's slots [from, to) with the experts that `experts` holds from `from` on. In
 // shared memory: counts (kWarps x E, each warp's own), sums (E), scan (E + 1), warps (kWarps).
 // With more than one run the other runs' counts are in L.counts.
+template <int kWarps>
 __device__ __forceinline__ void place_block(const Args &a, const int32_t *experts, int32_t *counts,
                                             int32_t *sums, int32_t *scan, int32_t *warps,
                                             int64_t from, int64_t to)
 {
     const RouteLaunch &L = a.L;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = kWarps * 32;
-    const int run = blockIdx.x;
+    constexpr int threads = kWarps * 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, run = blockIdx.x;
     const int64_t n = to - from, each = (n + kWarps - 1) / kWarps;
     const int64_t first = min(n, warp * each), last = min(n, first + each);
     for (int i = threadIdx.x; i < kWarps * L.E; i += threads)
@@ -395,12 +396,14 @@ __device__ __forceinline__ void place_block(const Args &a, const int32_t *expert
         }
     }
     __syncthreads();
-    // A thread has one or two neighbouring experts: its warps' first places among the expert's
-    // slots, and the padded length of its part, whose exclusive sum is the part's start.
-    const int own = L.E > threads ? 2 : 1;
-    int32_t length[2] = {0, 0};
+    // A thread has `own` neighbouring experts: the warps' first places among an expert's slots,
+    // and the padded length of its part, whose exclusive sum is the part's start.
+    constexpr int OWN = (kRouteMaxExperts + threads - 1) / threads;
+    const int own = (L.E + threads - 1) / threads;
+    int32_t length[OWN], sum = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < OWN; ++i) {
+        length[i] = 0;
         const int e = threadIdx.x * own + i;
         if (i < own && e < L.E) {
             int32_t at = scan[e];
@@ -413,9 +416,10 @@ __device__ __forceinline__ void place_block(const Args &a, const int32_t *expert
             if (a.runs == 1)
                 sums[e] = at;
             length[i] = (sums[e] + L.align - 1) / L.align * L.align;
+            sum += length[i];
         }
     }
-    int32_t x = length[0] + length[1];
+    int32_t x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const int32_t y = __shfl_up_sync(kAll, x, o);
@@ -425,12 +429,12 @@ __device__ __forceinline__ void place_block(const Args &a, const int32_t *expert
     if (lane == 31)
         warps[warp] = x;
     __syncthreads();  // and every read of scan as the counts before
-    int32_t start = x - length[0] - length[1];
+    int32_t start = x - sum;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
         start += w < warp ? warps[w] : 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < OWN; ++i) {
         const int e = threadIdx.x * own + i;
         if (i < own && e < L.E) {
             scan[e] = start;
@@ -473,21 +477,23 @@ __device__ __forceinline__ void place_block(const Args &a, const int32_t *expert
 }
 
 // Words of shared memory of place_block.
-__host__ __device__ constexpr int place_words(int E) { return (kWarps + 2) * E + 1 + kWarps; }
+__host__ __device__ constexpr int place_words(int warps, int E) { return (warps + 2) * E + 1 + warps; }
 
+template <int kWarps>
 __device__ __forceinline__ void place_in(const Args &a, const int32_t *experts, int32_t *words,
                                          int64_t from, int64_t to)
 {
     const int E = a.L.E;
-    place_block(a, experts, words, words + kWarps * E, words + (kWarps + 1) * E,
+    place_block<kWarps>(a, experts, words, words + kWarps * E, words + (kWarps + 1) * E,
                 words + (kWarps + 2) * E + 1, from, to);
 }
 
 // Experts and weights of a run of tokens, and the run's slots counted by expert; a single run
 // places them, too.
-template <int V>
-__global__ void __launch_bounds__(kWarps * 32, 1) choose_kernel(const Args a)
+template <int V, bool FEW>
+__global__ void __launch_bounds__(warps_of(V, FEW) * 32, 1) choose_kernel(const Args a)
 {
+    constexpr int kWarps = warps_of(V, FEW);
     extern __shared__ __align__(8) int32_t shared[];
     __shared__ int32_t chosen[kOneBlock * kRouteMaxChosen];
     const RouteLaunch &L = a.L;
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) choose_kernel(const Args a)
     const int64_t from = min(L.T, blockIdx.x * a.per), to = min(L.T, from + a.per);
     uint64_t *scratch = reinterpret_cast<uint64_t *>(shared) + warp * V * 32;
     float *held = reinterpret_cast<float *>(shared) + (kWarps * 2 + warp) * V * 32;
-    constexpr bool AHEAD = V <= 8;  // the next token's logits are read while this one is chosen for
+    constexpr bool AHEAD = V <= 4;  // the next token's logits are read while this one is chosen for
     float bias[V], z[V], next[V];
     auto read_bias = [&]() {
 #pragma unroll
@@ -522,7 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) choose_kernel(const Args a)
     }
     __syncthreads();
     if (a.runs == 1) {
-        place_in(a, chosen, shared, from * L.k, to * L.k);
+        place_in<kWarps>(a, chosen, shared, from * L.k, to * L.k);
         return;
     }
     for (int e = threadIdx.x; e < L.E; e += kWarps * 32)
@@ -536,12 +542,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) choose_kernel(const Args a)
         L.counts[(int64_t)blockIdx.x * L.E + e] = shared[e];
 }
 
-__global__ void __launch_bounds__(kWarps * 32) place_kernel(const Args a)
+constexpr int kPlaceWarps = 32;
+__global__ void __launch_bounds__(kPlaceWarps * 32) place_kernel(const Args a)
 {
     extern __shared__ int32_t shared[];
     const RouteLaunch &L = a.L;
     const int64_t from = min(L.T, blockIdx.x * a.per), to = min(L.T, from + a.per);
-    place_in(a, L.experts + from * L.k, shared, from * L.k, to * L.k);
+    place_in<kPlaceWarps>(a, L.experts + from * L.k, shared, from * L.k, to * L.k);
 }
 
 // dz from dw, a warp a token: with g_j = ds of the chosen (through the renormalisation where
@@ -711,21 +718,29 @@ __global__ void __launch_bounds__(128)
 
 static int runs_of(int64_t T) { return T <= kOneBlock ? 1 : (int)(T < kMaxRuns * 2 ? (T + 1) / 2 : kMaxRuns); }
 
-constexpr size_t place_bytes(int E) { return (size_t)place_words(E) * 4; }
+constexpr size_t place_bytes(int warps, int E) { return (size_t)place_words(warps, E) * 4; }
+
+template <int V, bool FEW>
+static cudaError_t launch_choose(const Args &a, cudaStream_t stream)
+{
+    constexpr int warps = warps_of(V, FEW);
+    constexpr size_t scratch = (size_t)warps * V * 32 * 12;  // the warps' keys and logits
+    constexpr size_t most = place_bytes(warps, V * 32);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        set_smem_limit_once(choose_kernel<V, FEW>, (int)(scratch > most ? scratch : most), done);
+    if (e != cudaSuccess)
+        return e;
+    const size_t place = place_bytes(warps, a.L.E), smem = place > scratch ? place : scratch;
+    choose_kernel<V, FEW><<<a.runs, warps * 32, smem, stream>>>(a);
+    return cudaGetLastError();
+}
 
 template <int V>
 static cudaError_t launch_choose(const Args &a, cudaStream_t stream)
 {
-    constexpr size_t exact = (size_t)kWarps * V * 32 * 12;  // the warps' scratch and logits
-    constexpr size_t most = place_bytes(V * 32);
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e =
-        set_smem_limit_once(choose_kernel<V>, (int)(exact > most ? exact : most), done);
-    if (e != cudaSuccess)
-        return e;
-    const size_t place = place_bytes(a.L.E), smem = place > exact ? place : exact;
-    choose_kernel<V><<<a.runs, kWarps * 32, smem, stream>>>(a);
-    return cudaGetLastError();
+    return a.L.T <= warps_of(V, true) ? launch_choose<V, true>(a, stream)
+                                      : launch_choose<V, false>(a, stream);
 }
 
 template <int V>
@@ -769,10 +784,10 @@ cudaError_t launch_route(const RouteLaunch &L, cudaStream_t stream)
     if (e != cudaSuccess || a.runs == 1)
         return e;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t f = set_smem_limit_once(place_kernel, (int)place_bytes(kRouteMaxExperts), done);
+    const cudaError_t f = set_smem_limit_once(place_kernel, (int)place_bytes(kPlaceWarps, kRouteMaxExperts), done);
     if (f != cudaSuccess)
         return f;
-    place_kernel<<<a.runs, kWarps * 32, place_bytes(L.E), stream>>>(a);
+    place_kernel<<<a.runs, kPlaceWarps * 32, place_bytes(kPlaceWarps, L.E), stream>>>(a);
     return cudaGetLastError();
 }
 
