@@ -13,6 +13,7 @@ from typing import Optional, Tuple
 
 import torch
 
+from . import binding as _binding
 from .binding import _call, _check, _empty, _need, load_library
 
 F8_BLOCK = 128  # values that share a scale
@@ -51,17 +52,31 @@ def _whole(name: str, v, low: int, high: int) -> int:
     return v
 
 
-def _codes(name: str, t, shape=None, dims: int = 2, device=None) -> int:
-    """Checks codes and returns the bytes between their rows."""
+def _codes(name: str, t, dims: int = 2, device: int = -1) -> int:
+    """Checks codes (on the device with that index) and returns the bytes between their rows."""
+    # One look at what a call that is in order passes (a decoded token's call takes little
+    # longer than its kernel); what fails it is looked at part by part for its message.
+    if type(t) is torch.Tensor and t.dtype is _F8 and t.dim() == dims and t.get_device() == device:
+        shape, strides = t.shape, t.stride()
+        cols, rows, ld = shape[-1], shape[-2], strides[-2]
+        if rows == 1 and dims == 2:
+            ld = (cols + 15) // 16 * 16
+        if (strides[-1] == 1 and ld % 16 == 0 and ld >= cols > 1 and rows > 0
+                and t.data_ptr() % 16 == 0
+                and (dims == 2 or (rows > 1 and strides[0] == rows * ld and shape[0] > 0))):
+            return ld
+    return _codes_in_detail(name, t, dims, device)
+
+
+def _codes_in_detail(name: str, t, dims: int, device: int) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != _F8:
         raise ValueError(f"{name} must be {_F8}, got {t.dtype}")
-    if t.dim() != dims or (shape is not None and t.shape != shape):
-        want = f"{dims}-D" if shape is None else " x ".join(map(str, shape))
-        raise ValueError(f"{name} must be a {want} tensor, got {' x '.join(map(str, t.shape))}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-D tensor, got {' x '.join(map(str, t.shape))}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     if t.numel() == 0:
         return (t.shape[-1] + 15) // 16 * 16
     rows, cols = t.shape[-2:]
@@ -77,8 +92,24 @@ def _codes(name: str, t, shape=None, dims: int = 2, device=None) -> int:
 
 def _new_codes(like: torch.Tensor, shape, stream: Stream) -> torch.Tensor:
     """Memory for codes whose rows are padded to 16 bytes, as a view of the shape."""
-    padded = (*shape[:-1], (shape[-1] + 15) // 16 * 16)
-    return _empty(like, padded, torch.uint8, stream).view(_F8)[..., :shape[-1]]
+    cols = shape[-1]
+    pitch = (cols + 15) // 16 * 16
+    held = _empty(like, (*shape[:-1], pitch), _F8, stream)
+    return held if pitch == cols else held.narrow(-1, 0, cols)
+
+
+def _index(t) -> int:
+    """The index of a tensor's CUDA device, -1 where it is none."""
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
+
+
+def _floats(name: str, t, shape, device: int) -> int:
+    """Checks contiguous fp32 values of a shape and returns their address."""
+    if (type(t) is torch.Tensor and t.dtype is torch.float32 and t.get_device() == device
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    _need(name, t, torch.float32, shape, torch.device("cuda", device))
+    return t.data_ptr()
 
 
 def _out(out, like: torch.Tensor, shape, stream: Stream, dtype=torch.float32) -> torch.Tensor:
@@ -100,7 +131,8 @@ def gemm_f8_quantize(X: torch.Tensor, kind: str = "rows", gather: Optional[torch
     name = _name(X.dtype)
     if kind not in ("rows", "columns", "both"):
         raise ValueError(f"kind must be rows, columns or both, got {kind!r}")
-    _whole("fan", fan, 1, 1 << 20)
+    if fan != 1 or fan is True:
+        _whole("fan", fan, 1, 1 << 20)
     M = source
     if gather is not None:
         M = _tensor("gather", gather, 1)[0]
@@ -113,19 +145,23 @@ def gemm_f8_quantize(X: torch.Tensor, kind: str = "rows", gather: Optional[torch
         if factors.numel() != source * fan:
             raise ValueError(f"factors must have {source * fan} values, got {factors.numel()}")
         _need("factors", factors, torch.float32, factors.shape, X.device)
-    got, pointers = [], []
-    for one, shape in (("rows", (M, _blocks(K))), ("columns", (_blocks(M), K))):
-        if kind in (one, "both"):
-            codes = _new_codes(X, (M, K), stream)
-            scales = _empty(X, shape, torch.float32, stream)
-            got += [codes, scales]
-            pointers += [codes.data_ptr(), scales.data_ptr()]
-        else:
-            pointers += [0, 0]
+    got, pointers = (), ()
+    if kind != "columns":
+        codes = _new_codes(X, (M, K), stream)
+        scales = _empty(X, (M, _blocks(K)), torch.float32, stream)
+        got, pointers = (codes, scales), (codes.data_ptr(), scales.data_ptr())
+    else:
+        pointers = (0, 0)
+    if kind != "rows":
+        codes = _new_codes(X, (M, K), stream)
+        scales = _empty(X, (_blocks(M), K), torch.float32, stream)
+        got, pointers = got + (codes, scales), pointers + (codes.data_ptr(), scales.data_ptr())
+    else:
+        pointers += (0, 0)
     _call(f"gemm_{name}_f8_quantize", X.get_device(), stream, M, K, X.data_ptr(), source,
           0 if gather is None else gather.data_ptr(), fan,
           0 if factors is None else factors.data_ptr(), *pointers)
-    return tuple(got)
+    return got
 
 
 def gemm_f8_quantize_tiles(W: torch.Tensor, stream: Stream = None
@@ -152,77 +188,80 @@ def gemm_f8_dequantize(codes: torch.Tensor, scales: torch.Tensor, kind: str = "r
     if kind not in F8_KINDS:
         raise ValueError(f"kind must be one of {tuple(F8_KINDS)}, got {kind!r}")
     dims = 3 if kind == "tiles" and isinstance(codes, torch.Tensor) and codes.dim() == 3 else 2
-    ld = _codes("codes", codes, dims=dims)
-    M, K = codes.shape[-2:]
-    held = {"rows": (M, _blocks(K)), "columns": (_blocks(M), K),
-            "tiles": (_blocks(M), _blocks(K))}[kind]
-    _need("scales", scales, torch.float32, (*codes.shape[:-2], *held), codes.device)
-    out = _out(out, codes, tuple(codes.shape), stream, dtype)
-    _call(f"gemm_{name}_f8_dequantize", codes.get_device(), stream,
-          codes.shape[0] if dims == 3 else 1, M, K, F8_KINDS[kind], codes.data_ptr(), ld,
-          scales.data_ptr(), out.data_ptr())
+    device = _index(codes)
+    ld = _codes("codes", codes, dims, device)
+    shape = codes.shape
+    M, K = shape[-2:]
+    held = ((M, _blocks(K)) if kind == "rows" else (_blocks(M), K) if kind == "columns"
+            else (*shape[:-2], _blocks(M), _blocks(K)))
+    scales_at = _floats("scales", scales, held, device)
+    out = _out(out, codes, shape, stream, dtype)
+    _call(f"gemm_{name}_f8_dequantize", device, stream, shape[0] if dims == 3 else 1, M, K,
+          F8_KINDS[kind], codes.data_ptr(), ld, scales_at, out.data_ptr())
     return out
 
 
-def _product(entry: str, names, A, a_scales, B, b_scales, offsets, out, stream: Stream):
+_FORWARD, _INPUT, _WEIGHT = "gemm_f8w8f32", "gemm_f8w8tf32", "gemm_f8tf8f32"
+
+
+def _product(entry: str, names, A, a_scales, B, b_scales, out, stream: Stream,
+             offsets=None, experts: bool = False):
     """Checks both operands of a product, names (A's, B's), and makes the call."""
-    experts = entry.endswith("_experts")
-    weight = entry.startswith("gemm_f8tf8f32")
-    lda = _codes(names[0], A)
-    device, batched = A.device, experts and not weight
-    ldb = _codes(names[1], B, dims=3 if batched else 2, device=device)
+    weight = entry is _WEIGHT
+    device = _index(A)
+    lda = _codes(names[0], A, 2, device)
+    ldb = _codes(names[1], B, 3 if experts and not weight else 2, device)
     rows, mid = A.shape
-    K, N = B.shape[-2:]
-    E = 1
+    shape = B.shape
+    K, N = shape[-2:]
+    head = ()
     if experts:
         count = _tensor("offsets", offsets, 1)[0]
-        _need("offsets", offsets, torch.int32, (count,), device)
-        E = B.shape[0] if batched else max(count - 1, 0)
+        _need("offsets", offsets, torch.int32, (count,), A.device)
+        E = count - 1 if weight else shape[0]
         if count != E + 1 or E < 1:
             raise ValueError(f"offsets must have an entry more than there are experts, got {count}")
+        head = (E, offsets.data_ptr())
     # sizes M (R), N, K as the C entry names them
     if weight:
-        if B.shape[0] != rows:
+        if shape[0] != rows:
             raise ValueError(f"{names[0]} and {names[1]} must have as many rows, got {rows} and "
-                             f"{B.shape[0]}")
+                             f"{shape[0]}")
         K = mid
-        shapes = (_blocks(rows), K), (_blocks(rows), N)
+        a_shape, b_shape = (_blocks(rows), K), (_blocks(rows), N)
         result = (E, K, N) if experts else (K, N)
     else:
-        forward = entry.startswith("gemm_f8w8f32")
-        inner = K if forward else N
-        if mid != inner:
+        if mid != (K if entry is _FORWARD else N):
             raise ValueError(f"{names[0]} is {rows} x {mid}, {names[1]} {K} x {N}: the sizes "
                              "summed over differ")
-        shapes = (rows, _blocks(mid)), (*B.shape[:-2], _blocks(K), _blocks(N))
-        result = (rows, N if forward else K)
-    _need(f"the scales of {names[0]}", a_scales, torch.float32, shapes[0], device)
-    _need(f"the scales of {names[1]}", b_scales, torch.float32, shapes[1], device)
+        a_shape, b_shape = (rows, _blocks(mid)), (*shape[:-2], _blocks(K), _blocks(N))
+        result = (rows, N if entry is _FORWARD else K)
+    a_at = _floats(f"{names[0]}'s scales", a_scales, a_shape, device)
+    b_at = _floats(f"{names[1]}'s scales", b_scales, b_shape, device)
     out = _out(out, A, result, stream)
-    head = (rows, N, K) + ((E, offsets.data_ptr()) if experts else ())
-    _call(entry, A.get_device(), stream, *head, A.data_ptr(), lda, a_scales.data_ptr(),
-          B.data_ptr(), ldb, b_scales.data_ptr(), out.data_ptr())
+    _call(f"{entry}_experts" if experts else entry, device, stream, rows, N, K, *head,
+          A.data_ptr(), lda, a_at, B.data_ptr(), ldb, b_at, out.data_ptr())
     return out
 
 
 def gemm_f8w8f32(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
                  out: Optional[torch.Tensor] = None, stream: Stream = None) -> torch.Tensor:
     """C = A @ W (fp32): A (M x K) as gemm_f8_quantize holds it by rows, W (K x N) by tiles."""
-    return _product("gemm_f8w8f32", ("A", "W"), A, a_scales, W, w_scales, None, out, stream)
+    return _product(_FORWARD, ("A", "W"), A, a_scales, W, w_scales, out, stream)
 
 
 def gemm_f8w8tf32(dY: torch.Tensor, y_scales: torch.Tensor, W: torch.Tensor,
                   w_scales: torch.Tensor, out: Optional[torch.Tensor] = None,
                   stream: Stream = None) -> torch.Tensor:
     """dX = dY @ W^T (fp32), the input's gradient: dY (M x N) by rows, W (K x N) by tiles."""
-    return _product("gemm_f8w8tf32", ("dY", "W"), dY, y_scales, W, w_scales, None, out, stream)
+    return _product(_INPUT, ("dY", "W"), dY, y_scales, W, w_scales, out, stream)
 
 
 def gemm_f8tf8f32(X: torch.Tensor, x_scales: torch.Tensor, dY: torch.Tensor,
                   y_scales: torch.Tensor, out: Optional[torch.Tensor] = None,
                   stream: Stream = None) -> torch.Tensor:
     """dW = X^T @ dY (K x N, fp32), the weight's gradient: X (M x K) and dY (M x N) by columns."""
-    return _product("gemm_f8tf8f32", ("X", "dY"), X, x_scales, dY, y_scales, None, out, stream)
+    return _product(_WEIGHT, ("X", "dY"), X, x_scales, dY, y_scales, out, stream)
 
 
 def gemm_f8w8f32_experts(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor,
@@ -230,8 +269,8 @@ def gemm_f8w8f32_experts(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tenso
                          out: Optional[torch.Tensor] = None, stream: Stream = None) -> torch.Tensor:
     """gemm_f8w8f32 of each expert: rows offsets[e] .. offsets[e + 1] - 1 of A (R x K) times W[e]
     (W: E x K x N). Rows of the result in no expert's part are left as they were."""
-    return _product("gemm_f8w8f32_experts", ("A", "W"), A, a_scales, W, w_scales, offsets, out,
-                    stream)
+    return _product(_FORWARD, ("A", "W"), A, a_scales, W, w_scales, out, stream,
+                    offsets, True)
 
 
 def gemm_f8w8tf32_experts(dY: torch.Tensor, y_scales: torch.Tensor, W: torch.Tensor,
@@ -239,8 +278,8 @@ def gemm_f8w8tf32_experts(dY: torch.Tensor, y_scales: torch.Tensor, W: torch.Ten
                           out: Optional[torch.Tensor] = None, stream: Stream = None
                           ) -> torch.Tensor:
     """gemm_f8w8tf32 of each expert: its rows of dY (R x N) times W[e]^T."""
-    return _product("gemm_f8w8tf32_experts", ("dY", "W"), dY, y_scales, W, w_scales, offsets, out,
-                    stream)
+    return _product(_INPUT, ("dY", "W"), dY, y_scales, W, w_scales, out, stream,
+                    offsets, True)
 
 
 def gemm_f8tf8f32_experts(X: torch.Tensor, x_scales: torch.Tensor, dY: torch.Tensor,
@@ -249,20 +288,22 @@ def gemm_f8tf8f32_experts(X: torch.Tensor, x_scales: torch.Tensor, dY: torch.Ten
                           ) -> torch.Tensor:
     """gemm_f8tf8f32 of each expert (E x K x N, fp32) over its rows of X (R x K) and dY (R x N);
     zeros for an expert without rows. The offsets are multiples of 128 (gemm_route's align)."""
-    return _product("gemm_f8tf8f32_experts", ("X", "dY"), X, x_scales, dY, y_scales, offsets, out,
-                    stream)
+    return _product(_WEIGHT, ("X", "dY"), X, x_scales, dY, y_scales, out, stream,
+                    offsets, True)
 
 
 def gemm_f8w8f32_selftest_timeout(A, a_scales, W, w_scales, out: torch.Tensor,
                                   wait_limit_ns: int) -> None:
     """Launch gemm_f8w8f32's kernel with its loads muted so every bounded wait runs out."""
-    lda, ldw = _codes("A", A), _codes("W", W)
+    device = _index(A)
+    lda, ldw = _codes("A", A, 2, device), _codes("W", W, 2, device)
     M, K = A.shape
     N = W.shape[1]
+    a_at = _floats("A's scales", a_scales, (M, _blocks(K)), device)
+    w_at = _floats("W's scales", w_scales, (_blocks(K), _blocks(N)), device)
     _need("out", out, torch.float32, (M, N), A.device)
-    _call("gemm_f8w8f32_selftest_timeout", A.get_device(), None, M, N, K, A.data_ptr(), lda,
-          a_scales.data_ptr(), W.data_ptr(), ldw, w_scales.data_ptr(), out.data_ptr(),
-          int(wait_limit_ns))
+    _call("gemm_f8w8f32_selftest_timeout", device, None, M, N, K, A.data_ptr(), lda, a_at,
+          W.data_ptr(), ldw, w_at, out.data_ptr(), int(wait_limit_ns))
 
 
 # ---------------------------------------------------------------- routing and joining
@@ -295,16 +336,17 @@ def gemm_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None
     makes the shortest order."""
     T, E = _tensor("logits", logits, 2)
     name = _name(logits.dtype)
-    _whole("k", k, 1, 32)
-    _whole("groups", groups, 1, 32)
-    _whole("top_groups", top_groups, 1, 32)
-    _whole("align", align, 1, 1024)
+    for what, v, most in (("k", k, 32), ("groups", groups, 32), ("top_groups", top_groups, 32),
+                          ("align", align, 1024)):
+        if type(v) is not int or not 1 <= v <= most:
+            _whole(what, v, 1, most)
     sigmoid = _score(score)
     if bias is not None:
         _need("bias", bias, torch.float32, (E,), logits.device)
-    R = gemm_route_rows(T, E, k, align)
-    need = int(load_library().gemm_route_workspace_bytes(T, E))
-    experts, slots = (_empty(logits, (T, k), torch.int32, stream) for _ in range(2))
+    R = T * k + min(E, T * k) * (align - 1)  # gemm_route_rows
+    need = int((_binding._lib or load_library()).gemm_route_workspace_bytes(T, E))
+    experts = _empty(logits, (T, k), torch.int32, stream)
+    slots = _empty(logits, (T, k), torch.int32, stream)
     weights = _empty(logits, (T, k), torch.float32, stream)
     rows = _empty(logits, (R,), torch.int32, stream)
     offsets = _empty(logits, (E + 1,), torch.int32, stream)
