@@ -50,15 +50,40 @@ __device__ __forceinline__ uint32_t codes2(float a, float b)
     return r;
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv, bool nil)
+// Two products at a time; + 0 makes a -0 a 0, so that the bytes past a row's end are 0.
+__device__ __forceinline__ void mul2(float &v0, float &v1, float s0, float s1)
 {
-    if (nil)
-        return make_uint2(0u, 0u);
-    return make_uint2(codes2(v[0] * inv, v[1] * inv) | codes2(v[2] * inv, v[3] * inv) << 16,
-                      codes2(v[4] * inv, v[5] * inv) | codes2(v[6] * inv, v[7] * inv) << 16);
+    asm("{\n\t.reg .b64 v, s, z;\n\t"
+        "mov.b64 v, {%0, %1};\n\t"
+        "mov.b64 s, {%2, %3};\n\t"
+        "mov.b64 z, {%4, %4};\n\t"
+        "fma.rn.f32x2 v, v, s, z;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}\n"
+        : "+f"(v0), "+f"(v1)
+        : "f"(s0), "f"(s1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint2 codes8(const float (&v)[8])
+{
+    return make_uint2(codes2(v[0], v[1]) | codes2(v[2], v[3]) << 16,
+                      codes2(v[4], v[5]) | codes2(v[6], v[7]) << 16);
+}
+
+__device__ __forceinline__ uint2 codes8(float (&v)[8], float inv, bool nil)
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+        mul2(v[j], v[j + 1], inv, inv);
+    return nil ? make_uint2(0u, 0u) : codes8(v);
+}
+
+// The larger of a and |b|; NaN where one is.
+__device__ __forceinline__ float max_magnitude(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+    return d;
+}
 
 template <int TYPE>
 __device__ __forceinline__ float load1(const void *X, int64_t i)
@@ -203,51 +228,57 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
         raw[i].values(v);
         if constexpr (FACTORS) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = fmaf(v[j], factor[i], 0.f);  // one rounding; no -0 past the row's end
-        }
-    };
-    // Magnitudes of row i: fp32 bits, or two 16-bit ones a word.
-    auto magnitudes = [&](int i, uint32_t (&m)[TOPS]) {
-        if constexpr (HALVES) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                m[j] = raw[i].w[j] & 0x7fff7fffu;
-        } else {
-            float v[8];
-            values(i, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m[j] = __float_as_uint(v[j]) & 0x7fffffffu;
+            for (int j = 0; j < 8; j += 2)
+                mul2(v[j], v[j + 1], factor[i], factor[i]);
         }
     };
     auto larger = [](uint32_t a, uint32_t b) { return HALVES ? max2(a, b) : max(a, b); };
 
-    uint32_t tops[DOWN ? TOPS : 1];
-    if constexpr (DOWN) {
+    // A row's largest magnitude is that of X's row times the factor's: rounding keeps order.
+    // A column's is found among the products.
+    uint32_t tops[DOWN ? TOPS : 1];  // of the columns: fp32 bits, or two 16-bit ones a word
+    float column[DOWN && !HALVES ? 8 : 1];
 #pragma unroll
-        for (int j = 0; j < TOPS; ++j)
-            tops[j] = 0;
-    }
+    for (int j = 0; j < (DOWN ? TOPS : 0); ++j)
+        tops[j] = 0;
+#pragma unroll
+    for (int j = 0; j < (DOWN && !HALVES ? 8 : 0); ++j)
+        column[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        uint32_t m[TOPS];
-        magnitudes(i, m);
-        if constexpr (DOWN) {
+        if constexpr (DOWN && HALVES) {
 #pragma unroll
-            for (int j = 0; j < TOPS; ++j)
-                tops[j] = larger(tops[j], m[j]);
+            for (int j = 0; j < 4; ++j)
+                tops[j] = max2(tops[j], raw[i].w[j] & 0x7fff7fffu);
+        } else if constexpr (DOWN) {
+            float v[8];
+            values(i, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                column[j] = max_magnitude(column[j], v[j]);
         }
         if constexpr (KIND & kRows) {
-            uint32_t top = m[0];
+            uint32_t top;
+            if constexpr (TYPE != kF32) {
+                top = raw[i].w[0] & 0x7fff7fffu;
 #pragma unroll
-            for (int j = 1; j < TOPS; ++j)
-                top = larger(top, m[j]);
+                for (int j = 1; j < 4; ++j)
+                    top = max2(top, raw[i].w[j] & 0x7fff7fffu);
 #pragma unroll
-            for (int o = 1; o < 16; o *= 2)
-                top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if constexpr (HALVES)
+                for (int o = 1; o < 16; o *= 2)
+                    top = max2(top, __shfl_xor_sync(0xffffffffu, top, o));
                 top = widen<TYPE>(max(top & 0xffffu, top >> 16));
+            } else {
+                top = raw[i].w[0] & 0x7fffffffu;
+#pragma unroll
+                for (int j = 1; j < 8; ++j)
+                    top = max(top, raw[i].w[j] & 0x7fffffffu);
+#pragma unroll
+                for (int o = 1; o < 16; o *= 2)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            if constexpr (FACTORS)
+                top = __float_as_uint(__uint_as_float(top) * factor[i]) & 0x7fffffffu;
             const Scale s = scale_of(top);
             const int64_t r = r0 + 16 * i;
             if (r < p.M) {
@@ -259,6 +290,11 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
                     p.row_scales[r * p.col_blocks + cb] = s.s;
             }
         }
+    }
+    if constexpr (DOWN && !HALVES) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            tops[j] = __float_as_uint(column[j]);
     }
 
     if constexpr (DOWN) {
@@ -316,9 +352,9 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
                 float v[8];
                 values(i, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] *= inv[j];
-                const uint2 q = codes8(v, 1.f, false);
+                for (int j = 0; j < 8; j += 2)
+                    mul2(v[j], v[j + 1], inv[j], inv[j + 1]);
+                const uint2 q = codes8(v);
                 if (r < p.M && c0 < pitch)
                     *reinterpret_cast<uint2 *>(p.col_codes + r * pitch + c0) =
                         make_uint2(q.x & keep[0], q.y & keep[1]);

@@ -67,10 +67,10 @@ struct Cfg {
     static constexpr int ROWS = SWAP ? NT : TILE_LANES;  // of C in a tile
     static constexpr int COLS = SWAP ? TILE_LANES : NT;
     static constexpr int BN = PAIR ? NT / 2 : NT;  // columns staged by a CTA
-    static constexpr int PW = PAIR ? 2 : 1;        // promoting warpgroups
+    static constexpr int PW = SWAP ? 1 : 2;        // promoting warpgroups
     static constexpr int THREADS = 128 * (1 + PW);
     // Registers a thread of a pair's warpgroups after the split of 3 x 168.
-    static constexpr int R_ISSUE = 56, R_PROMOTE = 224;
+    static constexpr int R_ISSUE = 48, R_PROMOTE = 224;
     static constexpr int CPT = NT / PW;  // columns of a promoting thread
     static constexpr int CH = CPT < 32 ? CPT : 32;  // read from tensor memory at once
     static constexpr int SETS = PAIR ? 2 : 4;
@@ -80,6 +80,7 @@ struct Cfg {
     // Floats of a slot: the lanes' scales or none, the columns' or none, the tiles'.
     static constexpr int SCALE_COLUMNS = SWAP ? 0 : LANES, SCALE_TILE = SCALE_COLUMNS + NT;
     static constexpr int SCALE_PITCH = SCALE_TILE + 4;
+    static_assert(!PAIR || (SCALE_SLOTS >= 2 * 4 * PW && NT >= 256), "room for 16 x 16 values a slot");
     static_assert(SCALE_AHEAD + 2 * SETS + 2 <= SCALE_SLOTS, "scales are read before their slot is written");
     static constexpr int STAGES = NT >= 128 ? 6 : NT == 64 ? 8 : 10;
     static constexpr int PITCH = NT + 4;  // floats per lane of a partial tile
@@ -114,7 +115,7 @@ struct Params {
     unsigned long long limit_ns;
     int splits;
     int mute;
-    int c_vec;  // rows of C on 32-byte boundaries
+    int c_vec;  // rows of C on 8-byte boundaries
 };
 
 // kind::f8f6f4, D fp32, both operands e4m3, M = 128 (256 for a pair), N = NT.
@@ -178,6 +179,11 @@ __device__ __forceinline__ float2 lds_f32x2(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b)
 {
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
@@ -202,25 +208,26 @@ struct Tile {
 template <int MODE, int NT, bool SWAP>
 struct Schedule {
     using Cf = Cfg<NT, SWAP>;
-    const int32_t *start;  // groups + 1 row offsets
-    const int32_t *tiles;  // groups + 1 running counts
+    uint32_t start;  // shared memory: groups + 1 row offsets, and as many running tile counts
     const Params *p;
 
-    __device__ __forceinline__ int total() const { return tiles[p->groups]; }
+    static constexpr uint32_t TILES = (kMaxGroups + 4) * 4;
+    __device__ __forceinline__ int total() const { return (int)lds32(start + TILES + p->groups * 4); }
 
     __device__ __forceinline__ Tile at(int t) const
     {
         int lo = 0, hi = p->groups - 1;  // the last group with tiles[g] <= t
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (tiles[mid] <= t)
+            if ((int)lds32(start + TILES + mid * 4) <= t)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         Tile x;
         x.group = lo;
-        const int begin = start[lo], end = start[lo + 1], local = t - tiles[lo];
+        const int begin = (int)lds32(start + lo * 4), end = (int)lds32(start + lo * 4 + 4);
+        const int local = t - (int)lds32(start + TILES + lo * 4);
         const int first = MODE == kF8Weight ? 0 : begin;
         x.row_end = MODE == kF8Weight ? p->rows : end;
         x.d0 = MODE == kF8Weight ? begin : 0;
@@ -296,7 +303,10 @@ __device__ __forceinline__ void count_tiles(const Params &p, int32_t *start, int
     }
 }
 
-template <int MODE, int NT, bool SWAP>
+// EIGHTS: rows of C start on 32 bytes and are whole eights (asked of a pair's forward and input
+// products: the two ways to store a tile in one kernel spill registers into its loop, 557 us
+// instead of 420 for 8192^3).
+template <int MODE, int NT, bool SWAP, bool EIGHTS>
 __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
     f8_tc_kernel(const __grid_constant__ CUtensorMap tm_lanes,
                  const __grid_constant__ CUtensorMap tm_cols, const Params p)
@@ -309,12 +319,13 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
     constexpr bool COLS_MN = SWAP ? false : MODE != kF8Input;
     constexpr bool COLUMN_SCALES = SWAP || MODE == kF8Weight;
     // Read from tensor memory as matrix fragments: a thread then has 4 lanes of a quarter of the
-    // columns, and half as many of the columns' scales to load.
-    constexpr bool FRAGMENTS = MODE == kF8Weight;
+    // columns, so a warp stores 32 bytes of each of eight rows of C at a time whatever their
+    // alignment, and a weight gradient's thread loads half as many of the columns' scales (8192^3
+    // 498 us, a lane a thread 550). On pairs a lane a thread is the faster form of the others:
+    // one scale a thread, and shared memory is what they wait for (420 us, fragments 480).
+    constexpr bool FRAGMENTS = !SWAP && (MODE == kF8Weight || !PAIR);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
-    int32_t *start = reinterpret_cast<int32_t *>(smem + Cf::OFF_GROUPS);
-    int32_t *tile_count = start + kMaxGroups + 4;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::OFF_BARS);
     uint64_t *empty = full + Cf::STAGES;
     uint64_t *tfull = empty + Cf::STAGES;
@@ -360,15 +371,17 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
             tmem_relinquish();
         }
     }
-    if (warp == 2)
-        count_tiles<MODE, NT, SWAP>(p, start, tile_count, lane);
+    if (warp == 2) {
+        int32_t *start = reinterpret_cast<int32_t *>(smem + Cf::OFF_GROUPS);
+        count_tiles<MODE, NT, SWAP>(p, start, start + kMaxGroups + 4, lane);
+    }
     tc_fence_before();
     __syncthreads();
     if constexpr (PAIR)
         cluster_sync();  // the peer's barriers are initialised before any remote signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const Schedule<MODE, NT, SWAP> plan{start, tile_count, &p};
+    const Schedule<MODE, NT, SWAP> plan{smem_u32(smem + Cf::OFF_GROUPS), &p};
     const int tiles = plan.total();
 
     if (wg == 0) {
@@ -531,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         columns[j] += MODE == kF8Weight ? p.cols : 1;
                     }
                     if constexpr (MODE != kF8Weight) {
-                        if (lane == 0 && warp - 2 < Cf::PW)
+                        if (lane == 0 && (PAIR || warp == 2))
                             cp_async_4_full(slot + (Cf::SCALE_TILE + warp - 2) * 4, tile);
                         tile += tile_step;
                     }
@@ -567,8 +580,8 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
             regs_inc<Cf::R_PROMOTE>();
         const int pw = wg - 1, quarter = warp & 3;
         const int row = quarter * 32 + lane;  // TMEM lane
-        const uint32_t ring = smem_u32(smem + Cf::OFF_SCALE);
-        uint32_t slot = 0;
+        constexpr uint32_t SLOT_BYTES = Cf::SCALE_PITCH * 4;
+        uint32_t scales = smem_u32(smem + Cf::OFF_SCALE), slot = 0;
         const uint32_t tfull_at = smem_u32(tfull);
         const uint32_t tempty_at = PAIR ? mapa_shared(smem_u32(tempty), leader) : smem_u32(tempty);
         Place<Cf::SETS> set;
@@ -576,74 +589,83 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
         bool seen = false;  // what the look ahead said
 #pragma unroll 1
         for (int t = unit; t < tiles; t += units) {
-            const Tile x = plan.at(t);
-            const Blocks b = blocks_of(x, S, rank);
-            const int lane0 = (SWAP ? x.c0 : x.r0) + half;
-            const int col0 = (SWAP ? x.r0 : x.c0) + pw * Cf::CPT;
+            const int blocks = blocks_of(plan.at(t), S, rank).count;
 #pragma unroll
             for (int j = 0; j < Cf::CPT; ++j)
                 acc[j] = 0.f;
 #pragma unroll 1
-            for (int i = 0; i < b.count; ++i) {
-                if (!seen)
+            for (int i = 0; i < blocks; ++i) {
+                if (FRAGMENTS || !seen)
                     wait_on(tfull_at + set.at * 8, set.phase, p.limit_ns, p.err, abort);
                 __syncwarp();  // the lanes left the wait each for itself; the load is the warp's
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + set.at * NT +
                                        (uint32_t)(pw * Cf::CPT);
-                const uint32_t scales = ring + slot * (Cf::SCALE_PITCH * 4);
-                slot = (slot + 1) % SCALE_SLOTS;
                 Place<Cf::SETS> next = set;
                 next.advance();
-                float ls = 1.f;
                 if constexpr (FRAGMENTS) {
-                    // acc: 64 columns c, lanes of half q, 8 columns k, lane t / 4 (+ 8).
-                    float rs[4];
+                    // acc: 32 columns c, lanes of half q, 8 columns k, lane t / 4 (+ 8 e).
+                    constexpr int C32 = Cf::CPT / 32;
+                    const uint32_t row_scales = scales + (quarter * 32 + (lane >> 2)) * 4;
+                    float2 cs[COLUMN_SCALES ? 4 : 1];
+                    float rs[2];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        rs[q] = lds_f32(scales + (quarter * 32 + q * 8 + (lane >> 2)) * 4);
-                    seen = peek(tfull_at + next.at * 8, next.phase);
+                    for (int n = 0; n < 2 * C32; ++n) {
+                        // A weight gradient keeps the columns' scales over both halves of the
+                        // lanes, the others the lanes' over the columns.
+                        const int c = COLUMN_SCALES ? n / 2 : n % C32, q = COLUMN_SCALES ? n % 2 : n / C32;
+                        uint32_t v[16];
+                        tmem_ld_16x256b_x4(taddr + ((uint32_t)(q * 16) << 16) + c * 32, v);
+                        if constexpr (COLUMN_SCALES) {
+                            if (q == 0)
 #pragma unroll
-                    for (int c = 0; c < Cf::CPT; c += 64) {
-                        float2 cs[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            cs[k] = lds_f32x2(scales + (Cf::SCALE_COLUMNS + pw * Cf::CPT + c + 8 * k +
-                                                        2 * (lane & 3)) * 4);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t v[32];
-                            tmem_ld_16x256b_x8(taddr + ((uint32_t)(q * 16) << 16) + c, v);
-                            tmem_arrived<32>(v);
-                            if (c + 64 == Cf::CPT && q == 1) {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0)
-                                    arrive_set<PAIR>(tempty_at + set.at * 8);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    float f0 = __uint_as_float(v[4 * k + 2 * e]);
-                                    float f1 = __uint_as_float(v[4 * k + 2 * e + 1]);
-                                    mul2(f0, f1, rs[2 * q + e]);
-                                    float *t = acc + ((c / 64 * 2 + q) * 8 + k) * 4 + 2 * e;
-                                    fma2_each(t[0], t[1], f0, f1, cs[k].x, cs[k].y);
-                                }
+                                for (int k = 0; k < 4; ++k)
+                                    cs[k] = lds_f32x2(scales + (Cf::SCALE_COLUMNS + pw * Cf::CPT + c * 32 +
+                                                                8 * k + 2 * (lane & 3)) * 4);
                         }
+                        if (COLUMN_SCALES || c == 0) {
+                            rs[0] = lds_f32(row_scales + q * 64);
+                            rs[1] = lds_f32(row_scales + q * 64 + 32);
+                            if constexpr (!COLUMN_SCALES) {
+                                const float tile = lds_f32(scales + (Cf::SCALE_TILE + (PAIR ? pw : 0)) * 4);
+                                rs[0] *= tile;
+                                rs[1] *= tile;
+                            }
+                        }
+                        tmem_arrived<16>(v);
+                        if (n == 2 * C32 - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                arrive_set<PAIR>(tempty_at + set.at * 8);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float f0 = __uint_as_float(v[4 * k + 2 * e]);
+                                float f1 = __uint_as_float(v[4 * k + 2 * e + 1]);
+                                float *t = acc + ((c * 2 + q) * 4 + k) * 4 + 2 * e;
+                                if constexpr (COLUMN_SCALES) {
+                                    mul2(f0, f1, rs[e]);
+                                    fma2_each(t[0], t[1], f0, f1, cs[k].x, cs[k].y);
+                                } else {
+                                    fma2(t[0], t[1], rs[e], f0, f1);
+                                }
+                            }
                     }
                 } else {
                     constexpr int CH = Cf::CH;
+                    float ls = 0.f;  // the tile's scale, and the lane's
 #pragma unroll
                     for (int c = 0; c < Cf::CPT; c += CH) {
                         uint32_t v[CH];
                         tmem_load<CH>(taddr + c, v);
                         if (c == 0) {  // while the first load is under way
                             seen = peek(tfull_at + next.at * 8, next.phase);
+                            ls = lds_f32(scales + (Cf::SCALE_TILE + pw) * 4);
                             if constexpr (!SWAP)
-                                ls = lds_f32(scales + row * 4);
-                            ls *= lds_f32(scales + (Cf::SCALE_TILE + pw) * 4);
+                                ls *= lds_f32(scales + row * 4);
                         }
                         tmem_arrived<CH>(v);
                         if (c + CH == Cf::CPT) {
@@ -660,7 +682,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                                 f[e] = __uint_as_float(v[j + e]);
                             float *a = acc + c + j;
                             if constexpr (SWAP) {
-                                const uint4 s = lds128(scales + (Cf::SCALE_COLUMNS + pw * Cf::CPT + c + j) * 4);
+                                const uint4 s = lds128(scales + (Cf::SCALE_COLUMNS + c + j) * 4);
                                 mul2(f[0], f[1], ls);
                                 mul2(f[2], f[3], ls);
                                 fma2_each(a[0], a[1], f[0], f[1], __uint_as_float(s.x), __uint_as_float(s.y));
@@ -673,13 +695,21 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                     }
                 }
                 set = next;
+                scales += SLOT_BYTES;
+                if (++slot == SCALE_SLOTS) {
+                    slot = 0;
+                    scales -= SCALE_SLOTS * SLOT_BYTES;
+                }
             }
+            const Tile x = plan.at(t);  // looked up again: its registers are the sums' meanwhile
+            const int lane0 = (SWAP ? x.c0 : x.r0) + half;
+            const int col0 = (SWAP ? x.r0 : x.c0) + pw * Cf::CPT;
             // Of fragments: f(lane of the tile's half, column, the two values from it).
             auto each_fragment = [&](auto f) {
 #pragma unroll
-                for (int i = 0; i < Cf::CPT / 2; ++i)  // c / 64, q, k, e as above
-                    f(quarter * 32 + (i / 16 % 2) * 16 + (i % 2) * 8 + (lane >> 2),
-                      pw * Cf::CPT + (i / 32) * 64 + (i / 2 % 8) * 8 + 2 * (lane & 3), acc + 2 * i);
+                for (int i = 0; i < Cf::CPT / 2; ++i)  // c, q, k, e as above
+                    f(quarter * 32 + (i / 8 % 2) * 16 + (i % 2) * 8 + (lane >> 2),
+                      pw * Cf::CPT + (i / 16) * 32 + (i / 2 % 4) * 8 + 2 * (lane & 3), acc + 2 * i);
             };
             if (S > 1) {
                 if constexpr (FRAGMENTS) {
@@ -723,53 +753,81 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         if (j < n)
                             *c = acc[j];
                 }
-            } else if (gl < x.row_end) {
-                float *c = C + (int64_t)gl * p.cols + col0;
-                const int n = p.cols - col0;
+            } else if constexpr (EIGHTS) {
+                if (gl < x.row_end) {
+                    float *c = C + (int64_t)gl * p.cols + col0;
 #pragma unroll
-                for (int j = 0; j < Cf::CPT; j += 8) {
-                    if (p.c_vec && j + 7 < n) {
-                        store8(c + j, acc + j);
-                    } else {
+                    for (int j = 0; j < Cf::CPT; j += 8)
+                        if (col0 + j < p.cols)
+                            store8(c + j, acc + j);
+                }
+            } else {
+                // 16 columns at a time through shared memory (the ring's columns, which this mode
+                // leaves, two slots a warp, 16 rows in each), so that a warp stores 64 bytes of
+                // two rows: 8192 x 8191 x 8192 takes 687 us where each lane stores its own row.
+                const uint32_t mine = smem_u32(smem + Cf::OFF_SCALE) + Cf::SCALE_COLUMNS * 4 +
+                                      (uint32_t)(2 * (pw * 4 + quarter)) * SLOT_BYTES;
+                const int r16 = lane & 15, hi = lane >> 4;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (j + e < n)
-                                c[j + e] = acc[j + e];
+                for (int j = 0; j < Cf::CPT; j += 16) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        sts_f32(mine + hi * SLOT_BYTES + (uint32_t)(r16 * 16 + (e ^ r16)) * 4, acc[j + e]);
+                    __syncwarp();
+                    const int gc = col0 + j + r16;
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) {
+                        const int l = 2 * i + hi, r = l & 15;
+                        const float v = lds_f32(mine + (l >> 4) * SLOT_BYTES + (uint32_t)(r * 16 + (r16 ^ r)) * 4);
+                        const int gr = lane0 + quarter * 32 + l;
+                        if (gr < x.row_end && gc < p.cols)
+                            C[(int64_t)gr * p.cols + gc] = v;
                     }
+                    __syncwarp();
                 }
             }
         }
     }
     __syncwarp();  // the barriers below are the whole warp's
 
+    // Read again rather than held through the roles, whose registers are the sums'.
+    const int tid = (int)special_tid_x();
     if (S > 1) {
         cluster_sync();  // every partial tile of the cluster is in shared memory
-        if (wg > 0 && unit < tiles) {
+        const uint32_t cta = cluster_ctarank();
+        const int rank = cta / CTAS, half = cta % CTAS == 0 ? 0 : LANES;
+        if (tid >= 128 && unit < plan.total()) {
             const Tile x = plan.at(unit);
-            const int row = threadIdx.x & 127, pw = wg - 1;
+            // Neighbouring threads take neighbours in a row of C: columns of the tile, or lanes.
             const int cols = NT / S, first = rank * cols;
-            const int gl = (SWAP ? x.c0 : x.r0) + half + row, col0 = SWAP ? x.r0 : x.c0;
-            const uint32_t mine = smem_u32(smem) + (uint32_t)(row * Cf::PITCH) * 4u;
+            const int lane0 = (SWAP ? x.c0 : x.r0) + half, col0 = SWAP ? x.r0 : x.c0;
             float *C = p.C + (MODE == kF8Weight ? (int64_t)x.group * p.rows * p.cols : 0);
-            for (int cc = pw * 2; cc < cols; cc += 2 * Cf::PW) {
-                const uint32_t off = (uint32_t)(first + cc) * 4u;
-                float2 sum = ld_shared_cluster_v2(mapa_shared(mine + off, cta % CTAS));
+            for (int i = tid - 128; i < LANES * cols / 2; i += 128 * Cf::PW) {
+                const int l = SWAP ? i % LANES : i / (cols / 2);
+                const int cc = first + 2 * (SWAP ? i / LANES : i % (cols / 2));
+                const uint32_t at = smem_u32(smem) + (uint32_t)(l * Cf::PITCH + cc) * 4u;
+                float2 sum = ld_shared_cluster_v2(mapa_shared(at, cta % CTAS));
                 for (int q = 1; q < S; ++q) {
-                    const float2 v = ld_shared_cluster_v2(
-                        mapa_shared(mine + off, (uint32_t)q * CTAS + cta % CTAS));
+                    const float2 v =
+                        ld_shared_cluster_v2(mapa_shared(at, (uint32_t)q * CTAS + cta % CTAS));
                     sum.x += v.x;
                     sum.y += v.y;
                 }
-                const float a[2] = {sum.x, sum.y};
-                const int gc = col0 + first + cc;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if constexpr (SWAP) {
-                        if (gl < p.cols && gc + e < x.row_end)
-                            C[(int64_t)(gc + e) * p.cols + gl] = a[e];
+                const int gl = lane0 + l, gc = col0 + cc;
+                if constexpr (SWAP) {
+                    if (gl < p.cols && gc < x.row_end)
+                        C[(int64_t)gc * p.cols + gl] = sum.x;
+                    if (gl < p.cols && gc + 1 < x.row_end)
+                        C[(int64_t)(gc + 1) * p.cols + gl] = sum.y;
+                } else if (gl < x.row_end) {
+                    float *c = C + (int64_t)gl * p.cols + gc;
+                    if (p.c_vec && gc + 1 < p.cols) {
+                        *reinterpret_cast<float2 *>(c) = sum;
                     } else {
-                        if (gl < x.row_end && gc + e < p.cols)
-                            C[(int64_t)gl * p.cols + gc + e] = a[e];
+                        if (gc < p.cols)
+                            c[0] = sum.x;
+                        if (gc + 1 < p.cols)
+                            c[1] = sum.y;
                     }
                 }
             }
@@ -782,7 +840,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
     // No copy into this CTA's shared memory may outlive it. The MMAs waited for every
     // stage's bytes, unless a role gave up: then copies that nobody waited for get
     // the time of a wait to land. (A pair's CTAs leave together, below.)
-    if (threadIdx.x == 0 && *abort) {
+    if (tid == 0 && *abort) {
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < p.limit_ns) {
         }
@@ -790,7 +848,8 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
     __syncwarp();
     if constexpr (PAIR)
         cluster_sync();  // no CTA leaves while its peer may still signal or read it
-    if (warp == 1) {
+    if (tid >> 5 == 1) {
+        const uint32_t tmem_base = lds32(smem_u32(tmem_slot));
         tc_fence_after();
         if constexpr (PAIR)
             tmem_dealloc_pair(tmem_base, Cf::TMEM_COLS);
@@ -828,7 +887,7 @@ static int64_t most_tiles(const F8Launch &L, int rows, int cols)
     return (L.rows / rows + (L.experts < L.rows ? L.experts : L.rows)) * tc;
 }
 
-template <int MODE, int NT, bool SWAP>
+template <int MODE, int NT, bool SWAP, bool EIGHTS = false>
 static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mute, cudaStream_t stream)
 {
     using Cf = Cfg<NT, SWAP>;
@@ -851,7 +910,7 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
     }
     if (!ok)
         return cudaErrorInvalidValue;
-    auto kernel = f8_tc_kernel<MODE, NT, SWAP>;
+    auto kernel = f8_tc_kernel<MODE, NT, SWAP, EIGHTS>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = set_smem_limit_once(kernel, (int)Cf::SMEM_BYTES, done);
     if (e != cudaSuccess)
@@ -872,7 +931,7 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
     p.err = d.err;
     p.limit_ns = d.wait_limit_ns;
     p.mute = mute ? 1 : 0;
-    p.c_vec = L.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 31) == 0;
+    p.c_vec = L.cols % 2 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 7) == 0;
     // Few tiles: split the depth while every CTA keeps at least two blocks (a pair four) and
     // all clusters (of at most 8 CTAs) are resident at once.
     constexpr int CTAS = Cf::CTAS, LEAST = Cf::PAIR ? 4 : 2;
@@ -923,8 +982,13 @@ static cudaError_t launch_mode(const F8Launch &L, const DeviceContext &d, bool m
         if (rows <= 128)
             return launch_cfg<MODE, 128, true>(L, d, mute, stream);
     }
-    if (most_tiles(L, 256, 256) * 4 >= d.sms)
+    if (most_tiles(L, 256, 256) * 4 >= d.sms) {
+        if constexpr (MODE != kF8Weight) {
+            if (L.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 31) == 0)
+                return launch_cfg<MODE, 256, false, true>(L, d, mute, stream);
+        }
         return launch_cfg<MODE, 256, false>(L, d, mute, stream);
+    }
     return launch_cfg<MODE, 128, false>(L, d, mute, stream);
 }
 
