@@ -8,8 +8,8 @@
 // a row (activations in a product), 128 of a column (the operands of a weight gradient, which
 // sums over rows), or 128 x 128 (weights).
 //
-// A block of 256 threads owns 128 columns of 16 P rows: thread (tid & 15, tid >> 4) holds eight
-// neighbouring columns of P rows 16 apart in registers, as they came, so X is read once whatever
+// A block owns 128 columns of some rows (128 where a scale spans them): thread (tid & 15, tid >> 4)
+// holds eight neighbouring columns of P rows in registers, as they came, so X is read once whatever
 // is made of it and several blocks fit an SM to cover each other's loads. A row's maximum meets
 // in 16 lanes, a column's in registers, two lanes and shared memory. Maxima are of the
 // magnitudes' bits, two 16-bit values at a time: their order is the values', and a NaN exceeds all.
@@ -120,7 +120,7 @@ struct Raw {
         }
     }
     // The first n of them.
-    __device__ __forceinline__ void load_some(const void *X, int64_t i, int64_t n)
+    __device__ __forceinline__ void load_some(const void *X, int64_t i, int n)
     {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -181,34 +181,42 @@ struct Params {
 
 enum Kind { kRows = 1, kColumns = 2, kBoth = 3, kTiles = 4 };
 
+// Threads of a block: twice as many where a scale spans 128 rows, so that a thread holds four of
+// them (eight, and their products by factors, left two blocks of 256 on an SM).
+__host__ __device__ constexpr int threads_of(int kind) { return kind == kRows ? 256 : 512; }
+
 template <int TYPE, int KIND, int P, bool FACTORS>
-__global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
+__global__ void __launch_bounds__(threads_of(KIND), KIND == kRows ? 4 : KIND == kTiles ? 1 : 2) f8_quantize_kernel(const Params p)
 {
     constexpr bool DOWN = KIND != kRows;  // a scale spans rows
     constexpr bool HALVES = TYPE != kF32 && !FACTORS;  // maxima of 16-bit magnitudes
     constexpr int TOPS = HALVES ? 4 : 8;
-    static_assert(!DOWN || P == 8, "128 rows");
-    __shared__ uint32_t top_of[DOWN ? 8 : 1][DOWN ? 128 : 1];
+    constexpr int SPAN = threads_of(KIND) / 16;  // rows that a block takes at once
+    static_assert(!DOWN || P * SPAN == kF8Block, "128 rows");
+    constexpr int WARPS = threads_of(KIND) / 32;
+    __shared__ uint32_t top_of[DOWN ? WARPS : 1][DOWN ? 128 : 1];
+    __shared__ __align__(16) float inverse[DOWN ? 128 : 4];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
-    const int64_t cb = blockIdx.x, all = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+    const int cb = blockIdx.x;
+    const int64_t all = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
     if (all >= p.blocks)
         return;
     const int64_t e = KIND == kTiles ? all / p.row_blocks : 0;
     const int64_t rb = KIND == kTiles ? all - e * p.row_blocks : all;
-    const int64_t c0 = cb * kF8Block + tx * 8;
-    const int64_t r0 = rb * (16 * P) + ty;
+    // Rows and columns are below 2^31; what they address is not.
+    const int M = (int)p.M, K = (int)p.K, pitch = (K + 15) & ~15;
+    const int c0 = cb * kF8Block + tx * 8, r0 = (int)rb * (SPAN * P) + ty;
     const int64_t base = e * p.M;  // first row of this matrix
-    const int64_t pitch = f8_pitch(p.K);
 
     Raw<TYPE> raw[P];
     float factor[FACTORS ? P : 1];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int64_t r = r0 + 16 * i;
+        const int r = r0 + SPAN * i;
         raw[i].clear();
         if constexpr (FACTORS)
             factor[i] = 0.f;
-        if (r >= p.M)
+        if (r >= M)
             continue;
         int64_t from = base + r;
         if (KIND != kTiles && p.rows) {
@@ -219,10 +227,10 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
             if constexpr (FACTORS)
                 factor[i] = __ldg(p.factors + slot);
         }
-        if (p.vec && c0 + 8 <= p.K)
+        if (p.vec && c0 + 8 <= K)
             raw[i].load(p.X, from * p.K + c0);
         else
-            raw[i].load_some(p.X, from * p.K + c0, p.K - c0);
+            raw[i].load_some(p.X, from * p.K + c0, K - c0);
     }
     auto values = [&](int i, float (&v)[8]) {
         raw[i].values(v);
@@ -280,14 +288,14 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
             if constexpr (FACTORS)
                 top = __float_as_uint(__uint_as_float(top) * factor[i]) & 0x7fffffffu;
             const Scale s = scale_of(top);
-            const int64_t r = r0 + 16 * i;
-            if (r < p.M) {
+            const int r = r0 + SPAN * i;
+            if (r < M) {
                 float v[8];
                 values(i, v);
                 if (c0 < pitch)
-                    *reinterpret_cast<uint2 *>(p.row_codes + r * pitch + c0) = codes8(v, s.inv, s.nil);
+                    *reinterpret_cast<uint2 *>(p.row_codes + (int64_t)r * pitch + c0) = codes8(v, s.inv, s.nil);
                 if (tx == 0)
-                    p.row_scales[r * p.col_blocks + cb] = s.s;
+                    p.row_scales[(int64_t)r * p.col_blocks + cb] = s.s;
             }
         }
     }
@@ -310,19 +318,24 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
                            : tops[j % TOPS];
         }
         __syncthreads();
+        bool bad = false;  // a value that is not finite
         if (threadIdx.x < 128) {
             uint32_t t = top_of[0][threadIdx.x];
 #pragma unroll
-            for (int w = 1; w < 8; ++w)
+            for (int w = 1; w < WARPS; ++w)
                 t = max(t, top_of[w][threadIdx.x]);
-            if constexpr (KIND == kTiles)
-                t = __reduce_max_sync(0xffffffffu, t);
-            top_of[0][threadIdx.x] = t;
-            const int64_t c = cb * kF8Block + threadIdx.x;
-            if (KIND != kTiles && c < p.K)
-                p.col_scales[rb * p.K + c] = scale_of(t).s;
+            if constexpr (KIND == kTiles) {
+                top_of[0][threadIdx.x] = __reduce_max_sync(0xffffffffu, t);
+            } else {
+                const Scale s = scale_of(t);
+                inverse[threadIdx.x] = s.inv;
+                bad = t >= kInfBits;
+                const int c = cb * kF8Block + threadIdx.x;
+                if (c < K)
+                    p.col_scales[rb * p.K + c] = s.s;
+            }
         }
-        __syncthreads();
+        bad = __syncthreads_or(bad);
         if constexpr (KIND == kTiles) {
             const Scale s = scale_of(max(max(top_of[0][0], top_of[0][32]),
                                          max(top_of[0][64], top_of[0][96])));
@@ -330,34 +343,35 @@ __global__ void __launch_bounds__(kThreads) f8_quantize_kernel(const Params p)
                 p.row_scales[(e * p.row_blocks + rb) * p.col_blocks + cb] = s.s;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int64_t r = r0 + 16 * i;
+                const int r = r0 + SPAN * i;
                 float v[8];
                 values(i, v);
-                if (r < p.M && c0 < pitch)
+                if (r < M && c0 < pitch)
                     *reinterpret_cast<uint2 *>(p.row_codes + (base + r) * pitch + c0) =
                         codes8(v, s.inv, s.nil);
             }
         } else {
             float inv[8];
-            uint32_t keep[2] = {0, 0};  // 0 for the codes of a column that are 0
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const Scale s = scale_of(top_of[0][tx * 8 + j]);
-                inv[j] = s.inv;
-                keep[j / 4] |= s.nil ? 0u : 0xffu << (8 * (j & 3));
+            for (int j = 0; j < 8; j += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(inverse + tx * 8 + j);
+                inv[j] = f.x, inv[j + 1] = f.y, inv[j + 2] = f.z, inv[j + 3] = f.w;
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int64_t r = r0 + 16 * i;
+                const int r = r0 + SPAN * i;
                 float v[8];
                 values(i, v);
+                if (bad) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = inv[j] == 0.f ? 0.f : v[j];
+                }
 #pragma unroll
                 for (int j = 0; j < 8; j += 2)
                     mul2(v[j], v[j + 1], inv[j], inv[j + 1]);
-                const uint2 q = codes8(v);
-                if (r < p.M && c0 < pitch)
-                    *reinterpret_cast<uint2 *>(p.col_codes + r * pitch + c0) =
-                        make_uint2(q.x & keep[0], q.y & keep[1]);
+                if (r < M && c0 < pitch)
+                    *reinterpret_cast<uint2 *>(p.col_codes + (int64_t)r * pitch + c0) = codes8(v);
             }
         }
     }
@@ -372,11 +386,11 @@ static cudaError_t launch_kind(int type, Params p, int64_t blocks, cudaStream_t 
     p.blocks = blocks;
     const dim3 grid((unsigned)p.col_blocks, (unsigned)y, (unsigned)z);
     if (type == kF32)
-        f8_quantize_kernel<kF32, KIND, P, FACTORS><<<grid, kThreads, 0, stream>>>(p);
+        f8_quantize_kernel<kF32, KIND, P, FACTORS><<<grid, threads_of(KIND), 0, stream>>>(p);
     else if (type == kBf16)
-        f8_quantize_kernel<kBf16, KIND, P, FACTORS><<<grid, kThreads, 0, stream>>>(p);
+        f8_quantize_kernel<kBf16, KIND, P, FACTORS><<<grid, threads_of(KIND), 0, stream>>>(p);
     else
-        f8_quantize_kernel<kF16, KIND, P, FACTORS><<<grid, kThreads, 0, stream>>>(p);
+        f8_quantize_kernel<kF16, KIND, P, FACTORS><<<grid, threads_of(KIND), 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -385,9 +399,9 @@ static cudaError_t launch_rows_and_columns(int type, const Params &p, cudaStream
 {
     const int64_t down = f8_blocks(p.M);
     if (p.row_codes && p.col_codes)
-        return launch_kind<kBoth, 8, FACTORS>(type, p, down, stream);
+        return launch_kind<kBoth, 4, FACTORS>(type, p, down, stream);
     if (p.col_codes)
-        return launch_kind<kColumns, 8, FACTORS>(type, p, down, stream);
+        return launch_kind<kColumns, 4, FACTORS>(type, p, down, stream);
     // Four rows a thread where that still makes many blocks.
     if (p.M * p.col_blocks >= 64 * 2048)
         return launch_kind<kRows, 4, FACTORS>(type, p, (p.M + 63) / 64, stream);
@@ -532,7 +546,7 @@ cudaError_t launch_f8_quantize_tiles(int64_t E, int64_t K, int64_t N, int type, 
     p.row_blocks = f8_blocks(K);
     p.col_blocks = f8_blocks(N);
     p.vec = rows_on_16(type, W, N);
-    return launch_kind<kTiles, 8, false>(type, p, E * p.row_blocks, stream);
+    return launch_kind<kTiles, 4, false>(type, p, E * p.row_blocks, stream);
 }
 
 cudaError_t launch_f8_dequantize(int64_t E, int64_t M, int64_t K, int bm, int bk, int type,
