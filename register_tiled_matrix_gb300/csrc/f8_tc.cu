@@ -18,7 +18,7 @@
 //  * PW promoting warpgroups: read a set (a lane a thread), scale it into fp32 totals in
 //    registers, and store them at the end of the tile.
 // Rows of A are the lanes: a thread's scale is its row's times the tile's of W. With few rows
-// W's columns take the lanes instead (SWAP) and 16 to 128 rows of A the accumulator's columns,
+// W's columns take the lanes instead (SWAP) and 16 to 64 rows of A the accumulator's columns,
 // so that no lane idles and W is read once; the rows' scales then come through shared memory,
 // as the columns' of a weight gradient do.
 //
@@ -972,6 +972,9 @@ template <int MODE>
 static cudaError_t launch_mode(const F8Launch &L, const DeviceContext &d, bool mute, cudaStream_t stream)
 {
     if constexpr (MODE != kF8Weight) {
+        // Up to 64 rows (of an expert, on average): W's columns on the lanes. With more, 128 x 128
+        // tiles read W as often and give every lane a row (65 x 4096 x 4096 18.6 us, 128 swapped
+        // columns 25.7).
         const int64_t rows = L.offsets ? (L.rows + L.experts - 1) / L.experts : L.rows;
         if (rows <= 16)
             return launch_cfg<MODE, 16, true>(L, d, mute, stream);
@@ -980,7 +983,7 @@ static cudaError_t launch_mode(const F8Launch &L, const DeviceContext &d, bool m
         if (rows <= 64)
             return launch_cfg<MODE, 64, true>(L, d, mute, stream);
         if (rows <= 128)
-            return launch_cfg<MODE, 128, true>(L, d, mute, stream);
+            return launch_cfg<MODE, 128, false>(L, d, mute, stream);
     }
     if (most_tiles(L, 256, 256) * 4 >= d.sms) {
         if constexpr (MODE != kF8Weight) {
