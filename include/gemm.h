@@ -47,7 +47,8 @@
  *
  * CUDA graphs. After a first call of the same kind on the device (which fills
  * that cache), calls of gemm_f32, gemm_f32_ws, gemm_bf16f32, gemm_f16f32,
- * gemm_bf16f32_ws and gemm_f16f32_ws only enqueue kernels on `stream`: they
+ * gemm_bf16f32_ws, gemm_f16f32_ws and of the low-bit, 8-bit floating-point,
+ * routing and experts' entry points only enqueue kernels on `stream`: they
  * can be recorded by stream capture and replayed; the pointers, sizes and
  * workspace are fixed at capture. gemm_get_device_error synchronises and
  * must not be called while its stream is being captured.
