@@ -185,3 +185,23 @@ def test_rows_past_32_bits():
     assert torch.equal(qc[first:].double(), want) and torch.equal(sc[-1:].double(), ws)
     back = rtm.gemm_f8_dequantize(q, s, "rows", torch.bfloat16)
     assert torch.equal(back[-200:], ref.values(q[-200:], s[-200:], "rows").bfloat16())
+
+
+@pytest.mark.parametrize("type_", TYPES)
+@pytest.mark.parametrize("M,K", [(4100, 4096), (2600, 6416), (140000, 16), (127, 131200)])
+def test_rows_alone_of_whole_sixteens(M, K, type_):
+    """The kernel of large conversions along rows, plain and gathered with factors."""
+    x = values(M, K, TYPES[type_], seed=K)
+    x[5, 3], x[M - 1, K - 1], x[7] = torch.nan, torch.inf, 0
+    check(*rtm.gemm_f8_quantize(x, "rows"), x, "rows")
+    g = torch.Generator(device=DEV).manual_seed(2)
+    rows = torch.randint(-1, 2 * M, (M,), generator=g, device=DEV, dtype=torch.int32)
+    rows[3] = 2 * M
+    factors = torch.randn(M, 2, generator=g, device=DEV)
+    got = rtm.gemm_f8_quantize(x, "rows", gather=rows, fan=2, factors=factors)
+    check(*got, ref.gathered(x, rows, 2, factors), "rows")
+    whole = torch.empty(M * K + 8, dtype=x.dtype, device=DEV)
+    odd = whole[8:].view(M, K)  # 16 bytes (fp32: 32) on: another kernel
+    odd.copy_(x)
+    for a, b in zip(rtm.gemm_f8_quantize(odd, "rows"), rtm.gemm_f8_quantize(x, "rows")):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
