@@ -80,14 +80,19 @@ struct Cfg {
     // Floats of a slot: the lanes' scales or none, the columns' or none, the tiles'.
     static constexpr int SCALE_COLUMNS = SWAP ? 0 : LANES, SCALE_TILE = SCALE_COLUMNS + NT;
     static constexpr int SCALE_PITCH = SCALE_TILE + 4;
-    static_assert(!PAIR || (SCALE_SLOTS >= 2 * 4 * PW && NT >= 256), "room for 16 x 16 values a slot");
+
     static_assert(SCALE_AHEAD + 2 * SETS + 2 <= SCALE_SLOTS, "scales are read before their slot is written");
-    static constexpr int STAGES = NT >= 128 ? 6 : NT == 64 ? 8 : 10;
+    // (Of a pair's six stages the sixth is the boxes' room: 8192^3 takes as long with five.)
+    static constexpr int STAGES = PAIR ? 5 : NT >= 128 ? 6 : NT == 64 ? 8 : 10;
     static constexpr int PITCH = NT + 4;  // floats per lane of a partial tile
     // Partial tiles have room of their own where the stages are too small.
     static constexpr uint32_t OFF_GROUPS = STAGES * STAGE_BYTES;
     static constexpr uint32_t OFF_SCALE = OFF_GROUPS + 2 * (kMaxGroups + 4) * 4;
-    static constexpr uint32_t OFF_BARS = OFF_SCALE + SCALE_SLOTS * SCALE_PITCH * 4;
+    // A pair's warps stage 16 columns of their 32 rows of C at a time, twice.
+    static constexpr uint32_t BOX_BYTES = 32 * 16 * 4;
+    static constexpr uint32_t OFF_BOXES = (OFF_SCALE + SCALE_SLOTS * SCALE_PITCH * 4 + 1023) / 1024 * 1024;
+    static constexpr uint32_t OFF_BARS = PAIR ? OFF_BOXES + 4 * PW * 2 * BOX_BYTES
+                                              : OFF_SCALE + SCALE_SLOTS * SCALE_PITCH * 4;
     static constexpr size_t SMEM_BYTES = OFF_BARS + 256 + 1024 /*align*/;
     static_assert(LANES * PITCH * 4 <= OFF_GROUPS, "a partial tile fits the stages");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -116,6 +121,7 @@ struct Params {
     int splits;
     int mute;
     int c_vec;  // rows of C on 8-byte boundaries
+    int c_boxes;  // on 16-byte boundaries: tiles of pairs are stored in boxes
 };
 
 // kind::f8f6f4, D fp32, both operands e4m3, M = 128 (256 for a pair), N = NT.
@@ -179,25 +185,12 @@ __device__ __forceinline__ float2 lds_f32x2(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void sts_f32(uint32_t addr, float v)
-{
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 __device__ __forceinline__ void sts_f32x2(uint32_t addr, float a, float b)
 {
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
 __device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds32(addr)); }
-
-// Eight neighbouring floats, 32-byte aligned: a whole sector in one store.
-__device__ __forceinline__ void store8(float *p, const float *v)
-{
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
-                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
-}
 
 // What a tile is: its expert, first row and column of C, the rows' end, and the depth it sums.
 struct Tile {
@@ -303,13 +296,11 @@ __device__ __forceinline__ void count_tiles(const Params &p, int32_t *start, int
     }
 }
 
-// EIGHTS: rows of C start on 32 bytes and are whole eights (asked of a pair's forward and input
-// products: the two ways to store a tile in one kernel spill registers into its loop, 557 us
-// instead of 420 for 8192^3).
-template <int MODE, int NT, bool SWAP, bool EIGHTS>
+template <int MODE, int NT, bool SWAP>
 __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
     f8_tc_kernel(const __grid_constant__ CUtensorMap tm_lanes,
-                 const __grid_constant__ CUtensorMap tm_cols, const Params p)
+                 const __grid_constant__ CUtensorMap tm_cols,
+                 const __grid_constant__ CUtensorMap tm_c, const Params p)
 {
     using Cf = Cfg<NT, SWAP>;
     constexpr bool PAIR = Cf::PAIR;
@@ -321,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
     // Read from tensor memory as matrix fragments: a thread then has 4 lanes of a quarter of the
     // columns, so a warp stores 32 bytes of each of eight rows of C at a time whatever their
     // alignment, and a weight gradient's thread loads half as many of the columns' scales (8192^3
-    // 498 us, a lane a thread 550). On pairs a lane a thread is the faster form of the others:
+    // 492 us, a lane a thread 550). On pairs a lane a thread is the faster form of the others:
     // one scale a thread, and shared memory is what they wait for (420 us, fragments 480).
     constexpr bool FRAGMENTS = !SWAP && (MODE == kF8Weight || !PAIR);
     extern __shared__ uint8_t smem_raw[];
@@ -360,6 +351,8 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
         fence_mbarrier_init();
         tma_prefetch_desc(&tm_lanes);
         tma_prefetch_desc(&tm_cols);
+        if (PAIR && p.c_boxes)
+            tma_prefetch_desc(&tm_c);
     }
     __syncwarp();
     if (warp == 1) {
@@ -587,8 +580,9 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
         Place<Cf::SETS> set;
         float acc[Cf::CPT];
         bool seen = false;  // what the look ahead said
+        // (The loop's bounds are read again: every register here is a sum's.)
 #pragma unroll 1
-        for (int t = unit; t < tiles; t += units) {
+        for (int t = unit; t < plan.total(); t += (int)gridDim.x / (S * CTAS)) {
             const int blocks = blocks_of(plan.at(t), S, rank).count;
 #pragma unroll
             for (int j = 0; j < Cf::CPT; ++j)
@@ -729,7 +723,73 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
             }
             float *C = p.C + (MODE == kF8Weight ? (int64_t)x.group * p.rows * p.cols : 0);
             const int gl = lane0 + row;
-            if constexpr (FRAGMENTS) {
+            if constexpr (PAIR) {
+                // 16 columns of the warp's 32 rows at a time through shared memory (64-byte
+                // swizzle, two boxes in turn), stored by the tensor-memory-access unit; by the
+                // warp, 64 bytes of two rows at a time, where rows of C are off its 16-byte
+                // boundaries or the box ends in another expert's rows. Straight from registers,
+                // in pieces of 8 to 32 bytes of 8 to 32 rows at a time: 8192 x 8192 x 2048
+                // 157 us (142 this way), the gradient of W of 4097 x 4091 x 4001 120 (97), and
+                // 8192 x 8191 x 8192, whose rows are off the boundaries, 423 (450).
+                // Rows behind the last end the loop in the forward and input products, where an
+                // expert's last tile can have many; in the gradient of W, where only the
+                // matrix's last tile has any, the same test costs a tenth (8192^3 546, 494).
+                const int r0 = lane0 + quarter * 32;
+                const uint32_t boxes = smem_u32(smem + Cf::OFF_BOXES) +
+                                       (uint32_t)(pw * 4 + quarter) * (2 * Cf::BOX_BYTES);
+                const bool boxed = p.c_boxes && (x.row_end == p.rows || r0 + 32 <= x.row_end);
+#pragma unroll
+                for (int j = 0; j < Cf::CPT; j += 16) {
+                    if (MODE != kF8Weight && r0 >= x.row_end)
+                        break;
+                    const uint32_t box = boxes + (uint32_t)(j / 16 & 1) * Cf::BOX_BYTES;
+                    if (lane == 0)
+                        bulk_wait_group_read<1>();  // what this box held has been read
+                    __syncwarp();
+                    if constexpr (FRAGMENTS) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {  // q, k, e
+                            const int q = i / 4, k = i / 2 % 2, e = i % 2;
+                            const int l = q * 16 + e * 8 + (lane >> 2);
+                            const float *v = acc + ((j / 32 * 2 + q) * 4 + j / 16 % 2 * 2 + k) * 4 + 2 * e;
+                            const uint32_t chunk = (uint32_t)(2 * k + ((lane & 3) >> 1));
+                            sts_f32x2(box + (uint32_t)l * 64 + ((chunk ^ (l >> 1 & 3)) << 4) + (lane & 1) * 8,
+                                      v[0], v[1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            sts128(box + (uint32_t)lane * 64 + ((c ^ (lane >> 1 & 3)) << 4),
+                                   make_uint4(__float_as_uint(acc[j + 4 * c]), __float_as_uint(acc[j + 4 * c + 1]),
+                                              __float_as_uint(acc[j + 4 * c + 2]),
+                                              __float_as_uint(acc[j + 4 * c + 3])));
+                    }
+                    const int c0 = col0 + j;
+                    if (boxed) {
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if ((MODE != kF8Weight || r0 < x.row_end) && c0 < p.cols)
+                                tma_store_3d(&tm_c, box, c0, r0, MODE == kF8Weight ? x.group : 0);
+                            bulk_commit_group();
+                        }
+                    } else {
+                        __syncwarp();
+                        const int c = lane & 15, hi = lane >> 4;
+                        const int rows = x.row_end - r0 - hi;
+                        float *to = C + (int64_t)(r0 + hi) * p.cols + c0 + c;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i, to += 2 * p.cols) {
+                            const float v = lds_f32(box + (uint32_t)(2 * i + hi) * 64 +
+                                                    (((c >> 2) ^ (i & 3)) << 4) + (c & 3) * 4);
+                            if (2 * i < rows && c0 + c < p.cols)
+                                *to = v;
+                        }
+                        if (lane == 0)
+                            bulk_commit_group();  // an empty one: the wait above counts groups
+                    }
+                }
+            } else if constexpr (FRAGMENTS) {
                 each_fragment([&](int l, int c, const float *v) {
                     const int r = lane0 + l, at = x.c0 + c;
                     float *to = C + (int64_t)r * p.cols + at;
@@ -744,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                             to[1] = v[1];
                     }
                 });
-            } else if constexpr (SWAP) {  // a warp's lanes: 32 consecutive floats of a row of C
+            } else {  // a warp's lanes: 32 consecutive floats of a row of C
                 if (gl < p.cols) {
                     float *c = C + (int64_t)col0 * p.cols + gl;
                     const int n = x.row_end - col0;
@@ -753,40 +813,10 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         if (j < n)
                             *c = acc[j];
                 }
-            } else if constexpr (EIGHTS) {
-                if (gl < x.row_end) {
-                    float *c = C + (int64_t)gl * p.cols + col0;
-#pragma unroll
-                    for (int j = 0; j < Cf::CPT; j += 8)
-                        if (col0 + j < p.cols)
-                            store8(c + j, acc + j);
-                }
-            } else {
-                // 16 columns at a time through shared memory (the ring's columns, which this mode
-                // leaves, two slots a warp, 16 rows in each), so that a warp stores 64 bytes of
-                // two rows: 8192 x 8191 x 8192 takes 687 us where each lane stores its own row.
-                const uint32_t mine = smem_u32(smem + Cf::OFF_SCALE) + Cf::SCALE_COLUMNS * 4 +
-                                      (uint32_t)(2 * (pw * 4 + quarter)) * SLOT_BYTES;
-                const int r16 = lane & 15, hi = lane >> 4;
-#pragma unroll
-                for (int j = 0; j < Cf::CPT; j += 16) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        sts_f32(mine + hi * SLOT_BYTES + (uint32_t)(r16 * 16 + (e ^ r16)) * 4, acc[j + e]);
-                    __syncwarp();
-                    const int gc = col0 + j + r16;
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const int l = 2 * i + hi, r = l & 15;
-                        const float v = lds_f32(mine + (l >> 4) * SLOT_BYTES + (uint32_t)(r * 16 + (r16 ^ r)) * 4);
-                        const int gr = lane0 + quarter * 32 + l;
-                        if (gr < x.row_end && gc < p.cols)
-                            C[(int64_t)gr * p.cols + gc] = v;
-                    }
-                    __syncwarp();
-                }
             }
         }
+        if (PAIR && lane == 0)
+            bulk_wait_group<0>();  // no store reads shared memory that is no longer this CTA's
     }
     __syncwarp();  // the barriers below are the whole warp's
 
@@ -876,6 +906,19 @@ static bool encode_codes(EncodeTiledFn fn, CUtensorMap *map, const void *base, u
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// batch x rows x cols floats of C in boxes of 32 x 16.
+static bool encode_result(EncodeTiledFn fn, CUtensorMap *map, float *base, uint64_t batch,
+                          uint64_t rows, uint64_t cols)
+{
+    cuuint64_t dims[3] = {cols, rows, batch};
+    cuuint64_t strides[2] = {cols * 4, batch > 1 ? rows * cols * 4 : cols * 4};
+    cuuint32_t box[3] = {16, 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Most tiles that any offsets can make.
 static int64_t most_tiles(const F8Launch &L, int rows, int cols)
 {
@@ -887,7 +930,7 @@ static int64_t most_tiles(const F8Launch &L, int rows, int cols)
     return (L.rows / rows + (L.experts < L.rows ? L.experts : L.rows)) * tc;
 }
 
-template <int MODE, int NT, bool SWAP, bool EIGHTS = false>
+template <int MODE, int NT, bool SWAP>
 static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mute, cudaStream_t stream)
 {
     using Cf = Cfg<NT, SWAP>;
@@ -908,9 +951,13 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
         else
             ok = ok && encode_codes(fn, &wm, L.b, E, L.cols, L.depth, L.ldb, SWAP ? LANES : Cf::BN);
     }
+    CUtensorMap result = {};
+    const bool boxes = Cf::PAIR && L.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 15) == 0;
+    if (boxes)
+        ok = ok && encode_result(fn, &result, L.C, MODE == kF8Weight ? E : 1, L.rows, L.cols);
     if (!ok)
         return cudaErrorInvalidValue;
-    auto kernel = f8_tc_kernel<MODE, NT, SWAP, EIGHTS>;
+    auto kernel = f8_tc_kernel<MODE, NT, SWAP>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = set_smem_limit_once(kernel, (int)Cf::SMEM_BYTES, done);
     if (e != cudaSuccess)
@@ -931,6 +978,7 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
     p.err = d.err;
     p.limit_ns = d.wait_limit_ns;
     p.mute = mute ? 1 : 0;
+    p.c_boxes = boxes ? 1 : 0;
     p.c_vec = L.cols % 2 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 7) == 0;
     // Few tiles: split the depth while every CTA keeps at least two blocks (a pair four) and
     // all clusters (of at most 8 CTAs) are resident at once.
@@ -965,7 +1013,7 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, lanes, cols, p);
+    return cudaLaunchKernelEx(&cfg, kernel, lanes, cols, result, p);
 }
 
 template <int MODE>
@@ -985,13 +1033,8 @@ static cudaError_t launch_mode(const F8Launch &L, const DeviceContext &d, bool m
         if (rows <= 128)
             return launch_cfg<MODE, 128, false>(L, d, mute, stream);
     }
-    if (most_tiles(L, 256, 256) * 4 >= d.sms) {
-        if constexpr (MODE != kF8Weight) {
-            if (L.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 31) == 0)
-                return launch_cfg<MODE, 256, false, true>(L, d, mute, stream);
-        }
+    if (most_tiles(L, 256, 256) * 4 >= d.sms)
         return launch_cfg<MODE, 256, false>(L, d, mute, stream);
-    }
     return launch_cfg<MODE, 128, false>(L, d, mute, stream);
 }
 

@@ -169,7 +169,18 @@ __device__ __forceinline__ void tma_store_2d(const void *tmap, uint32_t src, int
                  : "memory");
 }
 
-// The same box added element by element into global memory (fp32 add at the
+// The same of a 3-D tensor.
+__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int32_t c0, int32_t c1,
+                                             int32_t c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(tmap)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// The 2-D box of tma_store_2d added element by element into global memory (fp32 add at the
 // L2, tracked in bulk async-groups like a store).
 __device__ __forceinline__ void tma_reduce_add_2d(const void *tmap, uint32_t src, int32_t c0,
                                                   int32_t c1)

@@ -72,6 +72,15 @@ def test_rows_by_expert(direction, name, K, N):
     check_rows(direction, o, o[-1] + 37, K, N, 8, seed=K)
 
 
+@pytest.mark.parametrize("direction", ["forward", "input"])
+@pytest.mark.parametrize("K,N", [(1100, 1028), (1102, 1030)])
+def test_rows_by_expert_of_large_tiles(direction, K, N):
+    """Experts that end at, before and behind the 32 rows that are stored at a time."""
+    lengths = [n for m in range(14) for n in (256 + m, 32 * m, 33 * m, 255 - m, 31)]
+    o = parts(lengths, first=3)
+    check_rows(direction, o, o[-1] + 29, K, N, len(lengths), seed=N)
+
+
 @pytest.mark.parametrize("E,most", [(1, 300), (200, 7), (1024, 3), (64, 200)])
 def test_numbers_of_experts(E, most):
     g = torch.Generator().manual_seed(E)

@@ -118,6 +118,22 @@ def test_contiguous_codes_and_a_given_result():
     assert torch.equal(rtm.gemm_f8w8f32(a, s, w, t, out=odd), out)
 
 
+@pytest.mark.parametrize("direction", CALLS)
+@pytest.mark.parametrize("M,N,K", [(2030, 2004, 2012), (2030, 2002, 2010), (2031, 2001, 2009)])
+def test_large_results_at_every_alignment(direction, M, N, K):
+    """Rows of 16, 8 and 4 bytes' multiples, from 0, 4, 8 and 12 bytes behind a boundary."""
+    a, s, b, t, left, right = operands(direction, M, N, K)
+    rows, cols = left.shape[0], right.shape[1]
+    want = CALLS[direction](a, s, b, t)
+    ref.close(want, left @ right, left.abs() @ right.abs(), blocks(left.shape[1]))
+    for shift in range(4):
+        whole = torch.full((rows * cols + 64,), 7.0, device=DEV)
+        out = whole[32 + shift:32 + shift + rows * cols].view(rows, cols)
+        CALLS[direction](a, s, b, t, out=out)
+        assert torch.equal(out, want)
+        assert (whole[:32 + shift] == 7).all() and (whole[32 + shift + rows * cols:] == 7).all()
+
+
 @pytest.mark.parametrize("M", [5, 100, 600])
 def test_not_a_number_stays_in_its_row_and_column(M):
     K, N = 300, 400
