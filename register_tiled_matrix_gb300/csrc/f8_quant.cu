@@ -13,12 +13,15 @@
 // is made of it and several blocks fit an SM to cover each other's loads. A row's maximum meets
 // in 16 lanes, a column's in registers, two lanes and shared memory. Maxima are of the
 // magnitudes' bits, two 16-bit values at a time: their order is the values', and a NaN exceeds all.
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "f8.h"
+#include "kernels.h"
+#include "ptx.cuh"
 
 namespace rtm {
 namespace f8q {
@@ -186,7 +189,8 @@ enum Kind { kRows = 1, kColumns = 2, kBoth = 3, kTiles = 4 };
 __host__ __device__ constexpr int threads_of(int kind) { return kind == kRows ? 256 : 512; }
 
 template <int TYPE, int KIND, int P, bool FACTORS>
-__global__ void __launch_bounds__(threads_of(KIND), KIND == kRows ? 4 : KIND == kTiles ? 1 : 2) f8_quantize_kernel(const Params p)
+__global__ void __launch_bounds__(threads_of(KIND), KIND == kRows ? 4 : KIND == kTiles ? 1 : TYPE != kF32 && !FACTORS ? 3 : 2)
+    f8_quantize_kernel(const Params p)
 {
     constexpr bool DOWN = KIND != kRows;  // a scale spans rows
     constexpr bool HALVES = TYPE != kF32 && !FACTORS;  // maxima of 16-bit magnitudes
@@ -472,6 +476,256 @@ __global__ void __launch_bounds__(256) f8_quantize_rows_kernel(const Params p)
     }
 }
 
+// Scales that span rows, for rows of whole sixteens on 16-byte boundaries: the 128 x 128 values
+// of a block are copied to shared memory, 16 bytes at a time and zeros where there are none, and
+// read there once for the maxima and the row codes and once for the other codes. Held in
+// registers they leave two or three blocks on an SM; so it has five (fp32 three), which cover each
+// other's copies. A thread has 16 columns of four rows. us, and with the kernel above: 8192 x 8192
+// bf16 columns 41 (49), both 51 (64), tiles 36 (50); 32768 gathered rows of 2048, both ways, 59
+// (80), with factors 66 (84); fp32 tiles 57 (82). fp32 columns 66 (61) and both 80 (73) stay
+// above: their values take half an SM's shared memory twice over, and no more are in flight.
+template <int TYPE>
+struct Staged {
+    static constexpr int SIZE = TYPE == kF32 ? 4 : 2, CHUNKS = 8 * SIZE;  // of 16 bytes in 128 values
+    static constexpr uint32_t ROW = 128 * SIZE, BYTES = 128 * ROW;
+    // Chunk c of a row: the chunks that eight lanes read at once lie in different banks.
+    __device__ static uint32_t at(int row, int c)
+    {
+        return row * ROW + ((TYPE == kF32 ? c ^ (c >> 3 & 3) : c ^ (c >> 3 & 1)) << 4);
+    }
+};
+
+template <int TYPE, int KIND, bool FACTORS>
+__global__ void __launch_bounds__(256, TYPE == kF32 ? 3 : 5)
+    f8_quantize_staged_kernel(const Params p)
+{
+    using St = Staged<TYPE>;
+    constexpr int P = 4, SPAN = 32, WARPS = 8;  // rows of a thread, SPAN apart
+    constexpr bool PAIRS = TYPE != kF32 && !FACTORS;  // columns' maxima of 16-bit magnitudes, two a word
+    constexpr int TOPS = PAIRS ? 8 : 16, WORDS = TYPE == kF32 ? 16 : 8;
+    extern __shared__ __align__(16) uint8_t staged[];
+    __shared__ __align__(16) uint32_t top_of[WARPS][8 * TOPS];
+    __shared__ __align__(16) float inverse[128];
+    __shared__ float factors[FACTORS ? 128 : 1];
+    const int64_t all = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+    if (all >= p.blocks)
+        return;
+    const int64_t e = KIND == kTiles ? all / p.row_blocks : 0;
+    const int64_t rb = KIND == kTiles ? all - e * p.row_blocks : all;
+    const int64_t base = e * p.M;  // first row of this matrix
+    const int M = (int)p.M, K = (int)p.K, cb = blockIdx.x, row0 = (int)rb * kF8Block;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(staged);
+    {
+        constexpr int STEP = 256 / St::CHUNKS;  // rows copied at once
+        const int chunk = threadIdx.x % St::CHUNKS, c = cb * kF8Block + chunk * (16 / St::SIZE);
+#pragma unroll
+        for (int i = 0; i < 128 / STEP; ++i) {
+            const int l = threadIdx.x / St::CHUNKS + i * STEP, r = row0 + l;
+            int64_t from = base + r;
+            bool held = r < M && c < K;
+            if (KIND != kTiles && held && p.rows) {
+                const int slot = __ldg(p.rows + r);
+                from = (uint32_t)slot / p.fan;
+                held = slot >= 0 && from < p.source;
+            }
+            const void *x = static_cast<const uint8_t *>(p.X) + (held ? (from * p.K + c) * St::SIZE : 0);
+            cp_async_16(to + St::at(l, chunk), x, held ? 16u : 0u);
+        }
+        cp_async_commit();
+    }
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+    const int c0 = cb * kF8Block + tx * 16, r0 = row0 + ty;
+    if constexpr (FACTORS) {
+        if (threadIdx.x < 128) {
+            const int r = row0 + threadIdx.x, slot = r < M ? __ldg(p.rows + r) : -1;
+            factors[threadIdx.x] =
+                slot >= 0 && (uint32_t)slot / p.fan < p.source ? __ldg(p.factors + slot) : 0.f;
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // Words of row i, as they came.
+    auto read = [&](int i, uint32_t (&w)[WORDS]) {
+#pragma unroll
+        for (int q = 0; q < WORDS / 4; ++q) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(staged + St::at(ty + SPAN * i, tx * (WORDS / 4) + q));
+            w[4 * q] = a.x, w[4 * q + 1] = a.y, w[4 * q + 2] = a.z, w[4 * q + 3] = a.w;
+        }
+    };
+    // Eight of them, times the row's factor.
+    auto values = [&](const uint32_t (&w)[WORDS], int i, int h, float (&v)[8]) {
+        Raw<TYPE> eight;
+#pragma unroll
+        for (int j = 0; j < WORDS / 2; ++j)
+            eight.w[j] = w[h * (WORDS / 2) + j];
+        eight.values(v);
+        if constexpr (FACTORS) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 2)
+                mul2(v[j], v[j + 1], factors[ty + SPAN * i], factors[ty + SPAN * i]);
+        }
+    };
+
+    uint32_t tops[TOPS] = {};  // magnitudes' bits: their order is the values', NaN above all
+#pragma unroll(FACTORS ? 2 : P)  // two: registers for five blocks
+    for (int i = 0; i < P; ++i) {
+        uint32_t w[WORDS];
+        read(i, w);
+        uint32_t top = 0;
+        if constexpr (PAIRS) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                tops[j] = max2(tops[j], w[j] & 0x7fff7fffu);
+        }
+        if constexpr (KIND & kRows) {
+            if constexpr (TYPE == kF32) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    top = max(top, w[j] & 0x7fffffffu);
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = max2(top, w[j] & 0x7fff7fffu);
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2)
+                    top = max2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = widen<TYPE>(max(top & 0xffffu, top >> 16));
+            }
+            // That of X's row times the factor's is the products': rounding keeps order.
+            if constexpr (FACTORS)
+                top = __float_as_uint(__uint_as_float(top) * factors[ty + SPAN * i]) & 0x7fffffffu;
+        }
+        const Scale s = scale_of(top);
+        uint2 q[2];
+        if constexpr (!PAIRS || (KIND & kRows)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[8];
+                values(w, i, h, v);
+                if constexpr (!PAIRS) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        tops[8 * h + j] = max(tops[8 * h + j], __float_as_uint(v[j]) & 0x7fffffffu);
+                }
+                if constexpr (KIND & kRows)
+                    q[h] = codes8(v, s.inv, s.nil);
+            }
+        }
+        if constexpr (KIND & kRows) {
+            const int r = r0 + SPAN * i;
+            if (r < M) {
+                if (c0 < K)
+                    *reinterpret_cast<uint4 *>(p.row_codes + (int64_t)r * K + c0) =
+                        make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+                if (tx == 0)
+                    p.row_scales[(int64_t)r * p.col_blocks + cb] = s.s;
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < TOPS; ++j)
+#pragma unroll
+        for (int o = 8; o < 32; o *= 2) {
+            const uint32_t t = __shfl_xor_sync(0xffffffffu, tops[j], o);
+            tops[j] = PAIRS ? max2(tops[j], t) : max(tops[j], t);
+        }
+    if ((threadIdx.x & 31) < 8) {
+#pragma unroll
+        for (int j = 0; j < TOPS; j += 4)
+            *reinterpret_cast<uint4 *>(&top_of[threadIdx.x >> 5][tx * TOPS + j]) =
+                make_uint4(tops[j], tops[j + 1], tops[j + 2], tops[j + 3]);
+    }
+    __syncthreads();
+    bool bad = false;  // a value that is not finite
+    if (threadIdx.x < 8 * TOPS) {
+        uint32_t t = top_of[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w)
+            t = PAIRS ? max2(t, top_of[w][threadIdx.x]) : max(t, top_of[w][threadIdx.x]);
+        if constexpr (KIND == kTiles) {
+            top_of[0][threadIdx.x] =
+                __reduce_max_sync(0xffffffffu, PAIRS ? widen<TYPE == kF32 ? kBf16 : TYPE>(max(t & 0xffffu, t >> 16)) : t);
+        } else {
+#pragma unroll
+            for (int j = 0; j < (PAIRS ? 2 : 1); ++j) {
+                const uint32_t bits = PAIRS ? widen<TYPE == kF32 ? kBf16 : TYPE>(j ? t >> 16 : t & 0xffffu) : t;
+                const int at = PAIRS ? 2 * threadIdx.x + j : threadIdx.x;
+                const Scale s = scale_of(bits);
+                inverse[at] = s.inv;
+                bad |= bits >= kInfBits;
+                if (cb * kF8Block + at < K)
+                    p.col_scales[rb * p.K + cb * kF8Block + at] = s.s;
+            }
+        }
+    }
+    bad = __syncthreads_or(bad);
+    uint8_t *codes = p.col_codes;
+    Scale tile;
+    if constexpr (KIND == kTiles) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int j = 0; j < 8 * TOPS; j += 32)
+            t = max(t, top_of[0][j]);
+        tile = scale_of(t);
+        if (threadIdx.x == 0)
+            p.row_scales[(e * p.row_blocks + rb) * p.col_blocks + cb] = tile.s;
+        bad = tile.nil;
+        codes = p.row_codes;
+    }
+    float inv[16];
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        float4 f;
+        if constexpr (KIND == kTiles)
+            f = make_float4(tile.inv, tile.inv, tile.inv, tile.inv);
+        else
+            f = *reinterpret_cast<const float4 *>(inverse + tx * 16 + j);
+        inv[j] = f.x, inv[j + 1] = f.y, inv[j + 2] = f.z, inv[j + 3] = f.w;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        uint32_t w[WORDS];
+        read(i, w);
+        uint2 q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            values(w, i, h, v);
+            if (bad) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = inv[8 * h + j] == 0.f ? 0.f : v[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j += 2)
+                mul2(v[j], v[j + 1], inv[8 * h + j], inv[8 * h + j + 1]);
+            q[h] = codes8(v);
+        }
+        const int r = r0 + SPAN * i;
+        if (r < M && c0 < K)
+            *reinterpret_cast<uint4 *>(codes + (base + r) * K + c0) =
+                make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+    }
+}
+
+template <int TYPE, int KIND, bool FACTORS>
+static cudaError_t launch_staged(const Params &p, cudaStream_t stream)
+{
+    auto kernel = f8_quantize_staged_kernel<TYPE, KIND, FACTORS>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = set_smem_limit_once(kernel, (int)Staged<TYPE>::BYTES, done);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t y = p.blocks < 65535 ? p.blocks : 65535, z = (p.blocks + y - 1) / y;
+    if (z > 65535 || p.col_blocks > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    kernel<<<dim3((unsigned)p.col_blocks, (unsigned)y, (unsigned)z), 256, Staged<TYPE>::BYTES, stream>>>(p);
+    return cudaGetLastError();
+}
+
 template <bool FACTORS>
 static cudaError_t launch_rows(int type, Params p, cudaStream_t stream)
 {
@@ -492,6 +746,17 @@ static cudaError_t launch_rows(int type, Params p, cudaStream_t stream)
 template <int KIND, int P, bool FACTORS>
 static cudaError_t launch_kind(int type, Params p, int64_t blocks, cudaStream_t stream)
 {
+    if constexpr (KIND != kRows) {
+        if (p.K % 16 == 0 && p.vec) {
+            p.blocks = blocks;
+            if (type == kBf16)
+                return launch_staged<kBf16, KIND, FACTORS>(p, stream);
+            if (type == kF16)
+                return launch_staged<kF16, KIND, FACTORS>(p, stream);
+            if constexpr (KIND == kTiles)
+                return launch_staged<kF32, KIND, FACTORS>(p, stream);
+        }
+    }
     const int64_t y = blocks < 65535 ? blocks : 65535, z = (blocks + y - 1) / y;
     if (z > 65535 || p.col_blocks > 0x7fffffff)
         return cudaErrorInvalidValue;

@@ -205,3 +205,39 @@ def test_rows_alone_of_whole_sixteens(M, K, type_):
     odd.copy_(x)
     for a, b in zip(rtm.gemm_f8_quantize(odd, "rows"), rtm.gemm_f8_quantize(x, "rows")):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("type_", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 16), (129, 48), (257, 1024), (100, 144), (1000, 2000)])
+def test_scales_that_span_rows_of_whole_sixteens(M, K, type_):
+    """The kernels of such rows, and the one of rows off 16 bytes: the same codes."""
+    x = values(M, K, TYPES[type_], seed=K)
+    x[M // 2, K - 3], x[M - 1, 1], x[0] = torch.nan, -torch.inf, 0
+    x[:, 2] = 2.0 ** -20 if type_ == "f16" else 2.0 ** -110
+    whole = torch.empty(M * K + 1, dtype=x.dtype, device=DEV)
+    odd = whole[1:].view(M, K)
+    odd.copy_(x)
+    for one in (x, odd):
+        both = rtm.gemm_f8_quantize(one, "both")
+        check(*both[:2], x, "rows")
+        check(*both[2:], x, "columns")
+        check(*rtm.gemm_f8_quantize(one, "columns"), x, "columns")
+        check(*rtm.gemm_f8_quantize_tiles(one), x, "tiles")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rows = torch.randint(-1, 3 * M + 1, (M + 77,), generator=g, device=DEV, dtype=torch.int32)
+    factors = torch.randn(M, 3, generator=g, device=DEV)
+    for f in (None, factors):
+        want = ref.gathered(x, rows, 3, f)
+        both = rtm.gemm_f8_quantize(x, "both", gather=rows, fan=3, factors=f)
+        check(*both[:2], want, "rows")
+        check(*both[2:], want, "columns")
+        check(*rtm.gemm_f8_quantize(x, "columns", gather=rows, fan=3, factors=f), want, "columns")
+
+
+def test_matrices_of_whole_sixteens():
+    for dtype in TYPES.values():
+        w = values(3 * 200, 144, dtype, seed=4).view(3, 200, 144)
+        codes, scales = rtm.gemm_f8_quantize_tiles(w)
+        for e in range(3):
+            want, s = ref.quantize(w[e], "tiles")
+            assert torch.equal(codes[e].double(), want) and torch.equal(scales[e].double(), s)
