@@ -241,3 +241,21 @@ def test_matrices_of_whole_sixteens():
         for e in range(3):
             want, s = ref.quantize(w[e], "tiles")
             assert torch.equal(codes[e].double(), want) and torch.equal(scales[e].double(), s)
+
+
+@pytest.mark.parametrize("kind", ["rows", "columns", "tiles"])
+def test_back_at_every_alignment(kind):
+    """Scales off 16 bytes, results off 32: the same values."""
+    M, K = 260, 648
+    x = values(M, K, torch.float32)
+    codes, s = rtm.gemm_f8_quantize_tiles(x) if kind == "tiles" else rtm.gemm_f8_quantize(x, kind)
+    shifted = torch.empty(s.numel() + 1, device=DEV)[1:].view(s.shape)
+    shifted.copy_(s)
+    for dtype in TYPES.values():
+        want = ref.values(codes, s, kind).to(dtype)
+        for scales in (s, shifted):
+            for off in (0, 1, 4, 8):
+                whole = torch.full((M * K + 32,), 7.0, dtype=dtype, device=DEV)
+                out = whole[off:off + M * K].view(M, K)
+                assert torch.equal(rtm.gemm_f8_dequantize(codes, scales, kind, dtype, out=out), want)
+                assert (whole[:off] == 7).all() and (whole[off + M * K:] == 7).all()
