@@ -80,9 +80,10 @@ def _codes_in_detail(name: str, t, dims: int, device: int) -> int:
     if t.numel() == 0:
         return (t.shape[-1] + 15) // 16 * 16
     rows, cols = t.shape[-2:]
-    # A single row's stride says nothing; neither does one of a dimension of length 1.
-    ld = t.stride(-2) if rows > 1 else t.stride(-3) if dims == 3 and t.shape[0] > 1 else 0
-    ld = ld or (cols + 15) // 16 * 16
+    # The stride of a dimension of length 1 says nothing; any other one is the pitch as it is (0,
+    # a repeated row's, is refused below).
+    ld = (t.stride(-2) if rows > 1 else t.stride(-3) if dims == 3 and t.shape[0] > 1
+          else (cols + 15) // 16 * 16)
     if ((cols > 1 and t.stride(-1) != 1) or ld % 16 or ld < cols or t.data_ptr() % 16
             or (dims == 3 and t.shape[0] > 1 and t.stride(0) != rows * ld)):
         raise ValueError(f"{name}: a row's codes must be neighbours, rows a multiple of 16 bytes "
