@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(Cfg<NT, SWAP>::THREADS, 1)
                         const int rows = x.row_end - r0 - hi;
                         float *to = C + (int64_t)(r0 + hi) * p.cols + c0 + c;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i, to += 2 * p.cols) {
+                        for (int i = 0; i < 16; ++i, to += 2u * (uint32_t)p.cols) {  // below 2^32, not 2^31
                             const float v = lds_f32(box + (uint32_t)(2 * i + hi) * 64 +
                                                     (((c >> 2) ^ (i & 3)) << 4) + (c & 3) * 4);
                             if (2 * i < rows && c0 + c < p.cols)
