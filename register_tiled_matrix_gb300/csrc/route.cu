@@ -9,8 +9,8 @@
 // A warp owns a token, a lane every 32nd expert; maxima meet in warp reductions of the values'
 // ordered bits. Which experts are chosen must not hang on rounding. Without bias and groups the
 // logits decide (both scores rise with them). Otherwise fp32 scores decide while each gap that
-// matters exceeds what their rounding can move; a token with a closer one (2 in 1000 of random
-// ones) is decided again in fp64.
+// matters exceeds what their rounding can move; a token with a closer one (of random ones with a
+// bias 1 in 1000 for sigmoids, 6 for softmax) is decided again in fp64.
 //
 // The order by expert is a stable counting sort without atomics on positions: a block owns a
 // run of tokens and counts its slots by expert, a second launch adds the counts of the blocks
@@ -113,10 +113,11 @@ __device__ __forceinline__ int take_best(Key (&v)[V], int lane, Key &top)
     return (int)at;
 }
 
-// Whether a's lead over b is beyond what fp32 can have moved. A sigmoid is within 2e-7 of the
-// real one and 1e-6 of itself, a softmax score within 1e-6, and 6e-6 of itself while it is above
-// 1e-30 (the exponent's rounding, 2^-24 of at most 70, and the sum's); adding the bias or two
-// scores rounds once more, 2^-24 of the sum.
+// Whether a's lead over b, scores + bias, is beyond what fp32 can have moved. A sigmoid is within
+// 2.5e-7 of the real one and 1e-6 of itself, a softmax score within 1e-6, and 6e-6 of itself while
+// it is above 1e-30 (the exponent's rounding, 2^-24 of at most 70, and the sum's); adding the bias
+// rounds once more, 2^-24 of the sum. What is below b is then certain too: value + error rises
+// with the value.
 __device__ __forceinline__ bool leads(float a, float b, const RouteLaunch &L)
 {
     const float size = fabsf(a) + fabsf(b);
@@ -125,6 +126,16 @@ __device__ __forceinline__ bool leads(float a, float b, const RouteLaunch &L)
     return a - b > (L.sigmoid ? 2.5e-6f : 1.3e-5f) * size + 1e-30f;
 }
 __device__ __forceinline__ bool leads(double, double, const RouteLaunch &) { return true; }
+
+// What fp32 can have moved a group's sum of two scores + bias by, whose magnitudes add up to
+// `wide`: each rounds, 2^-24 of itself, and so does their sum. The sum's own magnitude bounds
+// nothing: biases of opposite sign cancel in it, their roundings do not.
+__device__ __forceinline__ float group_error(float wide, const RouteLaunch &L)
+{
+    if (L.bias)
+        return (L.sigmoid ? 5e-7f : 2e-6f) + 2.5e-7f * wide;
+    return (L.sigmoid ? 2.5e-6f : 1.3e-5f) * wide + 1e-30f;
+}
 
 struct Args {
     RouteLaunch L;
@@ -163,22 +174,24 @@ __device__ __forceinline__ bool select(typename S::Key (&v)[V], const RouteLaunc
             two = low > high ? low : high;
         }
         __syncwarp();
-        Key sum[1] = {S::key(size > 1 ? S::value(one) + S::value(two) : S::value(one))};
-        sum[0] = __shfl_sync(kAll, sum[0], min(lane, L.groups - 1) * share);  // lane g: group g's
-        if (lane >= L.groups)
-            sum[0] = 0;
+        const Value first = S::value(one), second = size > 1 ? S::value(two) : Value(0);
+        const int from = min(lane, L.groups - 1) * share;  // lane g: group g's
+        const Key total = __shfl_sync(kAll, S::key(first + second), from);
+        Key sum[1] = {lane < L.groups ? total : 0};
         uint32_t chosen = 0;
-        Value last = 0;
-        const int rounds = scored ? min(L.top_groups + 1, L.groups) : L.top_groups;
 #pragma unroll 1
-        for (int j = 0; j < rounds; ++j) {
+        for (int j = 0; j < L.top_groups; ++j) {
             Key top;
-            const int g = take_best<1>(sum, lane, top);
-            if (j == L.top_groups)
-                sure = leads(last, S::value(top), L);
-            else
-                chosen |= 1u << g;
-            last = S::value(top);
+            chosen |= 1u << take_best<1>(sum, lane, top);
+        }
+        // Certain where every group taken leads every other one, each with an error of its own.
+        // (Neighbours in the order do not tell: a sum far from another can have the larger one.)
+        if constexpr (sizeof(Key) == 4) {
+            const float wide = __shfl_sync(kAll, fabsf(first) + fabsf(second), from);
+            const float error = group_error(wide, L);
+            const bool taken = chosen >> lane & 1, other = lane < L.groups && !taken;
+            const uint32_t least = __reduce_min_sync(kAll, taken ? key_of(S::value(total) - error) : kAll);
+            sure = least > warp_max(other ? key_of(S::value(total) + error) : 0u);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
