@@ -580,13 +580,15 @@ __global__ void __launch_bounds__(256)
     read_token<V>(L, t, lane, z);
     const Shift f = shift_of<V>(L, z);
     int mine = -1;
-    float dw = 0.f, p = 0.f;
+    float dw = 0.f, p = 0.f, rest = 0.f;  // rest: 1 - p of a sigmoid, which p itself no longer tells
     if (lane < L.k) {
         const int e = experts[t * L.k + lane];
         if (e >= 0 && e < L.E) {
             mine = e;
             dw = dweights[t * L.k + lane];
-            p = score_of(L, f, load(L.logits, L.type, t * L.E + e));
+            const float x = load(L.logits, L.type, t * L.E + e);
+            p = score_of(L, f, x);
+            rest = score_of(L, f, -x);
         }
     }
     float g = L.scale * dw;
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(256)
         all += e == mine ? x : 0.f;
     }
     if (mine >= 0)
-        out[mine] = L.sigmoid ? all * p * (1.f - p) : p * (all - inner);
+        out[mine] = L.sigmoid ? all * p * rest : p * (all - inner);
 }
 
 // ---------------------------------------------------------------- joining
