@@ -565,8 +565,21 @@ __global__ void __launch_bounds__(kPlaceWarps * 32) place_kernel(const Args a)
     place_in<kPlaceWarps>(a, L.experts + from * L.k, shared, from * L.k, to * L.k);
 }
 
-// dz from dw, a warp a token: with g_j = ds of the chosen (through the renormalisation where
-// there is one), softmax: dz = s * (g - sum_j g_j s_j); sigmoid: dz = g * s * (1 - s).
+// The value of the lane whose weight (not negative) is largest; w: that weight.
+__device__ __forceinline__ float of_heaviest(float v, float weight, float &w)
+{
+    const uint32_t most = __reduce_max_sync(kAll, __float_as_uint(weight));
+    w = __uint_as_float(most);
+    return __shfl_sync(kAll, v, __ffs(__ballot_sync(kAll, __float_as_uint(weight) == most)) - 1);
+}
+
+// dz from dw, a warp a token: with g_j = ds of the chosen, softmax: dz = s * (g - sum_j g_j s_j);
+// sigmoid: dz = g * s * (1 - s). Of renormalised weights, with P = sum_j s_j, S = P + 1e-20,
+//     g_j = (sum_i s_i (dw_j - dw_i) + 1e-20 dw_j) / S^2,  sum_j g_j s_j = 1e-20 sum_j s_j dw_j / S^2
+// where the sum is P (dw_j - c) - sum_i s_i (dw_i - c), c the dw of the largest s_i. (c = 0, dw_j
+// less the weighted mean, leaves the mean's rounding where the dw are alike, one s_i outweighs
+// the others or k is 1: 1e-8 of dw / S where the gradient is 1e-20 of it.) `scale` comes last:
+// differences of the g are those of the dw.
 template <int V>
 __global__ void __launch_bounds__(256)
     route_backward_kernel(const RouteLaunch L, const int32_t *experts, const float *dweights,
@@ -591,18 +604,22 @@ __global__ void __launch_bounds__(256)
             rest = score_of(L, f, -x);
         }
     }
-    float g = L.scale * dw;
+    float g = dw, inner = 0.f;
     if (L.renormalise) {
-        const float total = warp_sum(p) + kNil, mean = warp_sum(dw * p) / total;
-        g = mine >= 0 ? L.scale * (dw - mean) / total : 0.f;
+        float w;
+        const float c = of_heaviest(dw, p, w), off = warp_sum(p * (dw - c));
+        const float total = warp_sum(p), part = 1.f / (total + kNil), nil = kNil * part;
+        g = mine >= 0 ? fmaf(fmaf(dw - c, total, -off), part, nil * dw) * part : 0.f;
+        inner = nil * (fmaf(c, total, off) * part);
+    } else if (!L.sigmoid) {
+        inner = warp_sum(g * p);
     }
-    const float inner = L.sigmoid ? 0.f : warp_sum(g * p);
     float *out = dlogits + t * L.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
         if (e < L.E)
-            out[e] = L.sigmoid ? 0.f : -inner * score_of(L, f, z[i]);
+            out[e] = L.sigmoid ? 0.f : -L.scale * (inner * score_of(L, f, z[i]));
     }
     __syncwarp();
     // The chosen experts' own terms; one that is named twice gets both.
@@ -613,7 +630,7 @@ __global__ void __launch_bounds__(256)
         all += e == mine ? x : 0.f;
     }
     if (mine >= 0)
-        out[mine] = L.sigmoid ? all * p * rest : p * (all - inner);
+        out[mine] = L.scale * (L.sigmoid ? all * p * rest : p * (all - inner));
 }
 
 // ---------------------------------------------------------------- joining

@@ -54,3 +54,60 @@ def test_sigmoids_near_1_against_differences():
     slope = (torch.sigmoid(-(x - h)) - torch.sigmoid(-(x + h))) / (2 * h)
     off = (got.double().gather(1, experts.long()) - slope).abs()
     assert (off <= (h * h / 6 + 2.0 ** -18) * slope + 2.0 ** -50 / h * torch.sigmoid(-x)).all()
+
+
+# ---- renormalised weights
+def renormalised(z, experts, dw, score, scale):
+    """(dlogits, what its terms' magnitudes add up to) in 64 bits, all but NIL sums of differences."""
+    at, dw = experts.long(), dw.double()
+    s = ref.scores(z, score)
+    p = s.gather(1, at)
+    total = p.sum(1, keepdim=True) + ref.NIL
+    between = dw[:, :, None] - dw[:, None, :]
+    g = ((p[:, None, :] * between).sum(2) + ref.NIL * dw) * scale / total ** 2
+    size = ((p[:, None, :] * between.abs()).sum(2) + ref.NIL * dw.abs()) * scale / total ** 2
+    if score == "sigmoid":
+        slope = p * torch.sigmoid(-z.double().gather(1, at))
+        zero = torch.zeros_like(s)
+        return zero.scatter(1, at, g * slope), zero.scatter(1, at, size * slope)
+    inner = scale * ref.NIL * (p * dw).sum(1, keepdim=True) / total ** 2
+    bound = scale * ref.NIL * (p * dw.abs()).sum(1, keepdim=True) / total ** 2
+    return (s * (torch.zeros_like(s).scatter(1, at, g) - inner),
+            s * (torch.zeros_like(s).scatter(1, at, size) + bound))
+
+
+# A score is within 2^-18 of itself: the exponent's rounding, 2^-24 of the at most 32 between two
+# logits (2^-19; a sigmoid's is 2^-21), exp's 2^-22, and of a softmax the sum of 2 additions in a
+# lane, 5 across lanes and a division, 8 * 2^-24. dlogits has it four times (its own, that of the
+# sum, twice that of S). The sum of differences may be made of differences from one dw, that of the
+# largest score: these are at most 2 k + 1 times the terms, with 8 roundings each; and 12 more.
+def tolerance(k):
+    return 2.0 ** -16 + (8 * (2 * k + 1) + 12) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 2, 8, 32])
+@pytest.mark.parametrize("spread", [1, 4])
+@pytest.mark.parametrize("alike", [False, True])
+def test_renormalised(alike, spread, k, score):
+    """`alike`: all of a token's dweights are equal, so that only NIL moves its weights."""
+    z = normal(400, 64, seed=k) * spread
+    dw = normal(400, 1, seed=3).expand(400, k).contiguous() if alike else normal(400, k, seed=3)
+    experts = rtm.gemm_route(z, k, score=score)[0]
+    got = rtm.gemm_route_backward(z, experts, dw, score=score, scale=1.5).double()
+    want, size = renormalised(z, experts, dw, score, 1.5)
+    assert ((got - want).abs() <= tolerance(k) * size + 1e-37).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_renormalised_scores_as_small_as_what_keeps_them_from_0(score):
+    """Chosen scores of 1e-16 to 1e-24 (one expert, that is not chosen, has the softmax): S is
+    1e-20 and they together, and the gradient is not small."""
+    z = uniform(-55, -37, 200, 16, seed=4)
+    z[:, 0] = 0.0
+    experts = torch.tensor([[3, 9, 5]], dtype=torch.int32, device=DEV).expand(200, 3).contiguous()
+    dw = normal(200, 3, seed=6)
+    got = rtm.gemm_route_backward(z, experts, dw, score=score).double()
+    want, size = renormalised(z, experts, dw, score, 1.0)
+    assert ((got - want).abs() <= 2 * tolerance(3) * size + 1e-37).all()  # the exponents are twice as large
+    assert float(want.abs().max()) > 1e-3
