@@ -574,13 +574,16 @@ __device__ __forceinline__ float of_heaviest(float v, float weight, float &w)
 }
 
 // dz from dw, a warp a token: with g_j = ds of the chosen, softmax: dz = s * (g - sum_j g_j s_j);
-// sigmoid: dz = g * s * (1 - s). Of renormalised weights, with P = sum_j s_j, S = P + 1e-20,
+// sigmoid: dz = g * s * (1 - s). A softmax's difference is sum_e s_e (g - g_e) over all experts,
+// g_e 0 of those that are not chosen. Without renormalisation (PLAIN) it is taken as g - c less
+// sum_e s_e (g_e - c), c the g of the largest of the chosen scores and of the others' sum: where
+// one score is nearly 1 the plain difference is rounding. Of renormalised weights, with P = sum_j s_j, S = P + 1e-20,
 //     g_j = (sum_i s_i (dw_j - dw_i) + 1e-20 dw_j) / S^2,  sum_j g_j s_j = 1e-20 sum_j s_j dw_j / S^2
 // where the sum is P (dw_j - c) - sum_i s_i (dw_i - c), c the dw of the largest s_i. (c = 0, dw_j
 // less the weighted mean, leaves the mean's rounding where the dw are alike, one s_i outweighs
 // the others or k is 1: 1e-8 of dw / S where the gradient is 1e-20 of it.) `scale` comes last:
 // differences of the g are those of the dw.
-template <int V>
+template <int V, bool PLAIN>
 __global__ void __launch_bounds__(256)
     route_backward_kernel(const RouteLaunch L, const int32_t *experts, const float *dweights,
                           float *dlogits)
@@ -611,26 +614,53 @@ __global__ void __launch_bounds__(256)
         const float total = warp_sum(p), part = 1.f / (total + kNil), nil = kNil * part;
         g = mine >= 0 ? fmaf(fmaf(dw - c, total, -off), part, nil * dw) * part : 0.f;
         inner = nil * (fmaf(c, total, off) * part);
-    } else if (!L.sigmoid) {
-        inner = warp_sum(g * p);
+    }
+    // The chosen experts' own terms; one that is named twice gets both.
+    float all = 0.f;
+    bool first = mine >= 0;  // of the slots that name this expert
+    auto add_up = [&]() {
+        all = 0.f;
+        for (int j = 0; j < L.k; ++j) {
+            const int e = __shfl_sync(kAll, mine, j);
+            const float x = __shfl_sync(kAll, g, j);
+            all += e == mine ? x : 0.f;
+            first = first && (e != mine || j >= lane);
+        }
+    };
+    float own = 0.f;
+    if constexpr (PLAIN) {
+        float others = 0.f, w;  // the scores of the experts that are not chosen
+        int named = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = score_of(L, f, z[i]);  // 0 behind the last expert
+            const uint32_t taken = __reduce_or_sync(kAll, mine >> 5 == i ? 1u << (mine & 31) : 0u);
+            others += taken >> lane & 1 ? 0.f : z[i];
+            named += __popc(taken);
+        }
+        others = warp_sum(others);
+        all = g;
+        if (named != __popc(__ballot_sync(kAll, mine >= 0)))
+            add_up();
+        const float heaviest = of_heaviest(all, first ? p : 0.f, w), c = others > w ? 0.f : heaviest;
+        const float off = fmaf(-c, others, warp_sum(first ? p * (all - c) : 0.f));
+        own = all - c - off;
+        inner = c + off;
     }
     float *out = dlogits + t * L.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * 32 + lane;
         if (e < L.E)
-            out[e] = L.sigmoid ? 0.f : -L.scale * (inner * score_of(L, f, z[i]));
+            out[e] = L.sigmoid ? 0.f : -L.scale * (inner * (PLAIN ? z[i] : score_of(L, f, z[i])));
     }
     __syncwarp();
-    // The chosen experts' own terms; one that is named twice gets both.
-    float all = 0.f;
-    for (int j = 0; j < L.k; ++j) {
-        const int e = __shfl_sync(kAll, mine, j);
-        const float x = __shfl_sync(kAll, g, j);
-        all += e == mine ? x : 0.f;
+    if constexpr (!PLAIN) {
+        add_up();
+        own = L.sigmoid ? all * rest : all - inner;
     }
     if (mine >= 0)
-        out[mine] = L.scale * (L.sigmoid ? all * p * rest : p * (all - inner));
+        out[mine] = L.scale * (p * own);
 }
 
 // ---------------------------------------------------------------- joining
@@ -785,7 +815,10 @@ static cudaError_t launch_backward(const RouteLaunch &L, const int32_t *experts,
     const int64_t blocks = (L.T + 7) / 8;
     if (blocks > 0x7fffffff)
         return cudaErrorInvalidValue;
-    route_backward_kernel<V><<<(unsigned)blocks, 256, 0, stream>>>(L, experts, dweights, dlogits);
+    if (!L.sigmoid && !L.renormalise)
+        route_backward_kernel<V, true><<<(unsigned)blocks, 256, 0, stream>>>(L, experts, dweights, dlogits);
+    else
+        route_backward_kernel<V, false><<<(unsigned)blocks, 256, 0, stream>>>(L, experts, dweights, dlogits);
     return cudaGetLastError();
 }
 

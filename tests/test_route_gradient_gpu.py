@@ -111,3 +111,59 @@ def test_renormalised_scores_as_small_as_what_keeps_them_from_0(score):
     want, size = renormalised(z, experts, dw, score, 1.0)
     assert ((got - want).abs() <= 2 * tolerance(3) * size + 1e-37).all()  # the exponents are twice as large
     assert float(want.abs().max()) > 1e-3
+
+
+# ---- softmax without renormalisation, where one score is nearly 1
+def plain_softmax(z, experts, dw, scale):
+    """(dlogits, what its terms' magnitudes add up to) in 64 bits, as sums of differences."""
+    at = experts.long()
+    s = ref.scores(z, "softmax")
+    g = torch.zeros_like(s).scatter_add(1, at, scale * dw.double())
+    between = g.gather(1, at)[:, :, None] - g[:, None, :]  # an expert's g less each other's
+    p = s.gather(1, at)
+    inner = (s * g).sum(1, keepdim=True)
+    bound = (s * torch.zeros_like(s).scatter_add(1, at, scale * dw.double().abs())).sum(1, keepdim=True)
+    return ((-s * inner).scatter(1, at, p * (s[:, None, :] * between).sum(2)),
+            (s * bound).scatter(1, at, p * (s[:, None, :] * between.abs()).sum(2)))
+
+
+# Two scores have 2 * 2^-18, as above; differences from one g are at most 2 k + 3 times the terms
+# (the experts that are not chosen count as one), with 8 roundings each: below tolerance(k).
+@pytest.mark.parametrize("k", [1, 2, 8, 32])
+@pytest.mark.parametrize("lead", [0, 8, 15])
+def test_a_softmax_score_near_1(lead, k):
+    z, dw = normal(300, 100, seed=k), normal(300, k, seed=lead)
+    z[torch.arange(300, device=DEV), torch.arange(300, device=DEV) % 100] += lead
+    experts = rtm.gemm_route(z, k)[0]
+    got = rtm.gemm_route_backward(z, experts, dw, renormalise=False, scale=1.5).double()
+    want, size = plain_softmax(z, experts, dw, 1.5)
+    off = (got - want).abs() - tolerance(k) * size
+    assert (off <= 1e-37).all()
+
+
+def test_named_twice_and_outside_beside_a_score_near_1():
+    z, dw = normal(100, 8, seed=1), normal(100, 4, seed=2)
+    z[:, 1] += 14
+    experts = torch.tensor([[1, 1, 2, 8]], dtype=torch.int32, device=DEV).expand(100, 4).contiguous()
+    got = rtm.gemm_route_backward(z, experts, dw, renormalise=False).double()
+    want, size = plain_softmax(z, experts[:, :3], dw[:, :3], 1.0)
+    assert ((got - want).abs() <= tolerance(3) * size + 1e-37).all()
+
+
+def test_a_softmax_score_near_1_against_differences():
+    """One expert chosen: its weight's slope by its own logit is that of the others' scores, which
+    keep their digits. A step of 2^-6: the error is step^2 / 6 and 2^-50 of the scores."""
+    z = normal(60, 16, seed=8)
+    z[:, 4] += 12
+    experts = rtm.gemm_route(z, 1)[0]
+    assert (experts == 4).all()
+    got = rtm.gemm_route_backward(z, experts, torch.ones(60, 1, device=DEV), renormalise=False)
+    h, step = 2.0 ** -6, torch.zeros(16, device=DEV, dtype=torch.float64)
+    step[4] = h
+    others = [None, None]
+    for i, x in enumerate((z.double() - step, z.double() + step)):
+        s = torch.softmax(x, 1)
+        others[i] = torch.cat((s[:, :4], s[:, 5:]), 1).sum(1)
+    slope = (others[0] - others[1]) / (2 * h)
+    off = (got[:, 4].double() - slope).abs()
+    assert (off <= (h * h / 6 + 2.0 ** -16 + 2.0 ** -50 / h) * slope).all()
