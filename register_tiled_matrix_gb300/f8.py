@@ -132,7 +132,7 @@ def gemm_f8_quantize(X: torch.Tensor, kind: str = "rows", gather: Optional[torch
     name = _name(X.dtype)
     if kind not in ("rows", "columns", "both"):
         raise ValueError(f"kind must be rows, columns or both, got {kind!r}")
-    if fan != 1 or fan is True:
+    if type(fan) is not int or fan != 1:
         _whole("fan", fan, 1, 1 << 20)
     M = source
     if gather is not None:

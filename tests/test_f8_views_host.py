@@ -71,3 +71,10 @@ def test_views_that_hold_their_rows_are_taken():
         got = f8._codes("codes", t, t.dim(), 0)
         # a single row's pitch is not told by its stride
         assert got >= t.shape[-1] and got % 16 == 0 and (t.numel() == 0 or t.shape[-2] == 1 or got == ld)
+
+
+@pytest.mark.parametrize("fan", [1.0, True, 0, -1, (1 << 20) + 1, "1", None])
+def test_a_fan_that_is_no_whole_number_is_refused(fan):
+    x, rows = (t.as_subclass(OnDevice) for t in (torch.ones(4, 16), torch.zeros(4, dtype=torch.int32)))
+    with pytest.raises(ValueError, match="fan must be a whole number"):
+        rtm.gemm_f8_quantize(x, gather=rows, fan=fan)
