@@ -317,6 +317,11 @@ def gemm_route_rows(T: int, E: int, k: int, align: int = 128) -> int:
     return n
 
 
+def _route_rows(T: int, E: int, k: int, align: int) -> int:
+    """gemm_route_rows of sizes in order, without a call into the library."""
+    return T * k + min(E, T * k) * (align - 1)
+
+
 def _score(score) -> int:
     if score not in _SCORES:
         raise ValueError(f"score must be one of {_SCORES}, got {score!r}")
@@ -344,7 +349,7 @@ def gemm_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None
     sigmoid = _score(score)
     if bias is not None:
         _need("bias", bias, torch.float32, (E,), logits.device)
-    R = T * k + min(E, T * k) * (align - 1)  # gemm_route_rows
+    R = _route_rows(T, E, k, align)
     need = int((_binding._lib or load_library()).gemm_route_workspace_bytes(T, E))
     experts = _empty(logits, (T, k), torch.int32, stream)
     slots = _empty(logits, (T, k), torch.int32, stream)

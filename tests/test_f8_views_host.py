@@ -78,3 +78,14 @@ def test_a_fan_that_is_no_whole_number_is_refused(fan):
     x, rows = (t.as_subclass(OnDevice) for t in (torch.ones(4, 16), torch.zeros(4, dtype=torch.int32)))
     with pytest.raises(ValueError, match="fan must be a whole number"):
         rtm.gemm_f8_quantize(x, gather=rows, fan=fan)
+
+
+def test_rows_of_the_order_are_as_many_as_the_library_writes():
+    """gemm_route makes `rows` by a formula of its own, and the C entry cannot see its length."""
+    rtm.build()
+    for T in (0, 1, 2, 31, 33, 1000, 70000, (2 ** 31 - 1 - 256 - 1024 * 1024) // 32):
+        for E in (1, 2, 7, 64, 1000, 1024):
+            for k in (1, 2, 8, 32):
+                for align in (1, 2, 127, 128, 1024):
+                    if k <= E:
+                        assert f8._route_rows(T, E, k, align) == rtm.gemm_route_rows(T, E, k, align)
