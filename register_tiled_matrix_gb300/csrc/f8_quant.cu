@@ -88,17 +88,6 @@ __device__ __forceinline__ float max_magnitude(float a, float b)
     return d;
 }
 
-template <int TYPE>
-__device__ __forceinline__ float load1(const void *X, int64_t i)
-{
-    if constexpr (TYPE == kF32)
-        return static_cast<const float *>(X)[i];
-    else if constexpr (TYPE == kBf16)
-        return __bfloat162float(static_cast<const __nv_bfloat16 *>(X)[i]);
-    else
-        return __half2float(static_cast<const __half *>(X)[i]);
-}
-
 // Eight values as they lie in memory.
 template <int TYPE>
 struct Raw {
