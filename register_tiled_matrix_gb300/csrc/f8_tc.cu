@@ -110,8 +110,7 @@ __device__ __forceinline__ void arrive_set(uint32_t bar)
 
 struct Params {
     int rows, cols;     // of C; weight: of one matrix C
-    int depth;          // forward, input; weight without offsets
-    int total;          // weight: rows of X and dY
+    int depth;          // weight: rows of X and dY
     int groups;         // experts
     const int32_t *offsets;
     const float *a_scales, *b_scales;
@@ -253,7 +252,7 @@ template <int MODE, int NT, bool SWAP>
 __device__ __forceinline__ void count_tiles(const Params &p, int32_t *start, int32_t *tiles, int lane)
 {
     using Cf = Cfg<NT, SWAP>;
-    const int most = MODE == kF8Weight ? p.total : p.rows;
+    const int most = MODE == kF8Weight ? p.depth : p.rows;
     const int tc = (p.cols + Cf::COLS - 1) / Cf::COLS;
     const int each = (p.rows + Cf::ROWS - 1) / Cf::ROWS * tc;  // weight: the same for every group
     int low = 0, sum = 0;
@@ -969,7 +968,6 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
     p.rows = (int)L.rows;
     p.cols = (int)L.cols;
     p.depth = (int)L.depth;
-    p.total = (int)L.depth;
     p.groups = L.experts;
     p.offsets = L.offsets;
     p.a_scales = L.a_scales;
