@@ -522,7 +522,10 @@ GEMM_API int gemm_q8tbf16f32_selftest_timeout(int64_t M, int64_t N, int64_t K,
  *                      a weight gradient, which sums over rows)
  *     GEMM_F8_TILES    K x N, scales ceil(K/128) x ceil(N/128): 128 x 128 tiles (weights); E
  *                      matrices one after another, each with tiles of its own
- * The products take any scales.
+ * The products take any scales, as long as fp32 holds the product of two that meet: the two are
+ * multiplied first (for few rows and for a weight gradient the sum takes one after the other), so
+ * where that is past 2^128 results are infinite or NaN, and where it is below 2^-149 zeros, even
+ * if the scaled sum itself would be neither.
  *
  * gemm_f8_pitch — bytes between the rows that the conversions below write: K rounded up to 16
  * (the bytes past K are written as 0), or GEMM_ERR_INVALID_ARG.
@@ -540,8 +543,9 @@ GEMM_API int gemm_q8tbf16f32_selftest_timeout(int64_t M, int64_t N, int64_t K,
  *
  * gemm_*_f8_quantize_tiles — the same for E matrices W of K x N, by tiles.
  *
- * gemm_*_f8_dequantize — E matrices M x K of the given kind back to values, code * scale rounded
- * once; the next matrix starts M * ld bytes on, its scales behind the last matrix's.
+ * gemm_*_f8_dequantize — E matrices M x K of the given kind back to values: code * scale in fp32
+ * (exact with the conversions' scales), rounded to the 16-bit type if it is one; the next matrix
+ * starts M * ld bytes on, its scales behind the last matrix's.
  */
 typedef enum gemm_f8_kind {
     GEMM_F8_ROWS = 0,
@@ -610,7 +614,9 @@ GEMM_API int gemm_f8w8f32_selftest_timeout(int64_t M, int64_t N, int64_t K, cons
  * Routing of T tokens to k of E experts (1 <= k <= 32, k <= E <= 1024) by their logits (T x E).
  *     s = softmax(logits) or, sigmoid != 0, 1 / (1 + exp(-logits)), of each token
  *     experts[t][j]: the k largest of s + bias (bias fp32, E, null for none), best first, ties
- *     to the lowest index, decided as in real numbers (fp32 where that is certain, else fp64)
+ *     to the lowest index, decided as fp64 has them (fp32 where that is certain; without bias
+ *     and groups by the logits themselves). What fp64 cannot tell is a tie: without bias, sigmoids
+ *     of 37 and more are 1, and a softmax score 745 below the largest logit is 0
  *     weights[t][j] = scale * s_j, or, renormalise != 0, scale * s_j / (sum_j s_j + 1e-20);
  *     the bias moves the choice and not the weights
  * With groups > 1 (at most 32, dividing E) the experts are in groups of E / groups neighbours;
