@@ -615,7 +615,7 @@ GEMM_API int gemm_f8w8f32_selftest_timeout(int64_t M, int64_t N, int64_t K, cons
  *     s = softmax(logits) or, sigmoid != 0, 1 / (1 + exp(-logits)), of each token
  *     experts[t][j]: the k largest of s + bias (bias fp32, E, null for none), best first, ties
  *     to the lowest index, decided as fp64 has them (fp32 where that is certain; without bias
- *     and groups by the logits themselves). What fp64 cannot tell is a tie: without bias, sigmoids
+ *     and groups by the logits themselves). What fp64 cannot tell is a tie: with groups, sigmoids
  *     of 37 and more are 1, and a softmax score 745 below the largest logit is 0
  *     weights[t][j] = scale * s_j, or, renormalise != 0, scale * s_j / (sum_j s_j + 1e-20);
  *     the bias moves the choice and not the weights

@@ -979,7 +979,9 @@ static cudaError_t launch_cfg(const F8Launch &L, const DeviceContext &d, bool mu
     p.c_boxes = boxes ? 1 : 0;
     p.c_vec = L.cols % 2 == 0 && (reinterpret_cast<uintptr_t>(L.C) & 7) == 0;
     // Few tiles: split the depth while every CTA keeps at least two blocks (a pair four) and
-    // all clusters (of at most 8 CTAs) are resident at once.
+    // all clusters (of at most 8 CTAs) are resident at once. (With one block a CTA 1 x 1024 x 1024
+    // takes 13.4 us instead of 11.4, with at least eight 128 x 1024 x 2048 17.6 instead of 15.5;
+    // four instead of two are the same but for 1 x 512 x 512, 9.4 against 11.4.)
     constexpr int CTAS = Cf::CTAS, LEAST = Cf::PAIR ? 4 : 2;
     const int64_t blocks = f8_blocks(L.depth) / (MODE == kF8Weight && L.offsets ? L.experts : 1);
     int splits = 1;
@@ -1018,9 +1020,11 @@ template <int MODE>
 static cudaError_t launch_mode(const F8Launch &L, const DeviceContext &d, bool mute, cudaStream_t stream)
 {
     if constexpr (MODE != kF8Weight) {
-        // Up to 64 rows (of an expert, on average): W's columns on the lanes. With more, 128 x 128
-        // tiles read W as often and give every lane a row (65 x 4096 x 4096 18.6 us, 128 swapped
-        // columns 25.7).
+        // Up to 64 rows (of an expert, on average; the ends of the parts count as rows): W's columns
+        // on the lanes, as few of the accumulator's as hold the rows (16 x 8192 x 8192 25.8 us,
+        // with 64 columns 27.8; 33 rows in 16 columns 37.0, in 64 28.8). With more, 128 x 128 tiles
+        // read W as often and give every lane a row (65 x 4096 x 4096 18.6 us, 128 swapped columns
+        // 25.7; 129 x 8192 x 8192 31.9, in 64 swapped columns 42.1).
         const int64_t rows = L.offsets ? (L.rows + L.experts - 1) / L.experts : L.rows;
         if (rows <= 16)
             return launch_cfg<MODE, 16, true>(L, d, mute, stream);
@@ -1031,6 +1035,10 @@ static cudaError_t launch_mode(const F8Launch &L, const DeviceContext &d, bool m
         if (rows <= 128)
             return launch_cfg<MODE, 128, false>(L, d, mute, stream);
     }
+    // Pairs from half as many tiles as there are pairs on: the tiles of 128 are then more than the
+    // SMs, two rounds of them. Depth 4096, us in pairs and in tiles of 128: 40 tiles of pairs 25.8
+    // and 33.9 (the gradient of W 29.9, 38.0), 72 tiles 27.8 and 33.9; below, where tiles of 128
+    // are one round, 36 tiles 30.8 and 21.7 (31.9, 23.7), 16 tiles 28.8 and 20.6.
     if (most_tiles(L, 256, 256) * 4 >= d.sms)
         return launch_cfg<MODE, 256, false>(L, d, mute, stream);
     return launch_cfg<MODE, 128, false>(L, d, mute, stream);

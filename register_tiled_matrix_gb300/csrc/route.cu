@@ -29,10 +29,13 @@ namespace rtm {
 namespace route {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kOneBlock = 32;    // tokens
+// Tokens that one block chooses for and orders: 16 of 256 grouped experts 14.5 us, in two launches
+// 16.5; 32 19.6 and 17.5 in a graph, where a launch costs no host time.
+constexpr int kOneBlock = 32;
 constexpr int kMaxRuns = 152;    // blocks of the two-launch form: one an SM
 // Warps of a block: as many as its registers and shared memory allow; eight for at most as many
-// tokens (one token of 256 experts: 13.4 us with 32, where most only take part in the order).
+// tokens (one token of 256 experts: 11.5 us, 13.4 with 32, where most only take part in the order;
+// 12 tokens 13.5 with 32, 15.6 with eight).
 __host__ __device__ constexpr int warps_of(int V, bool few) { return few ? 8 : V <= 8 ? 32 : 16; }
 constexpr float kNil = 1e-20f;
 constexpr uint32_t kNegInfKey = 0x007fffffu;
@@ -783,6 +786,7 @@ __global__ void __launch_bounds__(128)
     }
 }
 
+// Blocks, each a run of tokens: two tokens a block until there is a block on every SM.
 static int runs_of(int64_t T) { return T <= kOneBlock ? 1 : (int)(T < kMaxRuns * 2 ? (T + 1) / 2 : kMaxRuns); }
 
 constexpr size_t place_bytes(int warps, int E) { return (size_t)place_words(warps, E) * 4; }
@@ -894,7 +898,8 @@ static cudaError_t launch_join_backward(int64_t T, int64_t N, int k, int64_t R,
                                         const void *dY, const float *C, const int32_t *slots,
                                         float *dweights, cudaStream_t stream)
 {
-    // A block a slot while that leaves SMs idle.
+    // A block a slot while that leaves SMs idle: 1024 slots of 4096 11.4 us, a warp each 17.6; 4096
+    // of 512 11.4 and 10.4, 131072 of 512 96 and 64.
     const int64_t count = T * k;
     const bool few = count < 152 * 16;
     const int64_t blocks = few ? count : (count + 3) / 4;
