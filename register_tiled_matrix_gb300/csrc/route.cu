@@ -189,7 +189,7 @@ __device__ __forceinline__ bool select(typename S::Key (&v)[V], const RouteLaunc
         }
         // Certain where every group taken leads every other one, each with an error of its own.
         // (Neighbours in the order do not tell: a sum far from another can have the larger one.)
-        if constexpr (sizeof(Key) == 4) {
+        if (sizeof(Key) == 4 && L.top_groups < L.groups) {
             const float wide = __shfl_sync(kAll, fabsf(first) + fabsf(second), from);
             const float error = group_error(wide, L);
             const bool taken = chosen >> lane & 1, other = lane < L.groups && !taken;
