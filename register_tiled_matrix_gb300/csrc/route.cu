@@ -580,7 +580,8 @@ __device__ __forceinline__ float of_heaviest(float v, float weight, float &w)
 // sigmoid: dz = g * s * (1 - s). A softmax's difference is sum_e s_e (g - g_e) over all experts,
 // g_e 0 of those that are not chosen. Without renormalisation (PLAIN) it is taken as g - c less
 // sum_e s_e (g_e - c), c the g of the largest of the chosen scores and of the others' sum: where
-// one score is nearly 1 the plain difference is rounding. Of renormalised weights, with P = sum_j s_j, S = P + 1e-20,
+// one score is nearly 1 the plain difference is rounding.
+// Of renormalised weights, with P = sum_j s_j, S = P + 1e-20,
 //     g_j = (sum_i s_i (dw_j - dw_i) + 1e-20 dw_j) / S^2,  sum_j g_j s_j = 1e-20 sum_j s_j dw_j / S^2
 // where the sum is P (dw_j - c) - sum_i s_i (dw_i - c), c the dw of the largest s_i. (c = 0, dw_j
 // less the weighted mean, leaves the mean's rounding where the dw are alike, one s_i outweighs
